@@ -1,4 +1,5 @@
-"""MI355X (gfx950) FP32 SGEMM: C = alpha*A*B + beta*C on row-major matrices.
+"""MI355X (gfx950) FP32 SGEMM: C = alpha*A*B + beta*C on row-major matrices, and
+products whose B is picked row by row (experts, low-rank adapters).
 
 A thin Python binding of the C ABI in ``include/sgemm.h``: every function has
 the name and argument order of its C counterpart and only marshals arguments.
@@ -33,11 +34,18 @@ __all__ = [
     "sgemm_select_variant", "sgemm_select_variant_for", "sgemm_operands_load16", "sgemm_variant_builds",
     "SGEMM_BUILD_BUFFER_128", "SGEMM_BUILD_BUFFER_32", "SGEMM_BUILD_CHECKED", "SGEMM_BUILD_BUFFER_128_AB",
     "SGEMM_BUILD_SPLITK", "SGEMM_BUILD_STREAMK", "sgemm_status_string", "variants", "sgemm_device_fp32_peak",
+    "SGEMM_SCORE_SOFTMAX", "SGEMM_SCORE_SIGMOID", "sgemm_route", "sgemm_route_grad", "sgemm_group_rows",
+    "sgemm_group_rows_workspace_size", "sgemm_grouped", "sgemm_grouped_tn", "sgemm_combine",
+    "sgemm_combine_grad", "sgemm_adapters", "sgemm_adapters_workspace_size", "sgemm_adapters_grad",
+    "sgemm_adapters_grad_workspace_size",
 ]
 
 SGEMM_PATH_AUTO = 0
 SGEMM_PATH_VALU = 1
 SGEMM_PATH_MFMA = 2
+
+SGEMM_SCORE_SOFTMAX = 0
+SGEMM_SCORE_SIGMOID = 1
 
 SGEMM_ACCESS_AUTO = 0
 SGEMM_ACCESS_BUFFER_128 = 1
@@ -142,6 +150,26 @@ def load_library():
         lib.sgemm_status_string.restype = ctypes.c_char_p
         lib.sgemm_device_fp32_peak.argtypes = [i, vp, vp, vp]
         lib.sgemm_device_fp32_peak.restype = i
+        ll, sz = ctypes.c_longlong, ctypes.c_size_t
+        for name, args in {
+            "sgemm_route": [i, i, i, i, vp, i, vp, i, i, i, i, f, vp, vp, vp],
+            "sgemm_route_grad": [i, i, i, i, vp, i, i, f, vp, vp, vp, i, vp],
+            "sgemm_group_rows": [i, i, vp, vp, vp, vp, sz, vp],
+            "sgemm_grouped": [i, i, i, i, f, vp, i, i, vp, i, ll, i, f, vp, i, i, vp, vp, vp],
+            "sgemm_grouped_tn": [i, i, i, i, f, vp, i, i, vp, i, i, f, vp, i, ll, vp, vp, vp],
+            "sgemm_combine": [i, i, i, i, vp, vp, vp, i, f, vp, i, vp],
+            "sgemm_combine_grad": [i, i, i, i, vp, vp, vp, i, vp, i, vp, i, vp, vp],
+            "sgemm_adapters": [i, i, i, f, vp, i, vp, i, f, vp, i, i, i, vp, vp, vp, vp, i, ll, vp, i, ll, vp,
+                               sz, vp],
+            "sgemm_adapters_grad": [i, i, i, f, vp, i, vp, i, vp, i, i, i, vp, vp, vp, vp, i, ll, vp, i, ll, f,
+                                    vp, i, vp, i, ll, vp, i, ll, vp, sz, vp],
+        }.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = i
+        for name, n in (("sgemm_group_rows_workspace_size", 2), ("sgemm_adapters_workspace_size", 5),
+                        ("sgemm_adapters_grad_workspace_size", 5)):
+            getattr(lib, name).argtypes = [i] * n
+            getattr(lib, name).restype = sz
         _lib = lib
         return lib
 
@@ -418,3 +446,177 @@ def variants():
         _, bm, bn = sgemm_variant_tile(v)
         out.append((v, sgemm_variant_name(v), sgemm_variant_path(v), bm, bn))
     return out
+
+
+# ---- products whose B is picked row by row ----------------------------------
+# These calls take index tensors beside the matrices, so a tensor's type, place
+# and extent are looked at before its address goes to a kernel: float32 (ids and
+# offsets int32) on the current device, long enough for the sizes given.  An
+# ``int`` address is passed on as it is.
+class _Tensors:
+    """The address of each argument of one call."""
+    __slots__ = ("where", "device")
+
+    def __init__(self, where):
+        import torch
+        self.where = where
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+    def _address(self, x, what, kind, need, inner=None):
+        if x is None or isinstance(x, int):
+            return x
+        p = _ptr(x)
+        if str(x.dtype) != kind:
+            raise TypeError(f"{self.where}: {what} has type {x.dtype}, not {kind}")
+        if x.get_device() != self.device:
+            raise ValueError(f"{self.where}: {what} is on {x.device}, not on the current device cuda:{self.device}")
+        if not x.is_contiguous():
+            if inner is None or (x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1):
+                raise ValueError(f"{self.where}: {what} must be laid out "
+                                 + ("without gaps" if inner is None else "with its last dimension contiguous"))
+            have = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+        else:
+            have = x.numel()
+        if have < need:
+            raise ValueError(f"{self.where}: {what} holds {have} elements, {need} are needed")
+        return p
+
+    def matrix(self, x, what, rows, cols, ld, groups=1, stride=0):
+        """groups matrices of rows x cols, rows ld apart and matrices stride apart."""
+        some = groups > 0 and rows > 0 and cols > 0
+        need = (groups - 1) * stride + (rows - 1) * ld + cols if some else 0
+        return self._address(x, what, "torch.float32", need, cols)
+
+    def floats(self, x, what, n):
+        return self._address(x, what, "torch.float32", n)
+
+    def ints(self, x, what, n):
+        return self._address(x, what, "torch.int32", n)
+
+    def space(self, x, nbytes):
+        if x is None or isinstance(x, int):
+            return x, int(nbytes or 0)
+        if not x.is_contiguous():
+            raise ValueError(f"{self.where}: workspace must be laid out without gaps")
+        have = x.numel() * x.element_size()
+        if nbytes is not None and nbytes > have:
+            raise ValueError(f"{self.where}: workspace holds {have} bytes, not {nbytes}")
+        if x.is_cuda and x.get_device() != self.device:
+            raise ValueError(f"{self.where}: workspace is on {x.device}, not on the current device cuda:{self.device}")
+        return _ptr(x), int(have if nbytes is None else nbytes)
+
+
+def sgemm_route(T, E, k, scoring, logits, ldl, bias, groups, top_groups, group_best, renorm, scale, ids,
+                weights, stream=None, check=True):
+    """The k experts of each token (``ids``, T x k int32) and their ``weights`` (T x k)."""
+    t = _Tensors("sgemm_route")
+    return _ret(load_library().sgemm_route(
+        T, E, k, scoring, t.matrix(logits, "logits", T, E, ldl), ldl, t.floats(bias, "bias", E), groups, top_groups,
+        group_best, 1 if renorm else 0, scale, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
+        _stream(stream)), "sgemm_route", check)
+
+
+def sgemm_route_grad(T, E, k, scoring, logits, ldl, renorm, scale, ids, dweights, dlogits, lddl, stream=None,
+                     check=True):
+    """``dlogits`` (T x E) from the gradient of sgemm_route()'s weights."""
+    t = _Tensors("sgemm_route_grad")
+    return _ret(load_library().sgemm_route_grad(
+        T, E, k, scoring, t.matrix(logits, "logits", T, E, ldl), ldl, 1 if renorm else 0, scale,
+        t.ints(ids, "ids", T * k), t.floats(dweights, "dweights", T * k), t.matrix(dlogits, "dlogits", T, E, lddl),
+        lddl, _stream(stream)), "sgemm_route_grad", check)
+
+
+def sgemm_group_rows_workspace_size(R, G) -> int:
+    return int(load_library().sgemm_group_rows_workspace_size(int(R), int(G)))
+
+
+def sgemm_group_rows(R, G, ids, offsets, rows, workspace=None, workspace_bytes=None, stream=None, check=True):
+    """The R slots sorted by group: ``offsets`` (G + 1 int32) and ``rows`` (R int32)."""
+    t = _Tensors("sgemm_group_rows")
+    ws, nbytes = t.space(workspace, workspace_bytes)
+    return _ret(load_library().sgemm_group_rows(
+        R, G, t.ints(ids, "ids", R), t.ints(offsets, "offsets", G + 1), t.ints(rows, "rows", R), ws, nbytes,
+        _stream(stream)), "sgemm_group_rows", check)
+
+
+def _rows(R, div):
+    return -(-R // div) if div > 1 else R
+
+
+def sgemm_grouped(G, R, N, K, alpha, A, lda, a_div, B, ldb, stride_b, trans_b, beta, C, ldc, c_scatter, offsets,
+                  rows, stream=None, check=True):
+    """Every placed slot's row of ``A`` times its group's ``B`` (transposed with ``trans_b``)."""
+    t = _Tensors("sgemm_grouped")
+    b = (N, K) if trans_b else (K, N)
+    return _ret(load_library().sgemm_grouped(
+        G, R, N, K, alpha, t.matrix(A, "A", _rows(R, a_div), K, lda), lda, a_div,
+        t.matrix(B, "B", *b, ldb, G, stride_b), ldb, stride_b, 1 if trans_b else 0, beta,
+        t.matrix(C, "C", R, N, ldc), ldc, 1 if c_scatter else 0, t.ints(offsets, "offsets", G + 1),
+        t.ints(rows, "rows", R), _stream(stream)), "sgemm_grouped", check)
+
+
+def sgemm_grouped_tn(G, R, M, N, alpha, A, lda, a_div, B, ldb, b_div, beta, C, ldc, stride_c, offsets, rows,
+                     stream=None, check=True):
+    """Each group's sum over its slots of the outer products of their rows of ``A`` and ``B``."""
+    t = _Tensors("sgemm_grouped_tn")
+    return _ret(load_library().sgemm_grouped_tn(
+        G, R, M, N, alpha, t.matrix(A, "A", _rows(R, a_div), M, lda), lda, a_div,
+        t.matrix(B, "B", _rows(R, b_div), N, ldb), ldb, b_div, beta, t.matrix(C, "C", M, N, ldc, G, stride_c), ldc,
+        stride_c, t.ints(offsets, "offsets", G + 1), t.ints(rows, "rows", R), _stream(stream)),
+        "sgemm_grouped_tn", check)
+
+
+def sgemm_combine(T, k, N, E, ids, weights, Y, ldy, beta, out, ldo, stream=None, check=True):
+    """``out[t]`` = the weighted sum of token t's k rows of ``Y``, plus ``beta * out[t]``."""
+    t = _Tensors("sgemm_combine")
+    return _ret(load_library().sgemm_combine(
+        T, k, N, E, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
+        t.matrix(Y, "Y", T * k, N, ldy), ldy, beta, t.matrix(out, "out", T, N, ldo), ldo, _stream(stream)),
+        "sgemm_combine", check)
+
+
+def sgemm_combine_grad(T, k, N, E, ids, weights, dout, ldd, Y, ldy, dY, lddy, dweights, stream=None, check=True):
+    """``dY`` (T * k x N) and ``dweights`` (T x k) from ``dout``; either may be None."""
+    t = _Tensors("sgemm_combine_grad")
+    return _ret(load_library().sgemm_combine_grad(
+        T, k, N, E, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
+        t.matrix(dout, "dout", T, N, ldd), ldd, t.matrix(Y, "Y", T * k, N, ldy), ldy,
+        t.matrix(dY, "dY", T * k, N, lddy), lddy, t.floats(dweights, "dweights", T * k), _stream(stream)),
+        "sgemm_combine_grad", check)
+
+
+def sgemm_adapters_workspace_size(M, N, K, G, rank) -> int:
+    return int(load_library().sgemm_adapters_workspace_size(int(M), int(N), int(K), int(G), int(rank)))
+
+
+def sgemm_adapters_grad_workspace_size(M, N, K, G, rank) -> int:
+    return int(load_library().sgemm_adapters_grad_workspace_size(int(M), int(N), int(K), int(G), int(rank)))
+
+
+def sgemm_adapters(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, G, rank, ids, ranks, scales, U, ldu, stride_u, V,
+                   ldv, stride_v, workspace, workspace_bytes=None, stream=None, check=True):
+    """``C[m] = alpha * (A[m] B + scales[g] (A[m] U_g) V_g) + beta * C[m]`` with g = ``ids[m]``."""
+    t = _Tensors("sgemm_adapters")
+    ws, nbytes = t.space(workspace, workspace_bytes)
+    return _ret(load_library().sgemm_adapters(
+        M, N, K, alpha, t.matrix(A, "A", M, K, lda), lda, t.matrix(B, "B", K, N, ldb), ldb, beta,
+        t.matrix(C, "C", M, N, ldc), ldc, G, rank, t.ints(ids, "ids", M), t.ints(ranks, "ranks", G),
+        t.floats(scales, "scales", G), t.matrix(U, "U", K, rank, ldu, G, stride_u), ldu, stride_u,
+        t.matrix(V, "V", rank, N, ldv, G, stride_v), ldv, stride_v, ws, nbytes, _stream(stream)),
+        "sgemm_adapters", check)
+
+
+def sgemm_adapters_grad(M, N, K, alpha, A, lda, B, ldb, dC, lddc, G, rank, ids, ranks, scales, U, ldu, stride_u, V,
+                        ldv, stride_v, beta, dA, ldda, dU, lddu, stride_du, dV, lddv, stride_dv, workspace,
+                        workspace_bytes=None, stream=None, check=True):
+    """The gradients of sgemm_adapters() by A (``dA``) and by the adapters (``dU``, ``dV``)."""
+    t = _Tensors("sgemm_adapters_grad")
+    ws, nbytes = t.space(workspace, workspace_bytes)
+    return _ret(load_library().sgemm_adapters_grad(
+        M, N, K, alpha, t.matrix(A, "A", M, K, lda), lda, t.matrix(B, "B", K, N, ldb), ldb,
+        t.matrix(dC, "dC", M, N, lddc), lddc, G, rank, t.ints(ids, "ids", M), t.ints(ranks, "ranks", G),
+        t.floats(scales, "scales", G), t.matrix(U, "U", K, rank, ldu, G, stride_u), ldu, stride_u,
+        t.matrix(V, "V", rank, N, ldv, G, stride_v), ldv, stride_v, beta, t.matrix(dA, "dA", M, K, ldda), ldda,
+        t.matrix(dU, "dU", K, rank, lddu, G, stride_du), lddu, stride_du,
+        t.matrix(dV, "dV", rank, N, lddv, G, stride_dv), lddv, stride_dv, ws, nbytes, _stream(stream)),
+        "sgemm_adapters_grad", check)

@@ -1,0 +1,603 @@
+// rows.hip -- C ABI of the calls around products whose B is picked row by row
+// (see include/sgemm.h): argument checks, the choice of kernel and launches on
+// the caller's stream.  No state, no allocation.
+#include "sgemm.h"
+
+#include <limits.h>
+#include <stdint.h>
+
+#include "rows_kernels.hpp"
+
+namespace {
+
+using rowk::GroupedArgs;
+
+#define NEED(position, condition) \
+    if (!(condition)) return SGEMM_ERR_ARGUMENT - (position)
+
+template <class A>
+int enqueue(void (*kernel)(A), long long grid, int threads, const A &args, hipStream_t stream) {
+    if (grid <= 0) return SGEMM_OK;
+    // a launch holds fewer than 2^32 threads
+    if (grid > INT_MAX || grid * threads >= (1LL << 32)) return SGEMM_ERR_TOO_LARGE;
+    (void)hipGetLastError();  // drop any stale error so the code below is this launch's
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, args);
+    return (int)hipGetLastError();
+}
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// ---- the router ------------------------------------------------------------
+typedef void (*RouteFn)(rowk::RouteArgs);
+typedef void (*RouteGradFn)(rowk::RouteGradArgs);
+
+struct RouteKernel {
+    int experts, k;  // at most
+    int lanes;       // per row
+    RouteFn narrow, wide;
+    RouteGradFn grad;
+};
+#define ROUTE(L, V) {(L) * (V), (L), (L), rowk::route<L, V, false>, rowk::route<L, V, true>, rowk::route_grad<L, V>}
+const RouteKernel kRoutes[] = {ROUTE(16, 1), ROUTE(16, 2), ROUTE(16, 4), ROUTE(16, 8), ROUTE(16, 16),
+                               ROUTE(64, 1), ROUTE(64, 4), ROUTE(64, 16)};
+
+const RouteKernel &route_kernel(int E, int k) {
+    for (const RouteKernel &r : kRoutes)
+        if (E <= r.experts && k <= r.k) return r;
+    return kRoutes[sizeof kRoutes / sizeof kRoutes[0] - 1];
+}
+
+// ---- products over groups of rows -------------------------------------------
+// The row tiles that groups of R rows in all can need at most.
+long long row_tiles(const GroupedArgs &a, int bm) {
+    return a.R / bm + (a.offsets == nullptr ? 1 : (a.G < a.R ? a.G : a.R));
+}
+
+int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
+    if (a.R == 0 || a.N == 0 || a.G == 0) return SGEMM_OK;
+    if (a.alpha == 0.0f) a.K = 0;
+    if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
+    const long long grid = row_tiles(a, 32) * ceil_div(a.N, 32);
+    return enqueue(trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>, grid, 256, a, stream);
+}
+
+int grouped_tn(GroupedArgs a, hipStream_t stream) {
+    if (a.G == 0 || a.M == 0 || a.N == 0) return SGEMM_OK;
+    if (a.alpha == 0.0f) a.R = 0;  // every group's range is then empty
+    if (a.R == 0 && a.beta == 1.0f) return SGEMM_OK;
+    const long long tiles = ceil_div(a.M, 32) * ceil_div(a.N, 32);
+    if (tiles > INT_MAX / a.G) return SGEMM_ERR_TOO_LARGE;
+    return enqueue(rowk::grouped_tn_simple, tiles * a.G, 256, a, stream);
+}
+
+// ---- slots sorted by group ---------------------------------------------------
+// Workgroups of the two-launch form: runs of at least kGroupSlots slots, at most
+// 256 of them (each adds up the counts of all).
+int group_workgroups(int R) {
+    if (R <= rowk::kGroupSlots) return 1;
+    const long long n = ceil_div(R, rowk::kGroupSlots / 2);
+    return n < 256 ? (int)n : 256;
+}
+
+size_t group_bytes(int R, int G) {
+    const int n = group_workgroups(R);
+    return n == 1 ? 0 : round_up((size_t)n * G * 4);
+}
+
+template <int GMAX> int group_launch(rowk::GroupArgs a, int n, hipStream_t stream) {
+    if (n > 1) {
+        const int rc = enqueue(rowk::group_rows<GMAX, true>, n, rowk::kGroupThreads, a, stream);
+        if (rc != SGEMM_OK) return rc;
+    }
+    return enqueue(rowk::group_rows<GMAX, false>, n, rowk::kGroupThreads, a, stream);
+}
+
+int group(int R, int G, const int *ids, int *offsets, int *rows, void *workspace, hipStream_t stream) {
+    const int n = group_workgroups(R);
+    rowk::GroupArgs a;
+    a.R = R;
+    a.G = G;
+    a.run = n == 1 ? (R > 0 ? R : 1) : (int)ceil_div(R, n);
+    a.ids = ids;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.counts = static_cast<int *>(workspace);
+    return G <= 1024 ? group_launch<1024>(a, n, stream) : group_launch<SGEMM_MAX_GROUPS>(a, n, stream);
+}
+
+bool workspace_ok(const void *p, size_t have, size_t need) {
+    return need == 0 || (p != nullptr && have >= need && ((uintptr_t)p & 255u) == 0);
+}
+
+// ---- adapters ----------------------------------------------------------------
+// Workspace: [offsets][rows][group counts][H: M x rank][dH: M x rank][sgemm's]
+struct AdapterSpace {
+    size_t offsets, rows, counts, h, dh, product, end;
+    AdapterSpace(int M, int N, int K, int G, int rank, bool grad) {
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t here = at;
+            at += round_up(bytes);
+            return here;
+        };
+        offsets = take(((size_t)G + 1) * 4);
+        rows = take((size_t)M * 4);
+        counts = take(group_bytes(M, G));
+        h = take((size_t)M * rank * 4);
+        dh = take(grad ? (size_t)M * rank * 4 : 0);
+        product = take(grad ? 0 : sgemm_workspace_size(M, N, K));
+        end = at;
+    }
+};
+
+struct Adapters {
+    int M, N, K, G, rank;
+    float alpha;
+    const int *ids, *ranks;
+    const float *scales, *A, *U, *V;
+    int lda, ldu, ldv;
+    long long stride_u, stride_v;
+};
+
+GroupedArgs blank(int G, int R) {
+    GroupedArgs a = {};
+    a.G = G;
+    a.R = R;
+    a.alpha = 1.0f;
+    return a;
+}
+
+// H[m] = A[m] U_g for the placed rows
+GroupedArgs shrink(const Adapters &p, const int *offsets, const int *rows, float *H) {
+    GroupedArgs a = blank(p.G, p.M);
+    a.N = p.rank;
+    a.K = p.K;
+    a.A = p.A;
+    a.lda = p.lda;
+    a.a_div = 1;
+    a.B = p.U;
+    a.ldb = p.ldu;
+    a.stride_b = p.stride_u;
+    a.C = H;
+    a.ldc = p.rank;
+    a.c_scatter = 1;
+    a.offsets = offsets;
+    a.rows = rows;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_route(int T, int E, int k, int scoring, const float *logits, int ldl, const float *bias, int groups,
+                int top_groups, int group_best, int renorm, float scale, int *ids, float *weights,
+                hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, E >= 1 && E <= SGEMM_ROUTE_MAX_EXPERTS);
+    NEED(3, k >= 1 && k <= E && k <= SGEMM_ROUTE_MAX_K);
+    NEED(4, scoring == SGEMM_SCORE_SOFTMAX || scoring == SGEMM_SCORE_SIGMOID);
+    NEED(5, T == 0 || logits != nullptr);
+    NEED(6, ldl >= E);
+    NEED(8, groups >= 1 && groups <= 64 && E % groups == 0);
+    NEED(9, top_groups >= 1 && top_groups <= groups);
+    NEED(10, group_best == 1 || group_best == 2);
+    NEED(13, T == 0 || ids != nullptr);
+    NEED(14, T == 0 || weights != nullptr);
+    rowk::RouteArgs a;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.sigmoid = scoring == SGEMM_SCORE_SIGMOID;
+    a.groups = groups;
+    a.top_groups = top_groups;
+    a.group_best = group_best;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.inv_per = 1.0f / (float)(E / groups);
+    a.logits = logits;
+    a.bias = bias;
+    a.ldl = ldl;
+    a.ids = ids;
+    a.weights = weights;
+    const RouteKernel &r = route_kernel(E, k);
+    const bool wide = bias != nullptr || (groups > 1 && group_best == 2);
+    return enqueue(wide ? r.wide : r.narrow, ceil_div(T, rowk::kRouteThreads / r.lanes), rowk::kRouteThreads, a,
+                   stream);
+}
+
+int sgemm_route_grad(int T, int E, int k, int scoring, const float *logits, int ldl, int renorm, float scale,
+                     const int *ids, const float *dweights, float *dlogits, int lddl, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, E >= 1 && E <= SGEMM_ROUTE_MAX_EXPERTS);
+    NEED(3, k >= 1 && k <= E && k <= SGEMM_ROUTE_MAX_K);
+    NEED(4, scoring == SGEMM_SCORE_SOFTMAX || scoring == SGEMM_SCORE_SIGMOID);
+    NEED(5, T == 0 || logits != nullptr);
+    NEED(6, ldl >= E);
+    NEED(9, T == 0 || ids != nullptr);
+    NEED(10, T == 0 || dweights != nullptr);
+    NEED(11, T == 0 || dlogits != nullptr);
+    NEED(12, lddl >= E);
+    rowk::RouteGradArgs a;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.sigmoid = scoring == SGEMM_SCORE_SIGMOID;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.logits = logits;
+    a.ldl = ldl;
+    a.ids = ids;
+    a.dweights = dweights;
+    a.dlogits = dlogits;
+    a.lddl = lddl;
+    const RouteKernel &r = route_kernel(E, k);
+    return enqueue(r.grad, ceil_div(T, rowk::kRouteThreads / r.lanes), rowk::kRouteThreads, a, stream);
+}
+
+size_t sgemm_group_rows_workspace_size(int R, int G) {
+    return R < 0 || G < 1 || G > SGEMM_MAX_GROUPS ? 0 : group_bytes(R, G);
+}
+
+int sgemm_group_rows(int R, int G, const int *ids, int *offsets, int *rows, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+    NEED(1, R >= 0);
+    NEED(2, G >= 1 && G <= SGEMM_MAX_GROUPS);
+    NEED(3, R == 0 || ids != nullptr);
+    NEED(4, offsets != nullptr);
+    NEED(5, R == 0 || rows != nullptr);
+    if (!workspace_ok(workspace, workspace_bytes, group_bytes(R, G))) return SGEMM_ERR_WORKSPACE;
+    return group(R, G, ids, offsets, rows, workspace, stream);
+}
+
+int sgemm_grouped(int G, int R, int N, int K, float alpha, const float *A, int lda, int a_div, const float *B,
+                  int ldb, long long stride_b, int trans_b, float beta, float *C, int ldc, int c_scatter,
+                  const int *offsets, const int *rows, hipStream_t stream) {
+    NEED(1, G >= 0);
+    NEED(2, R >= 0);
+    NEED(3, N >= 0);
+    NEED(4, K >= 0);
+    const bool empty = G == 0 || R == 0 || N == 0;
+    const bool product = !empty && K > 0 && alpha != 0.0f;
+    NEED(6, (!product || A != nullptr) && aligned4(A));
+    NEED(7, lda >= (K > 1 ? K : 1));
+    NEED(8, a_div >= 0);
+    NEED(9, (!product || B != nullptr) && aligned4(B));
+    NEED(10, ldb >= (trans_b ? (K > 1 ? K : 1) : (N > 1 ? N : 1)));
+    NEED(11, stride_b >= 0);
+    NEED(14, (empty || C != nullptr) && aligned4(C));
+    NEED(15, ldc >= (N > 1 ? N : 1));
+    NEED(17, empty || offsets != nullptr);
+    NEED(18, empty || rows != nullptr || (a_div == 0 && c_scatter == 0));
+    GroupedArgs a = blank(G, R);
+    a.N = N;
+    a.K = K;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.A = A;
+    a.lda = lda;
+    a.a_div = a_div;
+    a.B = B;
+    a.ldb = ldb;
+    a.stride_b = stride_b;
+    a.C = C;
+    a.ldc = ldc;
+    a.c_scatter = c_scatter != 0;
+    a.offsets = offsets;
+    a.rows = rows;
+    return grouped(a, trans_b != 0, stream);
+}
+
+int sgemm_grouped_tn(int G, int R, int M, int N, float alpha, const float *A, int lda, int a_div, const float *B,
+                     int ldb, int b_div, float beta, float *C, int ldc, long long stride_c, const int *offsets,
+                     const int *rows, hipStream_t stream) {
+    NEED(1, G >= 0);
+    NEED(2, R >= 0);
+    NEED(3, M >= 0);
+    NEED(4, N >= 0);
+    const bool empty = G == 0 || M == 0 || N == 0;
+    const bool product = !empty && R > 0 && alpha != 0.0f;
+    NEED(6, (!product || A != nullptr) && aligned4(A));
+    NEED(7, lda >= (M > 1 ? M : 1));
+    NEED(8, a_div >= 0);
+    NEED(9, (!product || B != nullptr) && aligned4(B));
+    NEED(10, ldb >= (N > 1 ? N : 1));
+    NEED(11, b_div >= 0);
+    NEED(13, (empty || C != nullptr) && aligned4(C));
+    NEED(14, ldc >= (N > 1 ? N : 1));
+    NEED(15, G <= 1 || empty || stride_c >= (long long)(M - 1) * ldc + N);
+    NEED(16, !product || offsets != nullptr);
+    NEED(17, !product || rows != nullptr || (a_div == 0 && b_div == 0));
+    GroupedArgs a = blank(G, R);
+    a.M = M;
+    a.N = N;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.A = A;
+    a.lda = lda;
+    a.a_div = a_div;
+    a.B = B;
+    a.ldb = ldb;
+    a.b_div = b_div;
+    a.C = C;
+    a.ldc = ldc;
+    a.stride_c = stride_c;
+    a.offsets = offsets;
+    a.rows = rows;
+    if (!product) a.R = 0;  // offsets may be NULL: one empty group each
+    return grouped_tn(a, stream);
+}
+
+int sgemm_combine(int T, int k, int N, int E, const int *ids, const float *weights, const float *Y, int ldy,
+                  float beta, float *out, int ldo, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, k >= 1 && k <= SGEMM_ROUTE_MAX_K);
+    NEED(3, N >= 0);
+    NEED(4, E >= 0);
+    const bool empty = T == 0 || N == 0;
+    NEED(7, (empty || Y != nullptr) && aligned4(Y));
+    NEED(8, ldy >= (N > 1 ? N : 1));
+    NEED(10, (empty || out != nullptr) && aligned4(out));
+    NEED(11, ldo >= (N > 1 ? N : 1));
+    if (empty) return SGEMM_OK;
+    rowk::CombineArgs a;
+    a.T = T;
+    a.k = k;
+    a.N = N;
+    a.E = E;
+    a.ids = ids;
+    a.weights = weights;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.ldo = ldo;
+    a.beta = beta;
+    a.out = out;
+    a.chunks = (int)ceil_div(N, 256);
+    a.units = (int64_t)T * a.chunks;
+    return enqueue(rowk::combine, ceil_div(a.units, 4), 256, a, stream);
+}
+
+int sgemm_combine_grad(int T, int k, int N, int E, const int *ids, const float *weights, const float *dout,
+                       int ldd, const float *Y, int ldy, float *dY, int lddy, float *dweights,
+                       hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, k >= 1 && k <= SGEMM_ROUTE_MAX_K);
+    NEED(3, N >= 0);
+    NEED(4, E >= 0);
+    const bool empty = T == 0 || N == 0;
+    NEED(7, (empty || dout != nullptr) && aligned4(dout));
+    NEED(8, ldd >= (N > 1 ? N : 1));
+    NEED(9, (empty || dweights == nullptr || Y != nullptr) && aligned4(Y));
+    NEED(10, ldy >= (N > 1 ? N : 1));
+    NEED(11, aligned4(dY));
+    NEED(12, lddy >= (N > 1 ? N : 1));
+    if (T == 0 || (dweights == nullptr && (dY == nullptr || N == 0))) return SGEMM_OK;
+    rowk::CombineGradArgs a;
+    a.T = T;
+    a.k = k;
+    a.N = N;
+    a.E = E;
+    a.ids = ids;
+    a.weights = weights;
+    a.dout = dout;
+    a.ldd = ldd;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.dY = dY;
+    a.lddy = lddy;
+    a.dweights = dweights;
+    return enqueue(rowk::combine_grad, T, 256, a, stream);
+}
+
+size_t sgemm_adapters_workspace_size(int M, int N, int K, int G, int rank) {
+    if (M < 0 || N < 0 || K < 0 || G < 1 || G > SGEMM_MAX_GROUPS || rank < 1 || rank > SGEMM_MAX_RANK) return 0;
+    return AdapterSpace(M, N, K, G, rank, false).end;
+}
+
+size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank) {
+    if (M < 0 || N < 0 || K < 0 || G < 1 || G > SGEMM_MAX_GROUPS || rank < 1 || rank > SGEMM_MAX_RANK) return 0;
+    return AdapterSpace(M, N, K, G, rank, true).end;
+}
+
+int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta,
+                   float *C, int ldc, int G, int rank, const int *ids, const int *ranks, const float *scales,
+                   const float *U, int ldu, long long stride_u, const float *V, int ldv, long long stride_v,
+                   void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    NEED(1, M >= 0);
+    NEED(2, N >= 0);
+    NEED(3, K >= 0);
+    const bool empty = M == 0 || N == 0;
+    const bool product = !empty && K > 0 && alpha != 0.0f;
+    NEED(5, (!product || A != nullptr) && aligned4(A));
+    NEED(6, lda >= (K > 1 ? K : 1));
+    NEED(7, (!product || B != nullptr) && aligned4(B));
+    NEED(8, ldb >= (N > 1 ? N : 1));
+    NEED(10, (empty || C != nullptr) && aligned4(C));
+    NEED(11, ldc >= (N > 1 ? N : 1));
+    NEED(12, G >= 1 && G <= SGEMM_MAX_GROUPS);
+    NEED(13, rank >= 1 && rank <= SGEMM_MAX_RANK);
+    NEED(14, !product || ids != nullptr);
+    NEED(17, (!product || U != nullptr) && aligned4(U));
+    NEED(18, ldu >= rank);
+    NEED(19, stride_u >= 0);
+    NEED(20, (!product || V != nullptr) && aligned4(V));
+    NEED(21, ldv >= (N > 1 ? N : 1));
+    NEED(22, stride_v >= 0);
+    const AdapterSpace at(M, N, K, G, rank, false);
+    if (!workspace_ok(workspace, workspace_bytes, at.end)) return SGEMM_ERR_WORKSPACE;
+    if (!product) return sgemm(M, N, K, 0.0f, A, lda, B, ldb, beta, C, ldc, stream);
+    char *w = static_cast<char *>(workspace);
+    int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
+    float *H = reinterpret_cast<float *>(w + at.h);
+    const Adapters p = {M, N, K, G, rank, alpha, ids, ranks, scales, A, U, V, lda, ldu, ldv, stride_u, stride_v};
+
+    int rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
+    if (rc == SGEMM_OK) rc = grouped(shrink(p, offsets, rows, H), false, stream);
+    if (rc == SGEMM_OK)
+        rc = sgemm_ws(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, w + at.product, at.end - at.product, stream);
+    if (rc == SGEMM_OK) {  // C[m] += alpha scale H[m] V_g
+        GroupedArgs a = blank(G, M);
+        a.N = N;
+        a.K = rank;
+        a.alpha = alpha;
+        a.beta = 1.0f;
+        a.A = H;
+        a.lda = rank;
+        a.a_div = 1;
+        a.B = V;
+        a.ldb = ldv;
+        a.stride_b = stride_v;
+        a.C = C;
+        a.ldc = ldc;
+        a.c_scatter = 1;
+        a.offsets = offsets;
+        a.rows = rows;
+        a.scales = scales;
+        a.ranks = ranks;
+        a.rank_k = 1;
+        rc = grouped(a, false, stream);
+    }
+    return rc;
+}
+
+int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
+                        const float *dC, int lddc, int G, int rank, const int *ids, const int *ranks,
+                        const float *scales, const float *U, int ldu, long long stride_u, const float *V, int ldv,
+                        long long stride_v, float beta, float *dA, int ldda, float *dU, int lddu,
+                        long long stride_du, float *dV, int lddv, long long stride_dv, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+    NEED(1, M >= 0);
+    NEED(2, N >= 0);
+    NEED(3, K >= 0);
+    const bool product = M > 0 && alpha != 0.0f;
+    const bool adapters = dU != nullptr || dV != nullptr;
+    NEED(5, (!product || K == 0 || !adapters || A != nullptr) && aligned4(A));
+    NEED(6, lda >= (K > 1 ? K : 1));
+    NEED(7, (!product || K == 0 || N == 0 || dA == nullptr || B != nullptr) && aligned4(B));
+    NEED(8, ldb >= (N > 1 ? N : 1));
+    NEED(9, (!product || N == 0 || dC != nullptr) && aligned4(dC));
+    NEED(10, lddc >= (N > 1 ? N : 1));
+    NEED(11, G >= 1 && G <= SGEMM_MAX_GROUPS);
+    NEED(12, rank >= 1 && rank <= SGEMM_MAX_RANK);
+    NEED(13, !product || ids != nullptr);
+    NEED(16, (!product || K == 0 || U != nullptr) && aligned4(U));
+    NEED(17, ldu >= rank);
+    NEED(18, stride_u >= 0);
+    NEED(19, (!product || N == 0 || V != nullptr) && aligned4(V));
+    NEED(20, ldv >= (N > 1 ? N : 1));
+    NEED(21, stride_v >= 0);
+    NEED(23, aligned4(dA));
+    NEED(24, ldda >= (K > 1 ? K : 1));
+    NEED(25, (dU != nullptr || dV == nullptr) && aligned4(dU));
+    NEED(26, lddu >= rank);
+    NEED(27, G == 1 || K == 0 || stride_du >= (long long)(K - 1) * lddu + rank);
+    NEED(28, (dV != nullptr || dU == nullptr) && aligned4(dV));
+    NEED(29, lddv >= (N > 1 ? N : 1));
+    NEED(30, G == 1 || N == 0 || stride_dv >= (long long)(rank - 1) * lddv + N);
+    const AdapterSpace at(M, N, K, G, rank, true);
+    if (!workspace_ok(workspace, workspace_bytes, at.end)) return SGEMM_ERR_WORKSPACE;
+    char *w = static_cast<char *>(workspace);
+    int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
+    float *H = reinterpret_cast<float *>(w + at.h), *dH = reinterpret_cast<float *>(w + at.dh);
+    const Adapters p = {M, N, K, G, rank, alpha, ids, ranks, scales, A, U, V, lda, ldu, ldv, stride_u, stride_v};
+
+    int rc = SGEMM_OK;
+    if (product) {
+        rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
+        if (rc == SGEMM_OK) {  // dH[m] = alpha scale dC[m] V_g^T
+            GroupedArgs a = blank(G, M);
+            a.N = rank;
+            a.K = N;
+            a.alpha = alpha;
+            a.A = dC;
+            a.lda = lddc;
+            a.a_div = 1;
+            a.B = V;
+            a.ldb = ldv;
+            a.stride_b = stride_v;
+            a.C = dH;
+            a.ldc = rank;
+            a.c_scatter = 1;
+            a.offsets = offsets;
+            a.rows = rows;
+            a.scales = scales;
+            rc = grouped(a, true, stream);
+        }
+    }
+    if (rc == SGEMM_OK && dA != nullptr) {  // dA = alpha dC B^T
+        GroupedArgs a = blank(1, M);
+        a.N = K;
+        a.K = N;
+        a.alpha = alpha;
+        a.A = dC;
+        a.lda = lddc;
+        a.B = B;
+        a.ldb = ldb;
+        a.C = dA;
+        a.ldc = ldda;
+        rc = grouped(a, true, stream);
+        if (rc == SGEMM_OK && product) {  // dA[m] += dH[m] U_g^T
+            GroupedArgs b = blank(G, M);
+            b.N = K;
+            b.K = rank;
+            b.beta = 1.0f;
+            b.A = dH;
+            b.lda = rank;
+            b.a_div = 1;
+            b.B = U;
+            b.ldb = ldu;
+            b.stride_b = stride_u;
+            b.C = dA;
+            b.ldc = ldda;
+            b.c_scatter = 1;
+            b.offsets = offsets;
+            b.rows = rows;
+            b.ranks = ranks;
+            b.rank_k = 1;
+            rc = grouped(b, true, stream);
+        }
+    }
+    if (rc == SGEMM_OK && adapters) {
+        GroupedArgs a = blank(G, product ? M : 0);  // dU_g = A^T dH
+        a.M = K;
+        a.N = rank;
+        a.beta = beta;
+        a.A = A;
+        a.lda = lda;
+        a.a_div = 1;
+        a.B = dH;
+        a.ldb = rank;
+        a.b_div = 1;
+        a.C = dU;
+        a.ldc = lddu;
+        a.stride_c = stride_du;
+        a.offsets = product ? offsets : nullptr;
+        a.rows = rows;
+        a.ranks = ranks;
+        a.rank_n = 1;
+        rc = grouped_tn(a, stream);
+        if (rc == SGEMM_OK && product) rc = grouped(shrink(p, offsets, rows, H), false, stream);
+        if (rc == SGEMM_OK) {  // dV_g = alpha scale H^T dC
+            GroupedArgs b = a;
+            b.M = rank;
+            b.N = N;
+            b.alpha = alpha;
+            b.A = H;
+            b.lda = rank;
+            b.B = dC;
+            b.ldb = lddc;
+            b.C = dV;
+            b.ldc = lddv;
+            b.stride_c = stride_dv;
+            b.scales = scales;
+            b.rank_n = 0;
+            b.rank_m = 1;
+            rc = grouped_tn(b, stream);
+        }
+    }
+    return rc;
+}
+
+}  // extern "C"

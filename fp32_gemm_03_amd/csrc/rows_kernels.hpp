@@ -1,0 +1,756 @@
+// rows_kernels.hpp -- kernels of the calls around products whose B is picked
+// row by row: the router and its gradient, the slots sorted by group, the
+// weighted sum of a token's slots and its gradient, and the products in their
+// simplest form (any strides; the fast forms are in grouped_kernels.hpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+namespace rowk {
+
+// ---------------------------------------------------------------------------
+// Lane exchange inside a 16-lane DPP row and across a wave's four rows.
+// ---------------------------------------------------------------------------
+template <int CTRL> __device__ __forceinline__ int dpp(int v) {
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(dpp<CTRL>(__float_as_int(v)));
+}
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+    return __hiloint2double(dpp<CTRL>(__double2hiint(v)), dpp<CTRL>(__double2loint(v)));
+}
+__device__ __forceinline__ int at_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ float at_lane(float v, int l) { return __int_as_float(at_lane(__float_as_int(v), l)); }
+__device__ __forceinline__ double at_lane(double v, int l) {
+    return __hiloint2double(at_lane(__double2hiint(v), l), at_lane(__double2loint(v), l));
+}
+
+// op over the L lanes (16 or 64) that share a row; every lane gets the result,
+// always combined in the same order.  row_ror:n (0x120 + n) turns a 16-lane row.
+template <int L, class T, class Op> __device__ __forceinline__ T reduce(T v, Op op) {
+    static_assert(L == 16 || L == 64, "a DPP row or a wave");
+    v = op(v, dpp<0x128>(v));
+    v = op(v, dpp<0x124>(v));
+    v = op(v, dpp<0x122>(v));
+    v = op(v, dpp<0x121>(v));
+    if constexpr (L == 64) v = op(op(at_lane(v, 0), at_lane(v, 16)), op(at_lane(v, 32), at_lane(v, 48)));
+    return v;
+}
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+    __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+};
+struct Min {
+    __device__ __forceinline__ int operator()(int a, int b) const { return a < b ? a : b; }
+};
+struct Add {
+    template <class T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// four floats at any 4-byte alignment (one 16-byte access on gfx950)
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// ---------------------------------------------------------------------------
+// The router.  L lanes hold one row: element e = l + L v in register v of lane
+// l, so a load instruction covers 64 / L rows' contiguous pieces.  The k
+// choices are k rounds of an arg-max over the row: the lanes' own maxima, a
+// reduction over the L lanes, then the lowest index among the lanes that hold
+// the maximum; the owner's element is then taken out.
+//
+// What decides the order is a sum of scores (a bias, or the two best of a
+// group), where 32 bits would swap neighbours that differ by less than their
+// rounding: WIDE computes scores and keys in 64 bits.  Otherwise the scores
+// rise with the logits, and those are compared as they are.  The chosen
+// weights are computed in 64 bits either way (one lane per choice) and rounded
+// once.
+// ---------------------------------------------------------------------------
+struct RouteArgs {
+    int T, E, k, sigmoid, groups, top_groups, group_best, renorm;
+    float scale, inv_per;  // inv_per: 1 / (E / groups)
+    const float *logits, *bias;
+    int64_t ldl;
+    int *ids;
+    float *weights;
+};
+
+// exp(x - m) with m the row's maximum; equal values (infinities too) give 1
+__device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
+__device__ __forceinline__ double exp_below(double x, double m) { return x == m ? 1.0 : exp(x - m); }
+
+constexpr int kRouteThreads = 256;
+
+template <int L, int V, bool WIDE>
+__global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
+    typedef typename std::conditional<WIDE, double, float>::type Key;
+    constexpr int ROWS = kRouteThreads / L;
+    const Key NONE = -INFINITY;
+    __shared__ Key keys[ROWS][L * V + 1];
+    __shared__ Key worth[ROWS][L * V < 64 ? L * V : 64];
+    __shared__ int kept[ROWS][L * V < 64 ? L * V : 64];
+    const int l = threadIdx.x % L, r = threadIdx.x / L;
+    const int t = (int)blockIdx.x * ROWS + r;
+    const bool in = t < a.T;
+    const float *row = a.logits + (int64_t)(in ? t : 0) * a.ldl;
+
+    float x[V];
+    float top = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = l + L * v;
+        x[v] = in && e < a.E ? row[e] : -INFINITY;
+        nan |= x[v] != x[v];
+        top = fmaxf(top, x[v]);  // a NaN is passed over
+    }
+    top = reduce<L>(top, Max());
+    const int bad = reduce<L>(nan ? 0 : 1, Min());  // 0: some logit of the row is NaN
+
+    Key key[V];
+    double total = 0.0;
+    if constexpr (WIDE) {
+        if (!a.sigmoid) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                key[v] = exp_below((double)x[v], (double)top);
+                if (!(x[v] > -INFINITY)) key[v] = 0.0;
+                total += key[v];
+            }
+            total = reduce<L>(total, Add());
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = l + L * v;
+            double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[v])) : key[v] / total;
+            if (a.bias != nullptr && e < a.E) s += (double)a.bias[e];
+            key[v] = x[v] > -INFINITY && s == s ? s : NONE;
+        }
+    } else {
+        if (!a.sigmoid && !a.renorm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (x[v] > -INFINITY) sum += exp_below(x[v], top);
+            total = (double)reduce<L>(sum, Add());
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? x[v] : NONE;
+    }
+
+    if (a.groups > 1) {
+        // each group's worth, one lane per group from the keys in LDS; a group
+        // is kept when fewer than top_groups are worth more (or as much, with a
+        // lower index)
+        const int per = a.E / a.groups;
+#pragma unroll
+        for (int v = 0; v < V; ++v) keys[r][l + L * v] = key[v];
+        __syncthreads();
+        for (int g = l; g < a.groups; g += L) {
+            Key b0 = NONE, b1 = NONE;
+            for (int i = 0; i < per; ++i) {
+                const Key q = keys[r][g * per + i];
+                b1 = q > b0 ? b0 : (q > b1 ? q : b1);
+                b0 = q > b0 ? q : b0;
+            }
+            // (no sum where the second is missing: -inf counts nothing)
+            worth[r][g] = a.group_best == 2 && b1 > NONE ? b0 + b1 : b0;
+        }
+        __syncthreads();
+        for (int g = l; g < a.groups; g += L) {
+            const Key w = worth[r][g];
+            int above = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const Key o = worth[r][h];
+                above += (o > w || (o == w && h < g)) ? 1 : 0;
+            }
+            kept[r][g] = above < a.top_groups ? 1 : 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = l + L * v;
+            // exact: e < 1024, and (e + 1/2) / per is at least 1 / (2 per) from a whole number
+            const int g = (int)(((float)e + 0.5f) * a.inv_per);
+            if (e < a.E && !kept[r][g]) key[v] = NONE;
+        }
+    }
+
+    int mine = -1;  // lane j keeps choice j
+    for (int j = 0; j < a.k; ++j) {
+        Key best = NONE;
+        int at = INT_MAX;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (key[v] > best) {
+                best = key[v];
+                at = l + L * v;
+            }
+        const Key most = reduce<L>(best, Max());
+        const int first = reduce<L>(best == most && most > NONE ? at : INT_MAX, Min());
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (l + L * v == first) key[v] = NONE;
+        if (l == j) mine = first == INT_MAX ? -1 : first;
+    }
+
+    const bool found = mine >= 0;
+    const float xm = found ? row[mine] : -INFINITY;
+    double s;
+    if (a.sigmoid) {
+        s = 1.0 / (1.0 + exp(-(double)xm));
+    } else {
+        // renormalised over the chosen alone: their own maximum, so that far
+        // choices do not vanish
+        const float m = a.renorm ? reduce<L>(xm, Max()) : top;
+        s = exp_below((double)xm, (double)m);
+        if (!a.renorm) s /= total;
+    }
+    if (!found) s = 0.0;
+    if (a.renorm) {
+        const double sum = reduce<L>(s, Add());
+        s = sum > 0.0 ? s / sum : 0.0;
+    }
+    if (in && l < a.k) {
+        a.ids[(int64_t)t * a.k + l] = mine;
+        a.weights[(int64_t)t * a.k + l] = !found ? 0.0f : bad == 0 ? NAN : (float)(s * (double)a.scale);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The router's gradient, from the logits, the ids and the weights' gradient c:
+// with p the weights before `scale` and c scaled,
+//   renorm:  dl_i = p_i (c_i - sum c p) for the chosen (times 1 - s_i for the
+//            sigmoid), 0 elsewhere; the rest of the row need not be read;
+//   else softmax: dl_e = s_e (c_e - sum c s), sigmoid: dl_e = c_e s_e (1 - s_e).
+// The chosen parts are computed in 64 bits, one lane per choice, and spread
+// over the row through LDS.
+// ---------------------------------------------------------------------------
+struct RouteGradArgs {
+    int T, E, k, sigmoid, renorm;
+    float scale;
+    const float *logits;
+    int64_t ldl;
+    const int *ids;
+    const float *dweights;
+    float *dlogits;
+    int64_t lddl;
+};
+
+template <int L, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_grad(RouteGradArgs a) {
+    constexpr int ROWS = kRouteThreads / L;
+    __shared__ float spread[ROWS][L * V + 1];
+    const int l = threadIdx.x % L, r = threadIdx.x / L;
+    const int t = (int)blockIdx.x * ROWS + r;
+    const bool in = t < a.T;
+    const float *row = a.logits + (int64_t)(in ? t : 0) * a.ldl;
+    const bool whole = !a.sigmoid && !a.renorm;  // every element has a gradient
+
+    int id = -1;
+    float c = 0.0f;
+    if (in && l < a.k) {
+        id = a.ids[(int64_t)t * a.k + l];
+        if ((unsigned)id >= (unsigned)a.E) id = -1;
+        if (id >= 0) c = a.dweights[(int64_t)t * a.k + l] * a.scale;
+    }
+    const float xi = id >= 0 ? row[id] : -INFINITY;
+
+    float x[V], top = -INFINITY, sum = 0.0f;
+    if (whole) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = l + L * v;
+            x[v] = in && e < a.E ? row[e] : -INFINITY;
+            top = fmaxf(top, x[v]);
+        }
+        top = reduce<L>(top, Max());
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = x[v] == -INFINITY ? 0.0f : exp_below(x[v], top);
+            sum += x[v];
+        }
+        sum = reduce<L>(sum, Add());
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+
+    double d = 0.0;  // the chosen expert's own part
+    float q = 0.0f;  // what every element of the row subtracts
+    const bool has = xi > -INFINITY || xi != xi;
+    if (a.sigmoid) {
+        const double s = has ? 1.0 / (1.0 + exp(-(double)xi)) : 0.0;
+        const double other = 1.0 / (1.0 + exp((double)xi));  // 1 - s without cancellation
+        if (a.renorm) {
+            const double S = reduce<L>(id >= 0 ? s : 0.0, Add());
+            const double p = id >= 0 && S != 0.0 ? s / S : 0.0;
+            const double mean = reduce<L>(p * (double)c, Add());
+            d = p * ((double)c - mean) * other;
+        } else {
+            d = (double)c * s * other;
+        }
+    } else if (a.renorm) {
+        const float m = reduce<L>(xi, Max());
+        const double e = has ? exp_below((double)xi, (double)m) : 0.0;
+        const double S = reduce<L>(e, Add());
+        const double p = S != 0.0 ? e / S : 0.0;
+        d = p * ((double)c - reduce<L>(p * (double)c, Add()));
+    } else {
+        const double s = has ? exp_below((double)xi, (double)top) * (double)inv : 0.0;
+        q = (float)reduce<L>(s * (double)c, Add());
+        d = (double)c;
+    }
+
+#pragma unroll
+    for (int v = 0; v < V; ++v) spread[r][l + L * v] = 0.0f;
+    __syncthreads();
+    if (id >= 0) spread[r][id] = (float)d;
+    __syncthreads();
+    if (!in) return;
+    float *out = a.dlogits + (int64_t)t * a.lddl;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = l + L * v;
+        if (e >= a.E) continue;
+        const float w = spread[r][e];
+        out[e] = whole ? x[v] * inv * (w - q) : w;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Slots sorted by group: a counting sort that keeps the slots' order.  A
+// workgroup's waves each take a run of consecutive slots, 64 at a time.  The
+// place of a slot is: what lower groups hold, plus its group's slots in earlier
+// runs, plus those earlier in its own run, counted with one ballot per bit of
+// the id (the lanes whose ids agree in every bit), so there is no atomic and
+// the order is the slots' own.  One workgroup does it all up to kGroupSlots
+// slots; beyond, a first launch counts each workgroup's run and in a second
+// every workgroup adds up what lies before its own.
+// ---------------------------------------------------------------------------
+constexpr int kGroupWaves = 8;
+constexpr int kGroupThreads = 64 * kGroupWaves;
+constexpr int kGroupSlots = 4096;  // slots of one workgroup
+
+struct GroupArgs {
+    int R, G, run;  // run: slots per workgroup
+    const int *ids;
+    int *offsets, *rows, *counts;  // counts: [workgroups][G]
+};
+
+// lanes with the same id (all ones where `id` is G or more is not asked for)
+__device__ __forceinline__ unsigned long long same_id(int id, int bits) {
+    unsigned long long m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned long long set = __ballot((id >> b) & 1);
+        m &= (id >> b) & 1 ? set : ~set;
+    }
+    return m;
+}
+
+template <int GMAX, bool COUNT_ONLY>
+__global__ void __launch_bounds__(kGroupThreads) group_rows(GroupArgs a) {
+    __shared__ int count[kGroupWaves][GMAX];
+    __shared__ int wave_sum[kGroupWaves];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int nwg = gridDim.x, wg = blockIdx.x;
+    const int64_t wg0 = (int64_t)wg * a.run;
+    const int64_t wg1 = wg0 + a.run < a.R ? wg0 + a.run : a.R;
+    const int per = ((a.run + kGroupWaves - 1) / kGroupWaves + 63) / 64 * 64;  // slots per wave
+    const int64_t s0 = wg0 + (int64_t)w * per < wg1 ? wg0 + (int64_t)w * per : wg1;
+    const int64_t s1 = s0 + per < wg1 ? s0 + per : wg1;
+    const int bits = 32 - __clz(a.G);  // ids up to G itself, which stands for none
+    auto id_of = [&](int64_t s) {
+        const int id = s < s1 ? a.ids[s] : a.G;
+        return (unsigned)id < (unsigned)a.G ? id : a.G;
+    };
+    const unsigned long long below = (1ull << lane) - 1;
+
+    for (int i = lane; i < a.G; i += 64) count[w][i] = 0;
+    for (int64_t s = s0; s < s1; s += 64) {
+        const int id = id_of(s + lane);
+        const unsigned long long same = same_id(id, bits);
+        // the first lane of each id adds the number of its lanes
+        if (id < a.G && (same & below) == 0) count[w][id] += __popcll(same);
+    }
+    __syncthreads();
+    if constexpr (COUNT_ONLY) {
+        for (int g = tid; g < a.G; g += kGroupThreads) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kGroupWaves; ++i) n += count[i][g];
+            a.counts[(int64_t)wg * a.G + g] = n;
+        }
+        return;
+    }
+
+    // thread i takes PER consecutive groups: their totals, what earlier
+    // workgroups and earlier waves hold of them, and the sum of all lower ones
+    constexpr int PER = (GMAX + kGroupThreads - 1) / kGroupThreads;
+    int total[PER], before[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = tid * PER + i;
+        total[i] = before[i] = 0;
+        if (g < a.G) {
+            if (nwg == 1) {
+#pragma unroll
+                for (int j = 0; j < kGroupWaves; ++j) total[i] += count[j][g];
+            } else {
+                for (int b = 0; b < nwg; ++b) {
+                    const int n = a.counts[(int64_t)b * a.G + g];
+                    total[i] += n;
+                    before[i] += b < wg ? n : 0;
+                }
+            }
+        }
+        sum += total[i];
+    }
+    int upto = sum;  // inclusive over the wave's lanes
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 63) wave_sum[w] = upto;
+    __syncthreads();
+    int base = upto - sum;
+    for (int i = 0; i < w; ++i) base += wave_sum[i];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = tid * PER + i;
+        if (g >= a.G) break;
+        if (wg == 0) {
+            a.offsets[g] = base;
+            if (g == a.G - 1) a.offsets[a.G] = base + total[i];
+        }
+        int at = base + before[i];  // where this workgroup's first slot of g goes
+#pragma unroll
+        for (int j = 0; j < kGroupWaves; ++j) {
+            const int n = count[j][g];
+            count[j][g] = at;
+            at += n;
+        }
+        base += total[i];
+    }
+    __syncthreads();
+    for (int64_t s = s0; s < s1; s += 64) {
+        const int id = id_of(s + lane);
+        const unsigned long long same = same_id(id, bits);
+        int at = 0;
+        if (id < a.G) at = count[w][id];  // every lane reads before the first one writes
+        __builtin_amdgcn_wave_barrier();
+        if (id < a.G) {
+            a.rows[at + __popcll(same & below)] = (int)(s + lane);
+            if ((same & below) == 0) count[w][id] = at + __popcll(same);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The weighted sum of a token's k slots: one wave per 256 columns of a token,
+// 16 bytes per lane and slot, four slots' loads in flight.
+// ---------------------------------------------------------------------------
+struct CombineArgs {
+    int T, k, N, E;
+    const int *ids;
+    const float *weights, *Y;
+    int64_t ldy, ldo;
+    float beta;
+    float *out;
+    int chunks;  // of 256 columns
+    int64_t units;
+};
+
+__device__ __forceinline__ f32x4u load4(const float *p, int left) {
+    f32x4u v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (left >= 4) {
+        v = *reinterpret_cast<const f32x4u *>(p);
+    } else {
+        if (left > 0) v.x = p[0];
+        if (left > 1) v.y = p[1];
+        if (left > 2) v.z = p[2];
+    }
+    return v;
+}
+__device__ __forceinline__ void store4(float *p, int left, f32x4u v) {
+    if (left >= 4) {
+        *reinterpret_cast<f32x4u *>(p) = v;
+    } else {
+        if (left > 0) p[0] = v.x;
+        if (left > 1) p[1] = v.y;
+        if (left > 2) p[2] = v.z;
+    }
+}
+// (element by element: no packed FP32 instructions)
+__device__ __forceinline__ f32x4u fma4(float s, f32x4u a, f32x4u c) {
+    f32x4u r;
+    r.x = fmaf(s, a.x, c.x);
+    r.y = fmaf(s, a.y, c.y);
+    r.z = fmaf(s, a.z, c.z);
+    r.w = fmaf(s, a.w, c.w);
+    return r;
+}
+
+__global__ void __launch_bounds__(256) combine(CombineArgs a) {
+    const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (unit >= a.units) return;
+    const int t = (int)(unit / a.chunks), chunk = (int)(unit - (int64_t)t * a.chunks);
+    const int c = chunk * 256 + 4 * (int)(threadIdx.x & 63);
+    const int left = a.N - c;
+    if (left <= 0) return;
+    const int64_t s0 = (int64_t)t * a.k;
+    f32x4u acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+        f32x4u y[4];
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = 0.0f;
+            y[j] = acc;
+            if (j0 + j < a.k) {
+                const int64_t s = s0 + j0 + j;
+                const bool there = a.ids == nullptr || (unsigned)a.ids[s] < (unsigned)a.E;
+                if (there) {
+                    w[j] = a.weights == nullptr ? 1.0f : a.weights[s];
+                    y[j] = load4(a.Y + s * a.ldy + c, left);
+                } else {
+                    y[j] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+            } else {
+                y[j] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc = fma4(w[j], y[j], acc);
+    }
+    float *out = a.out + (int64_t)t * a.ldo + c;
+    if (a.beta != 0.0f) acc = fma4(a.beta, load4(out, left), acc);
+    store4(out, left, acc);
+}
+
+// Its gradient: a workgroup per token, dout read once per eight slots.
+struct CombineGradArgs {
+    int T, k, N, E;
+    const int *ids;
+    const float *weights, *dout, *Y;
+    int64_t ldd, ldy, lddy;
+    float *dY, *dweights;
+};
+
+__global__ void __launch_bounds__(256) combine_grad(CombineGradArgs a) {
+    constexpr int J = 8;
+    __shared__ float part[4][J];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int t = blockIdx.x;
+    const float *dout = a.dout + (int64_t)t * a.ldd;
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+        const int nj = a.k - j0 < J ? a.k - j0 : J;
+        const int64_t s0 = (int64_t)t * a.k + j0;
+        float dot[J], wt[J];
+        bool there[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            dot[j] = 0.0f;
+            there[j] = j < nj && (a.ids == nullptr || (unsigned)a.ids[s0 + (j < nj ? j : 0)] < (unsigned)a.E);
+            wt[j] = !there[j] ? 0.0f : a.weights == nullptr ? 1.0f : a.weights[s0 + j];
+        }
+        for (int c = 4 * tid; c < a.N; c += 1024) {
+            const int left = a.N - c;
+            const f32x4u d = load4(dout + c, left);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (j >= nj) break;
+                if (a.dweights != nullptr && there[j]) {
+                    const f32x4u y = load4(a.Y + (s0 + j) * a.ldy + c, left);
+                    dot[j] = fmaf(d.x, y.x, fmaf(d.y, y.y, fmaf(d.z, y.z, fmaf(d.w, y.w, dot[j]))));
+                }
+                if (a.dY != nullptr) {
+                    f32x4u g = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (there[j]) {
+                        g.x = wt[j] * d.x;
+                        g.y = wt[j] * d.y;
+                        g.z = wt[j] * d.z;
+                        g.w = wt[j] * d.w;
+                    }
+                    store4(a.dY + (s0 + j) * a.lddy + c, left, g);
+                }
+            }
+        }
+        if (a.dweights == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float s = reduce<64>(dot[j], Add());
+            if (lane == 0) part[w][j] = s;
+        }
+        __syncthreads();
+        if (tid < nj) a.dweights[s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Products over groups of rows: what every form of them is given.
+// ---------------------------------------------------------------------------
+struct GroupedArgs {
+    int G, R;       // offsets NULL: one group of all R rows
+    int N, K;       // tn: C_g is M x N
+    int M;          // tn only
+    float alpha, beta;
+    const float *A, *B;
+    float *C;
+    int64_t lda, ldb, ldc, stride_b, stride_c;
+    int a_div, b_div, c_scatter;
+    const int *offsets, *rows;
+    // adapters: a factor per group, and the part of K (NN, NT), of N or of M
+    // (tn: C's columns or rows beyond it get no contribution) that a group has
+    const float *scales;
+    const int *ranks;
+    int rank_k, rank_n, rank_m;
+    int xcd_shift;  // log2 of the device's XCDs
+};
+
+__device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+__device__ __forceinline__ void group_range(const GroupedArgs &a, int g, int &p0, int &p1) {
+    p0 = 0;
+    p1 = a.R;
+    if (a.offsets != nullptr) {
+        p0 = clamp_to(a.offsets[g], 0, a.R);
+        p1 = clamp_to(a.offsets[g + 1], 0, a.R);
+    }
+}
+
+// The group and first row of a launch's t-th tile of `bm` rows, groups in
+// order, each taking ceil(rows / bm) tiles.  A wave looks at 64 groups at a
+// time (each lane one), so every wave of a workgroup finds it by itself.
+// False: there are fewer tiles.
+__device__ __forceinline__ bool find_tile(const GroupedArgs &a, int bm, int t, int &g, int &p0, int &p1) {
+    const int lane = threadIdx.x & 63;
+    const int groups = a.offsets != nullptr ? a.G : 1;
+    for (int base = 0; base < groups; base += 64) {
+        int lo = 0, hi = 0;
+        if (base + lane < groups) group_range(a, base + lane, lo, hi);
+        const int n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
+        }
+        const unsigned long long past = __ballot(upto > t);
+        if (past != 0) {
+            const int at = __ffsll((long long)past) - 1;
+            const int first = __builtin_amdgcn_readlane(upto - n, at);
+            g = base + at;
+            p0 = __builtin_amdgcn_readlane(lo, at) + (t - first) * bm;
+            p1 = __builtin_amdgcn_readlane(hi, at);
+            return true;
+        }
+        t -= __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+// place p's row of an operand: p itself, or rows[p] / div; -1: no such slot
+__device__ __forceinline__ int64_t row_of(const GroupedArgs &a, int p, int div) {
+    if (div == 0) return p;
+    const int s = a.rows[p];
+    if ((unsigned)s >= (unsigned)a.R) return -1;
+    return div == 1 ? s : s / div;
+}
+
+__device__ __forceinline__ float group_alpha(const GroupedArgs &a, int g) {
+    return a.scales != nullptr ? a.alpha * a.scales[g] : a.alpha;
+}
+__device__ __forceinline__ int group_rank(const GroupedArgs &a, int g, int whole) {
+    return a.ranks != nullptr ? clamp_to(a.ranks[g], 0, whole) : whole;
+}
+
+// The simplest form, for operands that the fast ones do not take (offsets
+// beyond 32 bits): 32 x 32 of C per workgroup, 64-bit addresses, every access
+// checked.
+template <bool TRANS_B>
+__global__ void __launch_bounds__(256) grouped_simple(GroupedArgs a) {
+    constexpr int T = 32;
+    __shared__ float As[T][T + 1], Bs[T][T + 1];
+    const int ncol = (a.N + T - 1) / T;
+    const int n0 = (int)(blockIdx.x % ncol) * T;
+    int g, p0, p1;
+    if (!find_tile(a, T, (int)(blockIdx.x / ncol), g, p0, p1)) return;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const float *B = a.B + (int64_t)g * a.stride_b;
+    const int K = a.rank_k ? group_rank(a, g, a.K) : a.K;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < K; k0 += T) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty + 8 * i;
+            const int p = p0 + r;
+            const int64_t ar = p < p1 ? row_of(a, p, a.a_div) : -1;
+            As[r][tx] = ar >= 0 && k0 + tx < K ? a.A[ar * a.lda + k0 + tx] : 0.0f;
+            const int bk = TRANS_B ? k0 + tx : k0 + r, bn = TRANS_B ? n0 + r : n0 + tx;
+            const float b = bk < K && bn < a.N ? B[TRANS_B ? (int64_t)bn * a.ldb + bk : (int64_t)bk * a.ldb + bn] : 0.0f;
+            if (TRANS_B) Bs[tx][r] = b;
+            else Bs[r][tx] = b;
+        }
+        __syncthreads();
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(As[ty + 8 * i][k], Bs[k][tx], acc[i]);
+        __syncthreads();
+    }
+    const float al = group_alpha(a, g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = p0 + ty + 8 * i;
+        if (p >= p1 || n0 + tx >= a.N) continue;
+        const int64_t cr = row_of(a, p, a.c_scatter);
+        if (cr < 0) continue;
+        float *q = a.C + cr * a.ldc + n0 + tx;
+        *q = a.beta != 0.0f ? fmaf(a.beta, *q, al * acc[i]) : al * acc[i];
+    }
+}
+
+__global__ void __launch_bounds__(256) grouped_tn_simple(GroupedArgs a) {
+    constexpr int T = 32;
+    __shared__ float As[T][T + 1], Bs[T][T + 1];
+    const int nm = (a.M + T - 1) / T, nn = (a.N + T - 1) / T;
+    const int g = (int)(blockIdx.x / ((int64_t)nm * nn));
+    const int rest = (int)(blockIdx.x - (int64_t)g * nm * nn);
+    const int m0 = rest / nn * T, n0 = rest % nn * T;
+    int p0, p1;
+    group_range(a, g, p0, p1);
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q0 = p0; q0 < p1; q0 += T) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty + 8 * i, p = q0 + r;
+            const int64_t ar = p < p1 ? row_of(a, p, a.a_div) : -1;
+            const int64_t br = p < p1 ? row_of(a, p, a.b_div) : -1;
+            As[r][tx] = ar >= 0 && br >= 0 && m0 + tx < a.M ? a.A[ar * a.lda + m0 + tx] : 0.0f;
+            Bs[r][tx] = ar >= 0 && br >= 0 && n0 + tx < a.N ? a.B[br * a.ldb + n0 + tx] : 0.0f;
+        }
+        __syncthreads();
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(As[k][ty + 8 * i], Bs[k][tx], acc[i]);
+        __syncthreads();
+    }
+    const float al = group_alpha(a, g);
+    const int mr = a.rank_m ? group_rank(a, g, a.M) : a.M, nr = a.rank_n ? group_rank(a, g, a.N) : a.N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ty + 8 * i, n = n0 + tx;
+        if (m >= a.M || n >= a.N) continue;
+        float *q = a.C + (int64_t)g * a.stride_c + (int64_t)m * a.ldc + n;
+        const float v = m < mr && n < nr ? al * acc[i] : 0.0f;
+        *q = a.beta != 0.0f ? fmaf(a.beta, *q, v) : v;
+    }
+}
+
+}  // namespace rowk

@@ -1193,6 +1193,17 @@ int sgemm_operands_load16(const float *A, int lda, const float *B, int ldb, cons
 }
 
 const char *sgemm_status_string(int status) {
+    // the calls in rows.hip number an argument -(100 + its position)
+    static const char *const kArguments[] = {
+#define ARGUMENT(n) "invalid argument " #n
+        ARGUMENT(1),  ARGUMENT(2),  ARGUMENT(3),  ARGUMENT(4),  ARGUMENT(5),  ARGUMENT(6),  ARGUMENT(7),  ARGUMENT(8),
+        ARGUMENT(9),  ARGUMENT(10), ARGUMENT(11), ARGUMENT(12), ARGUMENT(13), ARGUMENT(14), ARGUMENT(15), ARGUMENT(16),
+        ARGUMENT(17), ARGUMENT(18), ARGUMENT(19), ARGUMENT(20), ARGUMENT(21), ARGUMENT(22), ARGUMENT(23), ARGUMENT(24),
+        ARGUMENT(25), ARGUMENT(26), ARGUMENT(27), ARGUMENT(28), ARGUMENT(29), ARGUMENT(30), ARGUMENT(31), ARGUMENT(32)};
+#undef ARGUMENT
+    constexpr int kCount = sizeof kArguments / sizeof kArguments[0];
+    if (status < SGEMM_ERR_ARGUMENT && status >= SGEMM_ERR_ARGUMENT - kCount)
+        return kArguments[SGEMM_ERR_ARGUMENT - status - 1];
     switch (status) {
         case SGEMM_OK: return "success";
         case -1: return "invalid argument: M < 0";

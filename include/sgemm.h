@@ -381,6 +381,157 @@ const char *sgemm_status_string(int status);
  * For reports that state the peak they divide by. */
 int sgemm_device_fp32_peak(int device, int *compute_units, int *clock_khz, double *tflops);
 
+/* ==== products whose B is picked row by row ==================================
+ * A layer of experts, or a projection with low-rank adapters, is a product
+ * whose rows do not share one B.  The calls below are its parts, all FP32
+ * like sgemm() (operands, products and sums; the router's scores in 64 bits
+ * where their order is decided by sums of them), all asynchronous on `stream`,
+ * with caller-owned device pointers, no allocation and results that are the
+ * same run to run.  A layer of experts is
+ *
+ *   sgemm_route        scores of T tokens -> ids (T x k) and weights (T x k)
+ *   sgemm_group_rows   ids -> the slots sorted by expert: offsets, rows
+ *   sgemm_grouped      every slot's row times its expert's B
+ *   sgemm_combine      the weighted sum of each token's k slots
+ *
+ * and back sgemm_combine_grad, sgemm_grouped (B transposed), sgemm_grouped_tn
+ * (the experts' gradients) and sgemm_route_grad.  sgemm_adapters() is a shared
+ * projection with a low-rank adapter per row.  A slot is one (token, choice)
+ * pair, number t * k + j.
+ *
+ * Return value.  0; SGEMM_ERR_WORKSPACE; SGEMM_ERR_TOO_LARGE (a grid beyond
+ * one launch); a positive hipError_t; or -(100 + position) for an invalid
+ * argument, numbered by its position in that call from 1 (-101 the first).
+ * Checks run before any HIP call and the first bad argument wins.  Sizes of
+ * zero are allowed where nothing is said: such a call launches nothing that
+ * would read or write through a pointer of an empty operand. */
+#define SGEMM_ERR_ARGUMENT (-100) /* minus the argument's position in its call */
+
+#define SGEMM_SCORE_SOFTMAX 0 /* s = exp(l) / sum exp(l) over the row */
+#define SGEMM_SCORE_SIGMOID 1 /* s = 1 / (1 + exp(-l)) */
+#define SGEMM_ROUTE_MAX_EXPERTS 1024
+#define SGEMM_ROUTE_MAX_K 64
+#define SGEMM_MAX_GROUPS 4096
+#define SGEMM_MAX_RANK 256
+
+/* The k experts of each token and their weights.  Row t of `logits` (T x E,
+ * leading dimension ldl) gives the scores s (`scoring`, SGEMM_SCORE_*).  The
+ * choice goes by key = s + bias[e] (bias: E floats or NULL; it takes no part in
+ * the weights).  With groups > 1 the E experts are `groups` runs of E / groups;
+ * a run is worth the sum of its group_best (1 or 2) highest keys, and only the
+ * top_groups runs worth most are chosen from.  The k highest keys are taken in
+ * falling order, ties (of runs too) to the lowest index.  weights[t * k + j] is
+ * the chosen score, divided by the sum of the token's k when renorm != 0 (0
+ * when that sum is 0), times `scale`.
+ *   Without a bias and with group_best 1 the order is that of the logits
+ * themselves, else keys are computed and compared in 64 bits.
+ *   A logit of -infinity masks its expert and a NaN logit or key is never
+ * chosen either; a choice left unfilled gets id -1 and weight 0 (all k where
+ * the row is masked throughout).  A row that holds a NaN logit gets NaN
+ * weights.  Logits of +infinity share a softmax row equally.
+ * 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E, 1 <= top_groups
+ * <= groups.  ids and weights are T x k without padding. */
+int sgemm_route(int T, int E, int k, int scoring, const float *logits, int ldl, const float *bias,
+                int groups, int top_groups, int group_best, int renorm, float scale, int *ids,
+                float *weights, hipStream_t stream);
+
+/* dlogits (T x E, leading dimension lddl, written whole) of the loss whose
+ * gradient by the weights is dweights (T x k), for the choice `ids` that
+ * sgemm_route() made (ids < 0 or >= E: nothing was chosen, dweights is not
+ * read).  With d_j = scale dweights_j, first, when renorm != 0,
+ * d_j <- (d_j - sum_i d_i s_i / S) / S over the chosen, S their sum of scores
+ * (d = 0 when S is 0); then softmax: dl_e = s_e (d_e - sum_i d_i s_i), sigmoid:
+ * dl_e = d_e s_e (1 - s_e), d_e = 0 for experts not chosen.  The choice itself
+ * and the bias have no gradient.  The ids of a row are distinct. */
+int sgemm_route_grad(int T, int E, int k, int scoring, const float *logits, int ldl, int renorm, float scale,
+                     const int *ids, const float *dweights, float *dlogits, int lddl, hipStream_t stream);
+
+/* Sorts R slots by group: offsets[g] (G + 1 ints) is where group g begins and
+ * offsets[G] the number of slots placed; rows[p] (R ints) is the slot at place
+ * p, slots of one group in rising order.  A slot whose id is outside [0, G) is
+ * placed nowhere; rows from offsets[G] on stay as they were.  1 <= G <= 4096.
+ * Workspace: at least sgemm_group_rows_workspace_size() bytes (0 for small R;
+ * then it may be NULL), 256-byte aligned, any contents; calls that share one
+ * must not overlap in time. */
+int sgemm_group_rows(int R, int G, const int *ids, int *offsets, int *rows, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+size_t sgemm_group_rows_workspace_size(int R, int G);
+
+/* Every placed slot's row times its group's B (K x N; N x K with trans_b != 0):
+ *   C[c] = alpha * A[a] * B_g + beta * C[c],  offsets[g] <= p < offsets[g + 1],
+ * B_g at B + g * stride_b with leading dimension ldb.  A's row a is p when
+ * a_div is 0, else rows[p] / a_div (1: a row per slot; k: a row per token).
+ * C's row c is p, or rows[p] when c_scatter != 0.  A's rows are R (a_div <= 1)
+ * or ceil(R / a_div), C's are R.  Rows of C that no placed slot names are not
+ * touched; beta == 0 does not read C, alpha == 0 or K == 0 read neither A nor
+ * B.  offsets and rows are device arrays as sgemm_group_rows() writes them
+ * (rows may be NULL when neither a_div nor c_scatter uses it; a value outside
+ * [0, R) is skipped, and each slot may be there once).  Offsets outside [0, R]
+ * are taken as the nearer end.  B's groups may overlap (stride_b 0 is one B for
+ * all).  Any 4-byte alignment and any leading dimensions; small ones (rows of
+ * A and a group's B within 4 GiB) take the fast kernels. */
+int sgemm_grouped(int G, int R, int N, int K, float alpha, const float *A, int lda, int a_div, const float *B,
+                  int ldb, long long stride_b, int trans_b, float beta, float *C, int ldc, int c_scatter,
+                  const int *offsets, const int *rows, hipStream_t stream);
+
+/* The gradient of sgemm_grouped() by B: each group's sum of outer products,
+ *   C_g = alpha * sum_p A[a]^T B[b] + beta * C_g,  offsets[g] <= p < offsets[g + 1],
+ * C_g (M x N) at C + g * stride_c with leading dimension ldc; A's rows hold M
+ * columns and B's N; a and b are p (div 0) or rows[p] / div as above.  Every
+ * C_g is written: an empty group's becomes beta * C_g.  The C_g must not
+ * overlap. */
+int sgemm_grouped_tn(int G, int R, int M, int N, float alpha, const float *A, int lda, int a_div, const float *B,
+                     int ldb, int b_div, float beta, float *C, int ldc, long long stride_c, const int *offsets,
+                     const int *rows, hipStream_t stream);
+
+/* out[t] = sum_j weights[t * k + j] * Y[t * k + j] + beta * out[t] for T rows of
+ * N columns, over the slots whose id is in [0, E), in rising j (rows of Y of
+ * other slots are not read).  ids NULL: all slots; weights NULL: all 1.
+ * 1 <= k <= 64. */
+int sgemm_combine(int T, int k, int N, int E, const int *ids, const float *weights, const float *Y, int ldy,
+                  float beta, float *out, int ldo, hipStream_t stream);
+
+/* Back through sgemm_combine() from dout (T x N): dY[t * k + j] = weights[t * k
+ * + j] * dout[t] and dweights[t * k + j] = <dout[t], Y[t * k + j]>, both 0 for
+ * a slot whose id is outside [0, E).  dY or dweights may be NULL (not wanted);
+ * Y is read for dweights only, weights for dY only (NULL: all 1). */
+int sgemm_combine_grad(int T, int k, int N, int E, const int *ids, const float *weights, const float *dout,
+                       int ldd, const float *Y, int ldy, float *dY, int lddy, float *dweights,
+                       hipStream_t stream);
+
+/* A shared projection with a low-rank adapter per row:
+ *   C[m] = alpha * (A[m] B + scales[g] * (A[m] U_g) V_g) + beta * C[m],  g = ids[m],
+ * U_g (K x ranks[g]) at U + g * stride_u with leading dimension ldu, V_g
+ * (ranks[g] x N) at V + g * stride_v with leading dimension ldv.  ids[m] outside
+ * [0, G): no adapter.  ranks NULL: all `rank`; else ranks[g] is taken within
+ * [0, rank], and what lies in U's columns and V's rows beyond it is not used.
+ * scales NULL: all 1.  1 <= G <= 4096, 1 <= rank <= 256.  beta == 0 does not
+ * read C; alpha == 0 or K == 0: C = beta * C.
+ * Workspace: at least sgemm_adapters_workspace_size() bytes, 256-byte aligned,
+ * any contents; calls that share one must not overlap in time. */
+int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
+                   float beta, float *C, int ldc, int G, int rank, const int *ids, const int *ranks,
+                   const float *scales, const float *U, int ldu, long long stride_u, const float *V, int ldv,
+                   long long stride_v, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t sgemm_adapters_workspace_size(int M, int N, int K, int G, int rank);
+
+/* Back through sgemm_adapters() from dC (M x N):
+ *   dA[m] = alpha * (dC[m] B^T + scales[g] * (dC[m] V_g^T) U_g^T)
+ *   dU_g  = alpha * scales[g] * sum_m A[m]^T (dC[m] V_g^T) + beta * dU_g
+ *   dV_g  = alpha * scales[g] * sum_m (A[m] U_g)^T dC[m] + beta * dV_g
+ * over the rows m of group g.  dA (M x K) is written; dU_g (K x rank) and dV_g
+ * (rank x N) are written whole for every g, with no contribution beyond
+ * ranks[g] and for adapters no row uses.  dA, or dU and dV together, may be
+ * NULL (not wanted).  Workspace as above, at least
+ * sgemm_adapters_grad_workspace_size() bytes. */
+int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
+                        const float *dC, int lddc, int G, int rank, const int *ids, const int *ranks,
+                        const float *scales, const float *U, int ldu, long long stride_u, const float *V,
+                        int ldv, long long stride_v, float beta, float *dA, int ldda, float *dU, int lddu,
+                        long long stride_du, float *dV, int lddv, long long stride_dv, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank);
+
 #ifdef __cplusplus
 }
 #endif
