@@ -452,78 +452,109 @@ def variants():
 # These calls take index tensors beside the matrices, so a tensor's type, place
 # and extent are looked at before its address goes to a kernel: float32 (ids and
 # offsets int32) on the current device, long enough for the sizes given.  An
-# ``int`` address is passed on as it is.
-class _Tensors:
-    """The address of each argument of one call."""
-    __slots__ = ("where", "device")
+# ``int`` address is passed on as it is.  A call is a few microseconds of kernel
+# where it serves single tokens, so the usual case (a contiguous tensor, torch's
+# current stream) takes the shortest way here: four queries per tensor, and the
+# stream's handle without a Stream object around it.
+_F32 = _I32 = None  # torch's types, once it is imported (_begin)
+_raw_stream = None
 
-    def __init__(self, where):
+
+def _begin(stream):
+    """The current device (-1: no GPU in use) and the stream's handle."""
+    global _F32, _I32, _raw_stream
+    if _F32 is None:
         import torch
-        self.where = where
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _I32, _F32 = torch.int32, torch.float32
+    import torch
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    if stream is None:
+        if device >= 0 and _raw_stream is not None:
+            return device, _raw_stream(device)
+        stream = torch.cuda.current_stream()
+        return torch.cuda.current_device(), stream.cuda_stream
+    if isinstance(stream, int):
+        return device, stream
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, not on the current device cuda:{device}")
+    return device, stream.cuda_stream
 
-    def _address(self, x, what, kind, need, inner=None):
-        if x is None or isinstance(x, int):
-            return x
-        p = _ptr(x)
-        if str(x.dtype) != kind:
-            raise TypeError(f"{self.where}: {what} has type {x.dtype}, not {kind}")
-        if x.get_device() != self.device:
-            raise ValueError(f"{self.where}: {what} is on {x.device}, not on the current device cuda:{self.device}")
-        if not x.is_contiguous():
-            if inner is None or (x.dim() and x.stride(-1) != 1 and x.shape[-1] > 1):
-                raise ValueError(f"{self.where}: {what} must be laid out "
-                                 + ("without gaps" if inner is None else "with its last dimension contiguous"))
-            have = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
-        else:
-            have = x.numel()
-        if have < need:
-            raise ValueError(f"{self.where}: {what} holds {have} elements, {need} are needed")
+
+def _address(what, x, kind, need, device, rows_apart=False):
+    """The address of a tensor of at least ``need`` elements of type ``kind``."""
+    if x is None or x.__class__ is int:
+        return x
+    if (getattr(x, "dtype", None) is kind and 0 <= device == x.get_device() and x.is_contiguous()
+            and x.numel() >= need):
+        return x.data_ptr()
+    p = _ptr(x)
+    if isinstance(x, int):
         return p
+    if x.dtype is not kind:
+        raise TypeError(f"{what} has type {x.dtype}, not {kind}")
+    if x.get_device() != device:
+        raise ValueError(f"{what} is on {x.device}, not on the current device cuda:{device}")
+    if x.is_contiguous():
+        have = x.numel()
+    elif rows_apart and x.stride(-1) == 1:  # a view of wider rows: what its storage holds
+        have = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+    else:
+        raise ValueError(f"{what} must be laid out "
+                         + ("with its last dimension contiguous" if rows_apart else "without gaps"))
+    if have < need:
+        raise ValueError(f"{what} holds {have} elements, {need} are needed")
+    return p
 
-    def matrix(self, x, what, rows, cols, ld, groups=1, stride=0):
-        """groups matrices of rows x cols, rows ld apart and matrices stride apart."""
-        some = groups > 0 and rows > 0 and cols > 0
-        need = (groups - 1) * stride + (rows - 1) * ld + cols if some else 0
-        return self._address(x, what, "torch.float32", need, cols)
 
-    def floats(self, x, what, n):
-        return self._address(x, what, "torch.float32", n)
+def _matrix(what, x, rows, cols, ld, device, groups=1, stride=0):
+    """groups matrices of rows x cols, rows ld apart and matrices stride apart."""
+    need = (groups - 1) * stride + (rows - 1) * ld + cols if groups > 0 and rows > 0 and cols > 0 else 0
+    return _address(what, x, _F32, need, device, True)
 
-    def ints(self, x, what, n):
-        return self._address(x, what, "torch.int32", n)
 
-    def space(self, x, nbytes):
-        if x is None or isinstance(x, int):
-            return x, int(nbytes or 0)
-        if not x.is_contiguous():
-            raise ValueError(f"{self.where}: workspace must be laid out without gaps")
-        have = x.numel() * x.element_size()
-        if nbytes is not None and nbytes > have:
-            raise ValueError(f"{self.where}: workspace holds {have} bytes, not {nbytes}")
-        if x.is_cuda and x.get_device() != self.device:
-            raise ValueError(f"{self.where}: workspace is on {x.device}, not on the current device cuda:{self.device}")
-        return _ptr(x), int(have if nbytes is None else nbytes)
+def _floats(what, x, n, device):
+    return _address(what, x, _F32, n, device)
+
+
+def _ints(what, x, n, device):
+    return _address(what, x, _I32, n, device)
+
+
+def _space(x, nbytes, device):
+    if x is None or isinstance(x, int):
+        return x, int(nbytes or 0)
+    p = _ptr(x)
+    if not x.is_contiguous():
+        raise ValueError("workspace must be laid out without gaps")
+    if x.get_device() != device:
+        raise ValueError(f"workspace is on {x.device}, not on the current device cuda:{device}")
+    have = x.numel() * x.element_size()
+    if nbytes is None:
+        return p, have
+    if nbytes > have:
+        raise ValueError(f"workspace holds {have} bytes, not {nbytes}")
+    return p, int(nbytes)
 
 
 def sgemm_route(T, E, k, scoring, logits, ldl, bias, groups, top_groups, group_best, renorm, scale, ids,
                 weights, stream=None, check=True):
     """The k experts of each token (``ids``, T x k int32) and their ``weights`` (T x k)."""
-    t = _Tensors("sgemm_route")
-    return _ret(load_library().sgemm_route(
-        T, E, k, scoring, t.matrix(logits, "logits", T, E, ldl), ldl, t.floats(bias, "bias", E), groups, top_groups,
-        group_best, 1 if renorm else 0, scale, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
-        _stream(stream)), "sgemm_route", check)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_route(
+        T, E, k, scoring, _matrix("logits", logits, T, E, ldl, d), ldl, _floats("bias", bias, E, d), groups,
+        top_groups, group_best, 1 if renorm else 0, scale, _ints("ids", ids, T * k, d),
+        _floats("weights", weights, T * k, d), s), "sgemm_route", check)
 
 
 def sgemm_route_grad(T, E, k, scoring, logits, ldl, renorm, scale, ids, dweights, dlogits, lddl, stream=None,
                      check=True):
     """``dlogits`` (T x E) from the gradient of sgemm_route()'s weights."""
-    t = _Tensors("sgemm_route_grad")
-    return _ret(load_library().sgemm_route_grad(
-        T, E, k, scoring, t.matrix(logits, "logits", T, E, ldl), ldl, 1 if renorm else 0, scale,
-        t.ints(ids, "ids", T * k), t.floats(dweights, "dweights", T * k), t.matrix(dlogits, "dlogits", T, E, lddl),
-        lddl, _stream(stream)), "sgemm_route_grad", check)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_route_grad(
+        T, E, k, scoring, _matrix("logits", logits, T, E, ldl, d), ldl, 1 if renorm else 0, scale,
+        _ints("ids", ids, T * k, d), _floats("dweights", dweights, T * k, d),
+        _matrix("dlogits", dlogits, T, E, lddl, d), lddl, s), "sgemm_route_grad", check)
 
 
 def sgemm_group_rows_workspace_size(R, G) -> int:
@@ -532,11 +563,11 @@ def sgemm_group_rows_workspace_size(R, G) -> int:
 
 def sgemm_group_rows(R, G, ids, offsets, rows, workspace=None, workspace_bytes=None, stream=None, check=True):
     """The R slots sorted by group: ``offsets`` (G + 1 int32) and ``rows`` (R int32)."""
-    t = _Tensors("sgemm_group_rows")
-    ws, nbytes = t.space(workspace, workspace_bytes)
-    return _ret(load_library().sgemm_group_rows(
-        R, G, t.ints(ids, "ids", R), t.ints(offsets, "offsets", G + 1), t.ints(rows, "rows", R), ws, nbytes,
-        _stream(stream)), "sgemm_group_rows", check)
+    d, s = _begin(stream)
+    ws, nbytes = _space(workspace, workspace_bytes, d)
+    return _ret((_lib or load_library()).sgemm_group_rows(
+        R, G, _ints("ids", ids, R, d), _ints("offsets", offsets, G + 1, d), _ints("rows", rows, R, d), ws, nbytes, s),
+        "sgemm_group_rows", check)
 
 
 def _rows(R, div):
@@ -546,42 +577,41 @@ def _rows(R, div):
 def sgemm_grouped(G, R, N, K, alpha, A, lda, a_div, B, ldb, stride_b, trans_b, beta, C, ldc, c_scatter, offsets,
                   rows, stream=None, check=True):
     """Every placed slot's row of ``A`` times its group's ``B`` (transposed with ``trans_b``)."""
-    t = _Tensors("sgemm_grouped")
-    b = (N, K) if trans_b else (K, N)
-    return _ret(load_library().sgemm_grouped(
-        G, R, N, K, alpha, t.matrix(A, "A", _rows(R, a_div), K, lda), lda, a_div,
-        t.matrix(B, "B", *b, ldb, G, stride_b), ldb, stride_b, 1 if trans_b else 0, beta,
-        t.matrix(C, "C", R, N, ldc), ldc, 1 if c_scatter else 0, t.ints(offsets, "offsets", G + 1),
-        t.ints(rows, "rows", R), _stream(stream)), "sgemm_grouped", check)
+    d, s = _begin(stream)
+    b_rows, b_cols = (N, K) if trans_b else (K, N)
+    return _ret((_lib or load_library()).sgemm_grouped(
+        G, R, N, K, alpha, _matrix("A", A, _rows(R, a_div), K, lda, d), lda, a_div,
+        _matrix("B", B, b_rows, b_cols, ldb, d, G, stride_b), ldb, stride_b, 1 if trans_b else 0, beta,
+        _matrix("C", C, R, N, ldc, d), ldc, 1 if c_scatter else 0, _ints("offsets", offsets, G + 1, d),
+        _ints("rows", rows, R, d), s), "sgemm_grouped", check)
 
 
 def sgemm_grouped_tn(G, R, M, N, alpha, A, lda, a_div, B, ldb, b_div, beta, C, ldc, stride_c, offsets, rows,
                      stream=None, check=True):
     """Each group's sum over its slots of the outer products of their rows of ``A`` and ``B``."""
-    t = _Tensors("sgemm_grouped_tn")
-    return _ret(load_library().sgemm_grouped_tn(
-        G, R, M, N, alpha, t.matrix(A, "A", _rows(R, a_div), M, lda), lda, a_div,
-        t.matrix(B, "B", _rows(R, b_div), N, ldb), ldb, b_div, beta, t.matrix(C, "C", M, N, ldc, G, stride_c), ldc,
-        stride_c, t.ints(offsets, "offsets", G + 1), t.ints(rows, "rows", R), _stream(stream)),
-        "sgemm_grouped_tn", check)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_grouped_tn(
+        G, R, M, N, alpha, _matrix("A", A, _rows(R, a_div), M, lda, d), lda, a_div,
+        _matrix("B", B, _rows(R, b_div), N, ldb, d), ldb, b_div, beta, _matrix("C", C, M, N, ldc, d, G, stride_c),
+        ldc, stride_c, _ints("offsets", offsets, G + 1, d), _ints("rows", rows, R, d), s), "sgemm_grouped_tn", check)
 
 
 def sgemm_combine(T, k, N, E, ids, weights, Y, ldy, beta, out, ldo, stream=None, check=True):
     """``out[t]`` = the weighted sum of token t's k rows of ``Y``, plus ``beta * out[t]``."""
-    t = _Tensors("sgemm_combine")
-    return _ret(load_library().sgemm_combine(
-        T, k, N, E, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
-        t.matrix(Y, "Y", T * k, N, ldy), ldy, beta, t.matrix(out, "out", T, N, ldo), ldo, _stream(stream)),
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_combine(
+        T, k, N, E, _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
+        _matrix("Y", Y, T * k, N, ldy, d), ldy, beta, _matrix("out", out, T, N, ldo, d), ldo, s),
         "sgemm_combine", check)
 
 
 def sgemm_combine_grad(T, k, N, E, ids, weights, dout, ldd, Y, ldy, dY, lddy, dweights, stream=None, check=True):
     """``dY`` (T * k x N) and ``dweights`` (T x k) from ``dout``; either may be None."""
-    t = _Tensors("sgemm_combine_grad")
-    return _ret(load_library().sgemm_combine_grad(
-        T, k, N, E, t.ints(ids, "ids", T * k), t.floats(weights, "weights", T * k),
-        t.matrix(dout, "dout", T, N, ldd), ldd, t.matrix(Y, "Y", T * k, N, ldy), ldy,
-        t.matrix(dY, "dY", T * k, N, lddy), lddy, t.floats(dweights, "dweights", T * k), _stream(stream)),
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_combine_grad(
+        T, k, N, E, _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
+        _matrix("dout", dout, T, N, ldd, d), ldd, _matrix("Y", Y, T * k, N, ldy, d), ldy,
+        _matrix("dY", dY, T * k, N, lddy, d), lddy, _floats("dweights", dweights, T * k, d), s),
         "sgemm_combine_grad", check)
 
 
@@ -596,27 +626,26 @@ def sgemm_adapters_grad_workspace_size(M, N, K, G, rank) -> int:
 def sgemm_adapters(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, G, rank, ids, ranks, scales, U, ldu, stride_u, V,
                    ldv, stride_v, workspace, workspace_bytes=None, stream=None, check=True):
     """``C[m] = alpha * (A[m] B + scales[g] (A[m] U_g) V_g) + beta * C[m]`` with g = ``ids[m]``."""
-    t = _Tensors("sgemm_adapters")
-    ws, nbytes = t.space(workspace, workspace_bytes)
-    return _ret(load_library().sgemm_adapters(
-        M, N, K, alpha, t.matrix(A, "A", M, K, lda), lda, t.matrix(B, "B", K, N, ldb), ldb, beta,
-        t.matrix(C, "C", M, N, ldc), ldc, G, rank, t.ints(ids, "ids", M), t.ints(ranks, "ranks", G),
-        t.floats(scales, "scales", G), t.matrix(U, "U", K, rank, ldu, G, stride_u), ldu, stride_u,
-        t.matrix(V, "V", rank, N, ldv, G, stride_v), ldv, stride_v, ws, nbytes, _stream(stream)),
-        "sgemm_adapters", check)
+    d, s = _begin(stream)
+    ws, nbytes = _space(workspace, workspace_bytes, d)
+    return _ret((_lib or load_library()).sgemm_adapters(
+        M, N, K, alpha, _matrix("A", A, M, K, lda, d), lda, _matrix("B", B, K, N, ldb, d), ldb, beta,
+        _matrix("C", C, M, N, ldc, d), ldc, G, rank, _ints("ids", ids, M, d), _ints("ranks", ranks, G, d),
+        _floats("scales", scales, G, d), _matrix("U", U, K, rank, ldu, d, G, stride_u), ldu, stride_u,
+        _matrix("V", V, rank, N, ldv, d, G, stride_v), ldv, stride_v, ws, nbytes, s), "sgemm_adapters", check)
 
 
 def sgemm_adapters_grad(M, N, K, alpha, A, lda, B, ldb, dC, lddc, G, rank, ids, ranks, scales, U, ldu, stride_u, V,
                         ldv, stride_v, beta, dA, ldda, dU, lddu, stride_du, dV, lddv, stride_dv, workspace,
                         workspace_bytes=None, stream=None, check=True):
     """The gradients of sgemm_adapters() by A (``dA``) and by the adapters (``dU``, ``dV``)."""
-    t = _Tensors("sgemm_adapters_grad")
-    ws, nbytes = t.space(workspace, workspace_bytes)
-    return _ret(load_library().sgemm_adapters_grad(
-        M, N, K, alpha, t.matrix(A, "A", M, K, lda), lda, t.matrix(B, "B", K, N, ldb), ldb,
-        t.matrix(dC, "dC", M, N, lddc), lddc, G, rank, t.ints(ids, "ids", M), t.ints(ranks, "ranks", G),
-        t.floats(scales, "scales", G), t.matrix(U, "U", K, rank, ldu, G, stride_u), ldu, stride_u,
-        t.matrix(V, "V", rank, N, ldv, G, stride_v), ldv, stride_v, beta, t.matrix(dA, "dA", M, K, ldda), ldda,
-        t.matrix(dU, "dU", K, rank, lddu, G, stride_du), lddu, stride_du,
-        t.matrix(dV, "dV", rank, N, lddv, G, stride_dv), lddv, stride_dv, ws, nbytes, _stream(stream)),
+    d, s = _begin(stream)
+    ws, nbytes = _space(workspace, workspace_bytes, d)
+    return _ret((_lib or load_library()).sgemm_adapters_grad(
+        M, N, K, alpha, _matrix("A", A, M, K, lda, d), lda, _matrix("B", B, K, N, ldb, d), ldb,
+        _matrix("dC", dC, M, N, lddc, d), lddc, G, rank, _ints("ids", ids, M, d), _ints("ranks", ranks, G, d),
+        _floats("scales", scales, G, d), _matrix("U", U, K, rank, ldu, d, G, stride_u), ldu, stride_u,
+        _matrix("V", V, rank, N, ldv, d, G, stride_v), ldv, stride_v, beta,
+        _matrix("dA", dA, M, K, ldda, d), ldda, _matrix("dU", dU, K, rank, lddu, d, G, stride_du), lddu, stride_du,
+        _matrix("dV", dV, rank, N, lddv, d, G, stride_dv), lddv, stride_dv, ws, nbytes, s),
         "sgemm_adapters_grad", check)

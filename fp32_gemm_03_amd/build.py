@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "rows.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "sgemm_kernels.hpp"), os.path.join(CSRC, "rows_kernels.hpp"),
-                     os.path.join(INCLUDE, "sgemm.h")]
+                     os.path.join(CSRC, "grouped_kernels.hpp"), os.path.join(INCLUDE, "sgemm.h")]
 LIBRARY = os.path.join(PKG, "libsgemm_mi355x.so")
 ARCH = "gfx950"
 
@@ -67,9 +67,10 @@ def _llvm_tool(name: str) -> str:
     return path
 
 
-def kernel_resources(library: str = LIBRARY) -> dict:
+def kernel_resources(library: str = LIBRARY, source: int = 0) -> dict:
     """``{kernel symbol: {field: int}}`` from the AMDGPU metadata of the
-    library's gfx950 code object: ``vgpr_count``, ``agpr_count``,
+    library's gfx950 code object of ``SOURCES[source]`` (each source file has
+    its own, one after the other): ``vgpr_count``, ``agpr_count``,
     ``sgpr_count``, ``vgpr_spill_count``, ``sgpr_spill_count``,
     ``private_segment_fixed_size`` (scratch bytes per lane) and
     ``group_segment_fixed_size`` (LDS bytes).  The code object is the one this
@@ -81,6 +82,10 @@ def kernel_resources(library: str = LIBRARY) -> dict:
         co = os.path.join(d, "gfx950.co")
         subprocess.run([_llvm_tool("llvm-objcopy"), "--dump-section=.hip_fatbin=" + fat, library,
                         os.path.join(d, "copy.so")], check=True, capture_output=True)
+        with open(fat, "rb") as f:
+            bundles = f.read().split(b"__CLANG_OFFLOAD_BUNDLE__")[1:]
+        with open(fat, "wb") as f:
+            f.write(b"__CLANG_OFFLOAD_BUNDLE__" + bundles[source])
         subprocess.run([_llvm_tool("clang-offload-bundler"), "--type=o", "--unbundle",
                         "--targets=hipv4-amdgcn-amd-amdhsa--" + ARCH, "--input=" + fat,
                         "--output=" + co], check=True, capture_output=True)
@@ -129,7 +134,9 @@ def main():
                     help="print each kernel's registers, spills, scratch and LDS from the built library")
     args = ap.parse_args()
     if args.resources:
-        res = kernel_resources()
+        res = {}
+        for source in range(len(SOURCES)):
+            res.update(kernel_resources(source=source))
         for name, pretty in zip(res, demangle(res)):
             r = res[name]
             print(f"{r.get('private_segment_fixed_size', -1):5d} B scratch  "

@@ -6,6 +6,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include "grouped_kernels.hpp"
 #include "rows_kernels.hpp"
 
 namespace {
@@ -55,21 +56,90 @@ long long row_tiles(const GroupedArgs &a, int bm) {
     return a.R / bm + (a.offsets == nullptr ? 1 : (a.G < a.R ? a.G : a.R));
 }
 
+typedef void (*GroupedFn)(GroupedArgs);
+
+// The fast kernels' byte offsets are 32-bit: a gathered operand is addressed
+// from its first row, one in order from the tile's (tn: the group's) first.
+constexpr long long kReach = 0xfffffff0LL;
+bool within_reach(long long rows, int div, int ld, long long tile_rows) {
+    const long long reached = div == 0 ? (rows < tile_rows ? rows : tile_rows) : ceil_div(rows, div);
+    return reached + 1 <= kReach / 4 / ld;
+}
+
+struct Block {
+    int bm, bn, threads;
+    GroupedFn nn, nt;
+};
+#define BLOCK(BM, BN, BK, WM, WN, WPE, RO)                                             \
+    {BM, BN, (BM / WM) * (BN / WN) * 64, rowk::grouped_mfma<BM, BN, BK, WM, WN, WPE, false, RO>, \
+     rowk::grouped_mfma<BM, BN, BK, WM, WN, WPE, true, RO>}
+const Block kSmall = BLOCK(64, 64, 32, 32, 32, 4, 1);
+const Block kLarge = BLOCK(128, 128, 16, 64, 64, 4, 0);
+#define THIN(MB, VW, WK, D) {16 * MB, 16 * VW, WK * 64, rowk::thin<MB, VW, WK, D, false>, rowk::thin<MB, VW, WK, D, true>}
+const Block kThin64 = THIN(1, 4, 4, 3), kThin64Deep = THIN(1, 4, 16, 3), kThin32 = THIN(1, 2, 16, 4),
+            kThin16 = THIN(1, 1, 16, 4);
+
+// Up to 16 rows per group on average, the thin kernel: 64 columns and four
+// waves where that gives two workgroups per CU (64 groups of two rows, 1280 x
+// 2048: 110 us, 5.5 TB/s, against 114 with 16 waves), 16 waves down to 192
+// workgroups, and narrower columns below (2 groups of one row, 1024 x 2048).
+// Else 128 x 128 where every CU has a tile, and 64 x 64 below.
+const Block &choose_block(const GroupedArgs &a) {
+    const long long groups = a.offsets == nullptr ? 1 : a.G, used = a.R < groups ? a.R : groups;
+    if (a.R <= 16 * groups) {
+        const long long wide = used * ceil_div(a.N, 64);
+        if (wide >= 512) return kThin64;
+        if (wide >= 192) return kThin64Deep;
+        return used * ceil_div(a.N, 32) >= 96 ? kThin32 : kThin16;
+    }
+    return row_tiles(a, 128) * ceil_div(a.N, 128) >= 256 ? kLarge : kSmall;
+}
+
+// log2 of the device's XCDs: consecutive workgroup ids go to them in turn
+int xcd_shift() {
+    int xcds = 1, shift = 0;
+    (void)sgemm_device_shape(nullptr, &xcds);
+    while ((2 << shift) <= xcds) ++shift;
+    return shift;
+}
+
 int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     if (a.R == 0 || a.N == 0 || a.G == 0) return SGEMM_OK;
+    // the kernels count a wave's 64 groups' tiles (16 rows at least) in 31 bits
+    if (a.R >= 1 << 29) return SGEMM_ERR_TOO_LARGE;
     if (a.alpha == 0.0f) a.K = 0;
     if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
-    const long long grid = row_tiles(a, 32) * ceil_div(a.N, 32);
-    return enqueue(trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>, grid, 256, a, stream);
+    const bool reach = within_reach(a.R, a.a_div, a.lda, 256) &&
+                       (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
+    const Block simple = {32, 32, 256, rowk::grouped_simple<false>, rowk::grouped_simple<true>};
+    const Block &b = reach ? choose_block(a) : simple;
+    const long long grid = row_tiles(a, b.bm) * ceil_div(a.N, b.bn);
+    a.xcd_shift = xcd_shift();
+    return enqueue(trans_b ? b.nt : b.nn, grid, b.threads, a, stream);
+}
+
+struct BlockTN {
+    int bm, bn, threads;
+    GroupedFn fn;
+};
+#define BLOCK_TN(BM, BN, BK, WM, WN, WPE) {BM, BN, (BM / WM) * (BN / WN) * 64, rowk::grouped_tn_mfma<BM, BN, BK, WM, WN, WPE>}
+const BlockTN kSmallTN = BLOCK_TN(64, 64, 32, 32, 32, 4), kLargeTN = BLOCK_TN(128, 128, 16, 64, 64, 4);
+
+const BlockTN &choose_tn(const GroupedArgs &a) {
+    return a.G * ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 512 ? kLargeTN : kSmallTN;
 }
 
 int grouped_tn(GroupedArgs a, hipStream_t stream) {
     if (a.G == 0 || a.M == 0 || a.N == 0) return SGEMM_OK;
     if (a.alpha == 0.0f) a.R = 0;  // every group's range is then empty
     if (a.R == 0 && a.beta == 1.0f) return SGEMM_OK;
-    const long long tiles = ceil_div(a.M, 32) * ceil_div(a.N, 32);
+    const bool reach = within_reach(a.R, a.a_div, a.lda, a.R) && within_reach(a.R, a.b_div, a.ldb, a.R);
+    const BlockTN simple = {32, 32, 256, rowk::grouped_tn_simple};
+    const BlockTN &b = reach ? choose_tn(a) : simple;
+    const long long tiles = ceil_div(a.M, b.bm) * ceil_div(a.N, b.bn);
     if (tiles > INT_MAX / a.G) return SGEMM_ERR_TOO_LARGE;
-    return enqueue(rowk::grouped_tn_simple, tiles * a.G, 256, a, stream);
+    a.xcd_shift = xcd_shift();
+    return enqueue(b.fn, tiles * a.G, b.threads, a, stream);
 }
 
 // ---- slots sorted by group ---------------------------------------------------

@@ -180,9 +180,13 @@ def test_status_strings_cover_every_position():
 
 def test_cpu_tensors_are_refused():
     import torch
-    x = torch.zeros(4, 8)
+    x = torch.zeros(8, 8)
     with pytest.raises(TypeError):
-        g.sgemm_combine(4, 2, 8, 3, None, None, x, 8, 0.0, x, 8, stream=0)
+        g.sgemm_combine(4, 2, 8, 3, None, None, x, 8, 0.0, P, 8, stream=0)
+    with pytest.raises(TypeError):
+        g.sgemm_combine(4, 2, 8, 3, None, None, P, 8, 0.0, x, 8, stream=0)
+    with pytest.raises(TypeError):
+        g.sgemm_combine(4, 2, 8, 3, torch.zeros(4, 2, dtype=torch.int32), None, P, 8, 0.0, P, 8, stream=0)
 
 
 def test_int_arguments_are_not_truncated():
