@@ -60,7 +60,7 @@ typedef void (*GroupedFn)(GroupedArgs);
 
 // The fast kernels' byte offsets are 32-bit: a gathered operand is addressed
 // from its first row, one in order from the tile's (tn: the group's) first.
-constexpr long long kReach = 0xfffffff0LL;
+constexpr long long kReach = 0xffffe000LL;
 bool within_reach(long long rows, int div, int ld, long long tile_rows) {
     const long long reached = div == 0 ? (rows < tile_rows ? rows : tile_rows) : ceil_div(rows, div);
     return reached + 1 <= kReach / 4 / ld;
@@ -70,29 +70,33 @@ struct Block {
     int bm, bn, threads;
     GroupedFn nn, nt;
 };
-#define BLOCK(BM, BN, BK, WM, WN, WPE, RO)                                             \
-    {BM, BN, (BM / WM) * (BN / WN) * 64, rowk::grouped_mfma<BM, BN, BK, WM, WN, WPE, false, RO>, \
-     rowk::grouped_mfma<BM, BN, BK, WM, WN, WPE, true, RO>}
-const Block kSmall = BLOCK(64, 64, 32, 32, 32, 4, 1);
-const Block kLarge = BLOCK(128, 128, 16, 64, 64, 4, 0);
-#define THIN(MB, VW, WK, D) {16 * MB, 16 * VW, WK * 64, rowk::thin<MB, VW, WK, D, false>, rowk::thin<MB, VW, WK, D, true>}
-const Block kThin64 = THIN(1, 4, 4, 3), kThin64Deep = THIN(1, 4, 16, 3), kThin32 = THIN(1, 2, 16, 4),
-            kThin16 = THIN(1, 1, 16, 4);
+#define THIN(MB, VW, WK, WN, WPE) \
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, rowk::thin<MB, VW, WK, WN, WPE, true>}
+// rows x columns of a tile; waves over K x waves over columns
+const Block kTall = THIN(4, 4, 2, 2, 2);      // 64 x 128, 2 x 2
+const Block kTallDeep = THIN(4, 4, 4, 1, 2);  // 64 x 64, 4 x 1
+const Block kLow = THIN(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
+const Block kLowFlat = THIN(2, 4, 1, 1, 4);   // 32 x 64, one wave
+const Block kNarrow = THIN(2, 2, 4, 1, 4);    // 32 x 32, 4 x 1
+const Block kNarrower = THIN(2, 1, 4, 1, 4);  // 32 x 16, 4 x 1
 
-// Up to 16 rows per group on average, the thin kernel: 64 columns and four
-// waves where that gives two workgroups per CU (64 groups of two rows, 1280 x
-// 2048: 110 us, 5.5 TB/s, against 114 with 16 waves), 16 waves down to 192
-// workgroups, and narrower columns below (2 groups of one row, 1024 x 2048).
-// Else 128 x 128 where every CU has a tile, and 64 x 64 below.
-const Block &choose_block(const GroupedArgs &a) {
-    const long long groups = a.offsets == nullptr ? 1 : a.G, used = a.R < groups ? a.R : groups;
-    if (a.R <= 16 * groups) {
-        const long long wide = used * ceil_div(a.N, 64);
-        if (wide >= 512) return kThin64;
-        if (wide >= 192) return kThin64Deep;
-        return used * ceil_div(a.N, 32) >= 96 ? kThin32 : kThin16;
-    }
-    return row_tiles(a, 128) * ceil_div(a.N, 128) >= 256 ? kLarge : kSmall;
+// Measured (us; groups x rows in all, N x K):
+//   K up to 64: one wave per tile, nothing to split (11 x 4096, 4096 x 32:
+//     24 against 44 on four waves).
+//   Few tiles of 32 x 64: narrower columns, so that more CUs read B (one row, 4096
+//     x 4096: 14.4 at 32 columns and 20.6 at 64; B as N x K, where a narrow tile's
+//     lines are still whole, 13.5 at 16 and 20.1 at 32).
+//   Many rows per group: 64 rows, read fewer times (16 x 8192, 4096 x 2048: 1024
+//     against 1100 on 32 rows; N x K 1110 against 1494), for K x N only where
+//     64 x 128 tiles fill the chip often enough (8 x 4022, 2048 x 1024, 1100 tiles:
+//     161 against 146 on 32 x 64).
+//   Else 32 x 64 with four waves over K (64 x 136, 1280 x 2048: 112, 5.4 TB/s).
+const Block &choose_block(const GroupedArgs &a, bool trans_b) {
+    const long long groups = a.offsets == nullptr ? 1 : a.G;
+    if (a.K <= 64) return kLowFlat;
+    if (row_tiles(a, 32) * ceil_div(a.N, 64) < 256) return trans_b ? kNarrower : kNarrow;
+    if (trans_b) return a.R > 64 * groups ? kTallDeep : kLow;
+    return row_tiles(a, 64) * ceil_div(a.N, 128) >= 2048 && a.R > 64 * groups ? kTall : kLow;
 }
 
 // log2 of the device's XCDs: consecutive workgroup ids go to them in turn
@@ -112,21 +116,27 @@ int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     const bool reach = within_reach(a.R, a.a_div, a.lda, 256) &&
                        (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
     const Block simple = {32, 32, 256, rowk::grouped_simple<false>, rowk::grouped_simple<true>};
-    const Block &b = reach ? choose_block(a) : simple;
-    const long long grid = row_tiles(a, b.bm) * ceil_div(a.N, b.bn);
-    a.xcd_shift = xcd_shift();
-    return enqueue(trans_b ? b.nt : b.nn, grid, b.threads, a, stream);
+    const Block &b = reach ? choose_block(a, trans_b) : simple;
+    a.xcd_shift = reach ? xcd_shift() : 0;
+    // every XCD's share of the tile columns, rounded up in every row of tiles
+    const long long columns = ceil_div(ceil_div(a.N, b.bn), 1LL << a.xcd_shift) << a.xcd_shift;
+    return enqueue(trans_b ? b.nt : b.nn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
 }
 
 struct BlockTN {
     int bm, bn, threads;
     GroupedFn fn;
 };
-#define BLOCK_TN(BM, BN, BK, WM, WN, WPE) {BM, BN, (BM / WM) * (BN / WN) * 64, rowk::grouped_tn_mfma<BM, BN, BK, WM, WN, WPE>}
-const BlockTN kSmallTN = BLOCK_TN(64, 64, 32, 32, 32, 4), kLargeTN = BLOCK_TN(128, 128, 16, 64, 64, 4);
+#define OUTER(VM, VN, WK, WPE) {16 * VM, 16 * VN, WK * 64, rowk::outer<VM, VN, WK, WPE>}
+const BlockTN kOuter = OUTER(4, 4, 1, 2), kOuterDeep = OUTER(4, 4, 4, 2);
+const BlockTN kOuterLow = OUTER(1, 4, 4, 4), kOuterNarrow = OUTER(4, 1, 4, 4);
 
+// 64 x 64 tiles, each of one wave where they fill the chip and of four that share
+// the slots below; 16 rows or columns (an adapter's rank) take tiles of 16.
 const BlockTN &choose_tn(const GroupedArgs &a) {
-    return a.G * ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 512 ? kLargeTN : kSmallTN;
+    if (a.M <= 32) return kOuterLow;
+    if (a.N <= 32) return kOuterNarrow;
+    return a.G * ceil_div(a.M, 64) * ceil_div(a.N, 64) >= 1024 ? kOuter : kOuterDeep;
 }
 
 int grouped_tn(GroupedArgs a, hipStream_t stream) {
@@ -136,10 +146,11 @@ int grouped_tn(GroupedArgs a, hipStream_t stream) {
     const bool reach = within_reach(a.R, a.a_div, a.lda, a.R) && within_reach(a.R, a.b_div, a.ldb, a.R);
     const BlockTN simple = {32, 32, 256, rowk::grouped_tn_simple};
     const BlockTN &b = reach ? choose_tn(a) : simple;
-    const long long tiles = ceil_div(a.M, b.bm) * ceil_div(a.N, b.bn);
-    if (tiles > INT_MAX / a.G) return SGEMM_ERR_TOO_LARGE;
-    a.xcd_shift = xcd_shift();
-    return enqueue(b.fn, tiles * a.G, b.threads, a, stream);
+    const long long nbm = ceil_div(a.M, b.bm), nbn = ceil_div(a.N, b.bn);
+    if (nbm * nbn > INT_MAX / a.G) return SGEMM_ERR_TOO_LARGE;
+    a.xcd_shift = reach ? xcd_shift() : 0;
+    const long long columns = ceil_div(nbn * a.G, 1LL << a.xcd_shift) << a.xcd_shift;
+    return enqueue(b.fn, nbm * columns, b.threads, a, stream);
 }
 
 // ---- slots sorted by group ---------------------------------------------------
