@@ -9,26 +9,11 @@
 // only 4-byte alignment.
 #pragma once
 
-#undef SGEMM_PHASES
-#include "sgemm_kernels.hpp"
-
 #include "rows_kernels.hpp"
 
 namespace rowk {
 
-using sgk::f32x2;
-using sgk::f32x4;
-using sgk::floatx16;
-using sgk::rsrc_t;
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-
-// A descriptor over [base, base + bytes), at most kOut bytes; an access at
-// kOut is outside every one (and its 16 bytes do not wrap).
-constexpr uint32_t kOut = 0xfffffff0u;
-__device__ __forceinline__ rsrc_t whole_rsrc(const void *base, int64_t bytes) {
-    const uint32_t n = bytes <= 0 ? 0u : (bytes >= (int64_t)kOut ? kOut : (uint32_t)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, sgk::kRsrcWord3);
-}
 
 // ---------------------------------------------------------------------------
 // The order of a launch's tiles.  Workgroup ids go to the XCDs in turn, and the
@@ -219,28 +204,45 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
     // acc[i][j] register r on lane (li, lk): row VM (4 lk + r) + i, column VN li + j
     const float al = group_alpha(a, g);
     const int mr = a.rank_m ? group_rank(a, g, a.M) : a.M, nr = a.rank_n ? group_rank(a, g, a.N) : a.N;
-    float *C = a.C + (int64_t)g * a.stride_c;
+    float *C = a.C + (int64_t)g * a.stride_c + (int64_t)m0 * a.ldc + n0;
+    const int rows = a.M - m0, cols = a.N - n0;  // of C from the tile's corner
+    if (VN == 4 && WK == 1 && cols >= BN && a.ldc < 1 << 22 && mr >= m0 + BM && nr >= n0 + BN) {
+        // Whole rows of the tile: the lanes' offsets stay and each row's place goes
+        // into a descriptor that ends at C_g's last element (64-bit addresses
+        // worked out per row took as long as a tenth of the MFMAs).
+        const uint32_t off = (uint32_t)(VM * 4 * lk) * (uint32_t)a.ldc * 4u + 16u * (uint32_t)li;
+        const int64_t end = ((int64_t)(rows - 1) * a.ldc + cols) * 4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < VM; ++i) {
+                const int64_t row = (int64_t)(VM * r + i) * a.ldc;
+                const rsrc_t rc = whole_rsrc(C + row, end - 4 * row);
+                f32x4 v;
+                v.x = al * acc[i][0 % VN][r];
+                v.y = al * acc[i][1 % VN][r];
+                v.z = al * acc[i][2 % VN][r];
+                v.w = al * acc[i][3 % VN][r];
+                if (a.beta != 0.0f) {
+                    const f32x4 old = sgk::raw_load_v4f32(rc, off, 0, 0);
+                    v.x = fmaf(a.beta, old.x, v.x);
+                    v.y = fmaf(a.beta, old.y, v.y);
+                    v.z = fmaf(a.beta, old.z, v.z);
+                    v.w = fmaf(a.beta, old.w, v.w);
+                }
+                sgk::raw_store_v4f32(v, rc, off, 0, sgk::kCPolStream);
+            }
+        return;
+    }
     auto write = [&](int m, int n, const auto &v) {
         constexpr int V = sizeof(v) / sizeof(float);
-        if (m >= a.M) return;
+        if (m >= rows) return;
         float *c = C + (int64_t)m * a.ldc + n;
-        if constexpr (V == 4) {
-            const int left = a.N - n;
-            if (left <= 0) return;
-            f32x4u old = {0.0f, 0.0f, 0.0f, 0.0f}, out;
-            if (a.beta != 0.0f) old = load4(c, left);
-            out.x = fmaf(a.beta, old.x, m < mr && n < nr ? al * v[0] : 0.0f);
-            out.y = fmaf(a.beta, old.y, m < mr && n + 1 < nr ? al * v[1] : 0.0f);
-            out.z = fmaf(a.beta, old.z, m < mr && n + 2 < nr ? al * v[2] : 0.0f);
-            out.w = fmaf(a.beta, old.w, m < mr && n + 3 < nr ? al * v[3] : 0.0f);
-            store4(c, left, out);
-        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (n + j >= a.N) continue;
-                const float x = m < mr && n + j < nr ? al * v[j] : 0.0f;
-                c[j] = a.beta != 0.0f ? fmaf(a.beta, c[j], x) : x;
-            }
+        for (int j = 0; j < V; ++j) {
+            if (n + j >= cols) continue;
+            const float x = m0 + m < mr && n0 + n + j < nr ? al * v[j] : 0.0f;
+            c[j] = a.beta != 0.0f ? fmaf(a.beta, c[j], x) : x;
         }
     };
 #pragma unroll
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
             for (int j = 0; j < VN; ++j) v[j] = acc[i][j][r];
             const int row = VM * (4 * lk + r) + i;
             if constexpr (WK == 1) {
-                write(m0 + row, n0 + VN * li, v);
+                write(row, VN * li, v);
             } else {
 #pragma unroll
                 for (int j = 0; j < VN; ++j) part[w][row * BN + VN * li + j] = v[j];
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 #pragma unroll
                 for (int i = 1; i < WK; ++i) v[j] += part[i][row * BN + col + j];
             }
-            write(m0 + row, n0 + col, v);
+            write(row, col, v);
         }
     }
 }
@@ -291,7 +293,7 @@ template <int MB, int VW, int WK, int WN, int WPE, bool TRANS_B>
 __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_eu(WPE))) thin(GroupedArgs a) {
     constexpr int ROWS = 16 * MB, COLS = 16 * VW, NT = WK * WN * 64;
     __shared__ __attribute__((aligned(16))) float part[WK > 1 ? WK : 1][WK > 1 ? WN * ROWS * COLS : 1];
-    __shared__ int c_row[ROWS];
+    __shared__ __attribute__((aligned(16))) int c_row[ROWS];
     Tile t;
     if (!place_tile(a, ROWS, COLS * WN, t)) return;
     const int g = t.g, p0 = t.p0, p1 = t.p1;
@@ -299,12 +301,13 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6) / WN, wn = __builtin_amdgcn_readfirstlane(tid >> 6) % WN;
     const int n0 = t.bn + wn * COLS;
     const int li = lane & 15, lk = lane >> 4;
-    const int K = a.rank_k ? group_rank(a, g, a.K) : a.K;
+    const int live = p1 - p0 < ROWS ? (p1 - p0 + 15) / 16 : MB;  // 16-row blocks
+    int my_row = -1;  // of C: thread m holds the tile's row m
+    if (tid < ROWS && p0 + tid < p1) my_row = (int)row_of(a, p0 + tid, a.c_scatter);
+
+    const int K = a.rank_k ? __builtin_amdgcn_readfirstlane(group_rank(a, g, a.K)) : a.K;
     const int steps = (K + 31) / 32;
     const int s0 = (int)((int64_t)steps * w / WK), s1 = (int)((int64_t)steps * (w + 1) / WK);
-    const int live = p1 - p0 < ROWS ? (p1 - p0 + 15) / 16 : MB;  // 16-row blocks
-    for (int m = tid; m < ROWS; m += NT) c_row[m] = p0 + m < p1 ? (int)row_of(a, p0 + m, a.c_scatter) : -1;
-
     const int64_t a_rows = a.a_div > 1 ? (a.R + a.a_div - 1) / a.a_div : a.R;
     const int64_t a_base = a.a_div == 0 ? p0 : 0;
     const float *a_from = a.A + a_base * a.lda;
@@ -321,7 +324,6 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     // K x N: rows from the group's first to K; N x K: from row n0 to the last
     const float *b_base = TRANS_B ? B + (int64_t)n0 * a.ldb : B + n0;
     const int64_t b_bytes = TRANS_B ? ((int64_t)(a.N - n0 - 1) * a.ldb + a.K) * 4 : ((int64_t)(K - 1) * a.ldb + (a.N - n0)) * 4;
-    const uint32_t ldb4 = (uint32_t)a.ldb * 4u;
     constexpr int BL = TRANS_B ? VW : 4;  // loads of B per 16 k
 
     floatx4 acc[MB][VW];
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
 #pragma unroll
         for (int j = 0; j < VW; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto k_loop = [&](auto blocks) {
+    auto k_loop = [&](auto blocks) __attribute__((always_inline)) {
         constexpr int L = decltype(blocks)::value;
         // A step is H halves of 16 k.  With 16 rows or fewer and B as N x K it is two,
         // so that what runs along K is read in whole 128-byte lines (1280 x 2048,
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
         static_assert(D >= 2, "steps in flight");
         const int last = (K + 16 * H - 1) / (16 * H);
         const int u0 = s0 * (2 / H), u1 = s1 * (2 / H) < last ? s1 * (2 / H) : last;
+        const uint32_t ldb4 = (uint32_t)a.ldb * 4u;
         uint32_t al[L], bl[BL];
 #pragma unroll
         for (int i = 0; i < L; ++i) al[i] = aoff[i] + (uint32_t)(16 * H * lk);
@@ -463,33 +466,45 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     // acc[i][j] register r on lane (li, lk): row 16 i + 4 lk + r, column VW li + j
     // (K x N) or 16 j + li (N x K)
     const float al = group_alpha(a, g);
+    if (tid < ROWS) c_row[tid] = my_row;
     if constexpr (WK == 1) {
-        __syncthreads();  // c_row
+        static_assert(VW == 4, "whole vectors of columns");
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             if (i >= live) break;
+            // four rows' old values in flight
+            const int4 rows = *reinterpret_cast<const int4 *>(&c_row[16 * i + 4 * lk]);
+            const int row[4] = {rows.x, rows.y, rows.z, rows.w};
+            f32x4u old[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int64_t c = c_row[16 * i + 4 * lk + r];
-                if (c < 0) continue;
-                float *q = a.C + c * a.ldc + n0;
-                if constexpr (TRANS_B || VW != 4) {
+                old[r] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
+                if (a.beta == 0.0f || row[r] < 0) continue;
+                const float *q = a.C + (int64_t)row[r] * a.ldc + n0;
+                if constexpr (TRANS_B) {
 #pragma unroll
-                    for (int j = 0; j < VW; ++j) {
-                        const int col = TRANS_B ? 16 * j + li : VW * li + j;
-                        if (n0 + col >= a.N) continue;
-                        const float v = al * acc[i][j][r];
-                        q[col] = a.beta != 0.0f ? fmaf(a.beta, q[col], v) : v;
-                    }
+                    for (int j = 0; j < VW; ++j)
+                        if (n0 + 16 * j + li < a.N) old[r][j] = q[16 * j + li];
                 } else {
-                    const int left = a.N - (n0 + 4 * li);
-                    f32x4u v;
-                    v.x = al * acc[i][0][r];
-                    v.y = al * acc[i][1][r];
-                    v.z = al * acc[i][2][r];
-                    v.w = al * acc[i][3][r];
-                    if (a.beta != 0.0f) v = fma4(a.beta, load4(q + 4 * li, left), v);
-                    store4(q + 4 * li, left, v);
+                    old[r] = load4(q + 4 * li, a.N - (n0 + 4 * li));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (row[r] < 0) continue;
+                float *q = a.C + (int64_t)row[r] * a.ldc + n0;
+                f32x4u v;
+                v.x = fmaf(a.beta, old[r].x, al * acc[i][0][r]);
+                v.y = fmaf(a.beta, old[r].y, al * acc[i][1][r]);
+                v.z = fmaf(a.beta, old[r].z, al * acc[i][2][r]);
+                v.w = fmaf(a.beta, old[r].w, al * acc[i][3][r]);
+                if constexpr (TRANS_B) {
+#pragma unroll
+                    for (int j = 0; j < VW; ++j)
+                        if (n0 + 16 * j + li < a.N) q[16 * j + li] = v[j];
+                } else {
+                    store4(q + 4 * li, a.N - (n0 + 4 * li), v);
                 }
             }
         }

@@ -99,12 +99,21 @@ const Block &choose_block(const GroupedArgs &a, bool trans_b) {
     return row_tiles(a, 64) * ceil_div(a.N, 128) >= 2048 && a.R > 64 * groups ? kTall : kLow;
 }
 
-// log2 of the device's XCDs: consecutive workgroup ids go to them in turn
-int xcd_shift() {
+// log2 of the device's XCDs: consecutive workgroup ids go to them in turn.  With
+// fewer tile columns than XCDs, 0: tiles in turn (dealt by column, an XCD would
+// hold all rows of some groups and none of others).
+int xcd_shift(long long columns) {
     int xcds = 1, shift = 0;
     (void)sgemm_device_shape(nullptr, &xcds);
     while ((2 << shift) <= xcds) ++shift;
-    return shift;
+    return columns < xcds ? 0 : shift;
+}
+
+int launch_block(const Block &b, GroupedFn fn, bool dealt, GroupedArgs a, hipStream_t stream) {
+    a.xcd_shift = dealt ? xcd_shift(ceil_div(a.N, b.bn)) : 0;
+    // every XCD's share of the tile columns, rounded up in every row of tiles
+    const long long columns = ceil_div(ceil_div(a.N, b.bn), 1LL << a.xcd_shift) << a.xcd_shift;
+    return enqueue(fn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
 }
 
 int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
@@ -117,10 +126,7 @@ int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
                        (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
     const Block simple = {32, 32, 256, rowk::grouped_simple<false>, rowk::grouped_simple<true>};
     const Block &b = reach ? choose_block(a, trans_b) : simple;
-    a.xcd_shift = reach ? xcd_shift() : 0;
-    // every XCD's share of the tile columns, rounded up in every row of tiles
-    const long long columns = ceil_div(ceil_div(a.N, b.bn), 1LL << a.xcd_shift) << a.xcd_shift;
-    return enqueue(trans_b ? b.nt : b.nn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
+    return launch_block(b, trans_b ? b.nt : b.nn, reach, a, stream);
 }
 
 struct BlockTN {
@@ -148,31 +154,28 @@ int grouped_tn(GroupedArgs a, hipStream_t stream) {
     const BlockTN &b = reach ? choose_tn(a) : simple;
     const long long nbm = ceil_div(a.M, b.bm), nbn = ceil_div(a.N, b.bn);
     if (nbm * nbn > INT_MAX / a.G) return SGEMM_ERR_TOO_LARGE;
-    a.xcd_shift = reach ? xcd_shift() : 0;
+    a.xcd_shift = reach ? xcd_shift(nbn) : 0;
     const long long columns = ceil_div(nbn * a.G, 1LL << a.xcd_shift) << a.xcd_shift;
     return enqueue(b.fn, nbm * columns, b.threads, a, stream);
 }
 
 // ---- slots sorted by group ---------------------------------------------------
-// Workgroups of the two-launch form: runs of at least kGroupSlots slots, at most
-// 256 of them (each adds up the counts of all).
-int group_workgroups(int R) {
-    if (R <= rowk::kGroupSlots) return 1;
-    const long long n = ceil_div(R, rowk::kGroupSlots / 2);
-    return n < 256 ? (int)n : 256;
-}
+// Slots per workgroup of the two-launch form: one turn of kGroupSlots, more beyond
+// 256 workgroups (each adds up the counts of all).
+int group_run(int R) { return (int)(ceil_div(R > 0 ? R : 1, 256LL * rowk::kGroupSlots) * rowk::kGroupSlots); }
+int group_workgroups(int R) { return R <= rowk::kGroupSlots ? 1 : (int)ceil_div(R, group_run(R)); }
 
 size_t group_bytes(int R, int G) {
     const int n = group_workgroups(R);
     return n == 1 ? 0 : round_up((size_t)n * G * 4);
 }
 
-template <int GMAX> int group_launch(rowk::GroupArgs a, int n, hipStream_t stream) {
+template <int GMAX, int WAVES> int group_launch(rowk::GroupArgs a, int n, hipStream_t stream) {
     if (n > 1) {
-        const int rc = enqueue(rowk::group_rows<GMAX, true>, n, rowk::kGroupThreads, a, stream);
+        const int rc = enqueue(rowk::group_rows<GMAX, WAVES, true>, n, 64 * WAVES, a, stream);
         if (rc != SGEMM_OK) return rc;
     }
-    return enqueue(rowk::group_rows<GMAX, false>, n, rowk::kGroupThreads, a, stream);
+    return enqueue(rowk::group_rows<GMAX, WAVES, false>, n, 64 * WAVES, a, stream);
 }
 
 int group(int R, int G, const int *ids, int *offsets, int *rows, void *workspace, hipStream_t stream) {
@@ -180,12 +183,13 @@ int group(int R, int G, const int *ids, int *offsets, int *rows, void *workspace
     rowk::GroupArgs a;
     a.R = R;
     a.G = G;
-    a.run = n == 1 ? (R > 0 ? R : 1) : (int)ceil_div(R, n);
+    a.run = group_run(R);
     a.ids = ids;
     a.offsets = offsets;
     a.rows = rows;
     a.counts = static_cast<int *>(workspace);
-    return G <= 1024 ? group_launch<1024>(a, n, stream) : group_launch<SGEMM_MAX_GROUPS>(a, n, stream);
+    if (R <= 64) return enqueue(rowk::group_few, 1, 64, a, stream);
+    return G <= 1024 ? group_launch<1024, 16>(a, n, stream) : group_launch<SGEMM_MAX_GROUPS, 8>(a, n, stream);
 }
 
 bool workspace_ok(const void *p, size_t have, size_t need) {
@@ -193,7 +197,22 @@ bool workspace_ok(const void *p, size_t have, size_t need) {
 }
 
 // ---- adapters ----------------------------------------------------------------
-// Workspace: [offsets][rows][group counts][H: M x rank][dH: M x rank][sgemm's]
+// Up to 64 rows, which a batch of sequences has, each with an adapter of its own:
+// h = A[m] U_g in pieces of K, C = alpha h V_g + beta C, both a workgroup per row
+// and piece, and C += alpha A B.  More: rows sorted by adapter, H = A U_g, the
+// projection, and C += H V_g.  (Summing A B and H V_g over sorted rows in one
+// grouped product was slower, 4096 x 4096 x 2048 with 11 adapters 613 us against
+// 559: sgemm's blocks gain more than C's extra traffic costs.)
+constexpr int kFewRows = 64;
+
+// Pieces of K that the few rows' h are summed in: a workgroup's loads of 128 k's
+// of any rank are in flight at once.
+int shrink_parts(int K) {
+    const int n = K / 128;
+    return n < 1 ? 1 : (n > 16 ? 16 : n);
+}
+
+// Workspace: [offsets][rows][group counts][H][dH: M x rank][sgemm's]
 struct AdapterSpace {
     size_t offsets, rows, counts, h, dh, product, end;
     AdapterSpace(int M, int N, int K, int G, int rank, bool grad) {
@@ -206,20 +225,11 @@ struct AdapterSpace {
         offsets = take(((size_t)G + 1) * 4);
         rows = take((size_t)M * 4);
         counts = take(group_bytes(M, G));
-        h = take((size_t)M * rank * 4);
+        h = take((size_t)M * rank * 4 * (M <= kFewRows && !grad ? shrink_parts(K) : 1));
         dh = take(grad ? (size_t)M * rank * 4 : 0);
-        product = take(grad ? 0 : sgemm_workspace_size(M, N, K));
+        product = take(grad || M <= 512 ? 0 : sgemm_workspace_size(M, N, K));
         end = at;
     }
-};
-
-struct Adapters {
-    int M, N, K, G, rank;
-    float alpha;
-    const int *ids, *ranks;
-    const float *scales, *A, *U, *V;
-    int lda, ldu, ldv;
-    long long stride_u, stride_v;
 };
 
 GroupedArgs blank(int G, int R) {
@@ -230,22 +240,68 @@ GroupedArgs blank(int G, int R) {
     return a;
 }
 
-// H[m] = A[m] U_g for the placed rows
-GroupedArgs shrink(const Adapters &p, const int *offsets, const int *rows, float *H) {
-    GroupedArgs a = blank(p.G, p.M);
-    a.N = p.rank;
-    a.K = p.K;
-    a.A = p.A;
-    a.lda = p.lda;
+// C = alpha A B + beta C: up to 512 rows on the grouped kernels, as one group (100 x
+// 4096 x 4096 36 us against sgemm_ws's 42, 300 rows 94 against 98), beyond on
+// sgemm's blocks (4096 x 4096 x 2048 473 against 482, 2000 x 2048 x 1024 66 against 68).
+int project(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta, float *C,
+            int ldc, void *workspace, size_t bytes, hipStream_t stream) {
+    if (M > 512) return sgemm_ws(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, workspace, bytes, stream);
+    GroupedArgs a = blank(1, M);
+    a.N = N;
+    a.K = K;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.A = A;
+    a.lda = lda;
+    a.B = B;
+    a.ldb = ldb;
+    a.C = C;
+    a.ldc = ldc;
+    return grouped(a, false, stream);
+}
+
+// H[m] = scales[g] A[m] U_g for the placed rows (trans_u: U_g rank x K)
+GroupedArgs shrink(int M, int K, int G, int rank, const float *A, int lda, const float *U, int ldu,
+                   long long stride_u, const float *scales, const int *offsets, const int *rows, float *H) {
+    GroupedArgs a = blank(G, M);
+    a.N = rank;
+    a.K = K;
+    a.A = A;
+    a.lda = lda;
     a.a_div = 1;
-    a.B = p.U;
-    a.ldb = p.ldu;
-    a.stride_b = p.stride_u;
+    a.B = U;
+    a.ldb = ldu;
+    a.stride_b = stride_u;
     a.C = H;
-    a.ldc = p.rank;
+    a.ldc = rank;
     a.c_scatter = 1;
     a.offsets = offsets;
     a.rows = rows;
+    a.scales = scales;
+    return a;
+}
+
+// C[m] += alpha H[m] V_g (trans_v: V_g N x rank)
+GroupedArgs expand(int M, int N, int G, int rank, float alpha, const float *H, const float *V, int ldv,
+                   long long stride_v, const int *ranks, const int *offsets, const int *rows, float *C, int ldc) {
+    GroupedArgs a = blank(G, M);
+    a.N = N;
+    a.K = rank;
+    a.alpha = alpha;
+    a.beta = 1.0f;
+    a.A = H;
+    a.lda = rank;
+    a.a_div = 1;
+    a.B = V;
+    a.ldb = ldv;
+    a.stride_b = stride_v;
+    a.C = C;
+    a.ldc = ldc;
+    a.c_scatter = 1;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.ranks = ranks;
+    a.rank_k = 1;
     return a;
 }
 
@@ -512,34 +568,54 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
     char *w = static_cast<char *>(workspace);
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h);
-    const Adapters p = {M, N, K, G, rank, alpha, ids, ranks, scales, A, U, V, lda, ldu, ldv, stride_u, stride_v};
-
-    int rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
-    if (rc == SGEMM_OK) rc = grouped(shrink(p, offsets, rows, H), false, stream);
-    if (rc == SGEMM_OK)
-        rc = sgemm_ws(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, w + at.product, at.end - at.product, stream);
-    if (rc == SGEMM_OK) {  // C[m] += alpha scale H[m] V_g
-        GroupedArgs a = blank(G, M);
-        a.N = N;
-        a.K = rank;
-        a.alpha = alpha;
-        a.beta = 1.0f;
-        a.A = H;
-        a.lda = rank;
-        a.a_div = 1;
-        a.B = V;
-        a.ldb = ldv;
-        a.stride_b = stride_v;
-        a.C = C;
-        a.ldc = ldc;
-        a.c_scatter = 1;
-        a.offsets = offsets;
-        a.rows = rows;
-        a.scales = scales;
-        a.ranks = ranks;
-        a.rank_k = 1;
-        rc = grouped(a, false, stream);
+    int rc;
+    // (a piece of U within 32-bit offsets)
+    if (M <= kFewRows && ceil_div(K, shrink_parts(K)) + 1 <= kReach / 4 / ldu) {
+        rowk::ShrinkArgs h;
+        h.M = M;
+        h.K = K;
+        h.G = G;
+        h.rank = rank;
+        h.parts = shrink_parts(K);
+        h.A = A;
+        h.U = U;
+        h.lda = lda;
+        h.ldu = ldu;
+        h.stride_u = stride_u;
+        h.ids = ids;
+        h.ranks = ranks;
+        h.H = H;
+        rc = enqueue(rowk::shrink_rows, (long long)M * h.parts, 256, h, stream);
+        if (rc != SGEMM_OK) return rc;
+        rowk::ExpandArgs e;
+        e.M = M;
+        e.N = N;
+        e.G = G;
+        e.rank = rank;
+        e.parts = h.parts;
+        e.chunks = (int)ceil_div(N, 256);
+        e.alpha = alpha;
+        e.beta = beta;
+        e.H = H;
+        e.V = V;
+        e.scales = scales;
+        e.ldv = ldv;
+        e.stride_v = stride_v;
+        e.ldc = ldc;
+        e.ids = ids;
+        e.ranks = ranks;
+        e.C = C;
+        rc = enqueue(rowk::expand_rows, (long long)M * e.chunks, 64, e, stream);
+        if (rc != SGEMM_OK) return rc;
+        return project(M, N, K, alpha, A, lda, B, ldb, 1.0f, C, ldc, nullptr, 0, stream);
     }
+    rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
+    if (rc == SGEMM_OK)
+        rc = grouped(shrink(M, K, G, rank, A, lda, U, ldu, stride_u, scales, offsets, rows, H), false, stream);
+    if (rc == SGEMM_OK)
+        rc = project(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, w + at.product, at.end - at.product, stream);
+    if (rc == SGEMM_OK)
+        rc = grouped(expand(M, N, G, rank, alpha, H, V, ldv, stride_v, ranks, offsets, rows, C, ldc), false, stream);
     return rc;
 }
 
@@ -582,32 +658,13 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
     char *w = static_cast<char *>(workspace);
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h), *dH = reinterpret_cast<float *>(w + at.dh);
-    const Adapters p = {M, N, K, G, rank, alpha, ids, ranks, scales, A, U, V, lda, ldu, ldv, stride_u, stride_v};
-
     int rc = SGEMM_OK;
     if (product) {
         rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
-        if (rc == SGEMM_OK) {  // dH[m] = alpha scale dC[m] V_g^T
-            GroupedArgs a = blank(G, M);
-            a.N = rank;
-            a.K = N;
-            a.alpha = alpha;
-            a.A = dC;
-            a.lda = lddc;
-            a.a_div = 1;
-            a.B = V;
-            a.ldb = ldv;
-            a.stride_b = stride_v;
-            a.C = dH;
-            a.ldc = rank;
-            a.c_scatter = 1;
-            a.offsets = offsets;
-            a.rows = rows;
-            a.scales = scales;
-            rc = grouped(a, true, stream);
-        }
+        if (rc == SGEMM_OK)  // dH[m] = scale dC[m] V_g^T
+            rc = grouped(shrink(M, N, G, rank, dC, lddc, V, ldv, stride_v, scales, offsets, rows, dH), true, stream);
     }
-    if (rc == SGEMM_OK && dA != nullptr) {  // dA = alpha dC B^T
+    if (rc == SGEMM_OK && dA != nullptr) {
         GroupedArgs a = blank(1, M);
         a.N = K;
         a.K = N;
@@ -619,31 +676,15 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
         a.C = dA;
         a.ldc = ldda;
         rc = grouped(a, true, stream);
-        if (rc == SGEMM_OK && product) {  // dA[m] += dH[m] U_g^T
-            GroupedArgs b = blank(G, M);
-            b.N = K;
-            b.K = rank;
-            b.beta = 1.0f;
-            b.A = dH;
-            b.lda = rank;
-            b.a_div = 1;
-            b.B = U;
-            b.ldb = ldu;
-            b.stride_b = stride_u;
-            b.C = dA;
-            b.ldc = ldda;
-            b.c_scatter = 1;
-            b.offsets = offsets;
-            b.rows = rows;
-            b.ranks = ranks;
-            b.rank_k = 1;
-            rc = grouped(b, true, stream);
-        }
+        if (rc == SGEMM_OK && product)
+            rc = grouped(expand(M, K, G, rank, alpha, dH, U, ldu, stride_u, ranks, offsets, rows, dA, ldda), true,
+                         stream);
     }
     if (rc == SGEMM_OK && adapters) {
-        GroupedArgs a = blank(G, product ? M : 0);  // dU_g = A^T dH
+        GroupedArgs a = blank(G, product ? M : 0);  // dU_g = alpha A^T dH
         a.M = K;
         a.N = rank;
+        a.alpha = alpha;
         a.beta = beta;
         a.A = A;
         a.lda = lda;
@@ -659,12 +700,12 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
         a.ranks = ranks;
         a.rank_n = 1;
         rc = grouped_tn(a, stream);
-        if (rc == SGEMM_OK && product) rc = grouped(shrink(p, offsets, rows, H), false, stream);
-        if (rc == SGEMM_OK) {  // dV_g = alpha scale H^T dC
+        if (rc == SGEMM_OK && product)
+            rc = grouped(shrink(M, K, G, rank, A, lda, U, ldu, stride_u, scales, offsets, rows, H), false, stream);
+        if (rc == SGEMM_OK) {  // dV_g = alpha H^T dC
             GroupedArgs b = a;
             b.M = rank;
             b.N = N;
-            b.alpha = alpha;
             b.A = H;
             b.lda = rank;
             b.B = dC;
@@ -672,7 +713,6 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
             b.C = dV;
             b.ldc = lddv;
             b.stride_c = stride_dv;
-            b.scales = scales;
             b.rank_n = 0;
             b.rank_m = 1;
             rc = grouped_tn(b, stream);

@@ -11,7 +11,22 @@
 
 #include <type_traits>
 
+#undef SGEMM_PHASES
+#include "sgemm_kernels.hpp"
+
 namespace rowk {
+
+using sgk::f32x2;
+using sgk::f32x4;
+using sgk::rsrc_t;
+
+// A descriptor over [base, base + bytes), at most kOut bytes; an access at
+// kOut is outside every one (and its 16 bytes do not wrap).
+constexpr uint32_t kOut = 0xfffffff0u;
+__device__ __forceinline__ rsrc_t whole_rsrc(const void *base, int64_t bytes) {
+    const uint32_t n = bytes <= 0 ? 0u : (bytes >= (int64_t)kOut ? kOut : (uint32_t)bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, sgk::kRsrcWord3);
+}
 
 // ---------------------------------------------------------------------------
 // Lane exchange inside a 16-lane DPP row and across a wave's four rows.
@@ -55,6 +70,36 @@ struct Add {
 
 // four floats at any 4-byte alignment (one 16-byte access on gfx950)
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ f32x4u load4(const float *p, int left) {
+    f32x4u v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (left >= 4) {
+        v = *reinterpret_cast<const f32x4u *>(p);
+    } else {
+        if (left > 0) v.x = p[0];
+        if (left > 1) v.y = p[1];
+        if (left > 2) v.z = p[2];
+    }
+    return v;
+}
+__device__ __forceinline__ void store4(float *p, int left, f32x4u v) {
+    if (left >= 4) {
+        *reinterpret_cast<f32x4u *>(p) = v;
+    } else {
+        if (left > 0) p[0] = v.x;
+        if (left > 1) p[1] = v.y;
+        if (left > 2) p[2] = v.z;
+    }
+}
+// (element by element: no packed FP32 instructions)
+template <class V> __device__ __forceinline__ V fma4(float s, V a, V c) {
+    V r;
+    r.x = fmaf(s, a.x, c.x);
+    r.y = fmaf(s, a.y, c.y);
+    r.z = fmaf(s, a.z, c.z);
+    r.w = fmaf(s, a.w, c.w);
+    return r;
+}
 
 // ---------------------------------------------------------------------------
 // The router.  L lanes hold one row: element e = l + L v in register v of lane
@@ -321,26 +366,24 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad(RouteGradArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Slots sorted by group: a counting sort that keeps the slots' order.  A
-// workgroup's waves each take a run of consecutive slots, 64 at a time.  The
-// place of a slot is: what lower groups hold, plus its group's slots in earlier
-// runs, plus those earlier in its own run, counted with one ballot per bit of
-// the id (the lanes whose ids agree in every bit), so there is no atomic and
-// the order is the slots' own.  One workgroup does it all up to kGroupSlots
-// slots; beyond, a first launch counts each workgroup's run and in a second
+// Slots sorted by group: a counting sort that keeps the slots' order.  4096 slots
+// at a time, each of a workgroup's waves taking a run of consecutive ones, 64 to a
+// register.  The place of a slot is: where its group begins, plus the group's
+// slots in earlier runs, plus those earlier in its own run; these are counted with
+// one ballot per bit of the id (the lanes whose ids agree in every bit), so there is
+// no atomic and the order is the slots' own.  One workgroup does it all up to 4096
+// slots; beyond, a first launch counts each workgroup's slots and in a second
 // every workgroup adds up what lies before its own.
 // ---------------------------------------------------------------------------
-constexpr int kGroupWaves = 8;
-constexpr int kGroupThreads = 64 * kGroupWaves;
-constexpr int kGroupSlots = 4096;  // slots of one workgroup
+constexpr int kGroupSlots = 4096;
 
 struct GroupArgs {
-    int R, G, run;  // run: slots per workgroup
+    int R, G, run;  // run: slots per workgroup, whole turns of kGroupSlots
     const int *ids;
     int *offsets, *rows, *counts;  // counts: [workgroups][G]
 };
 
-// lanes with the same id (all ones where `id` is G or more is not asked for)
+// lanes with the same id
 __device__ __forceinline__ unsigned long long same_id(int id, int bits) {
     unsigned long long m = ~0ull;
     for (int b = 0; b < bits; ++b) {
@@ -350,59 +393,79 @@ __device__ __forceinline__ unsigned long long same_id(int id, int bits) {
     return m;
 }
 
-template <int GMAX, bool COUNT_ONLY>
-__global__ void __launch_bounds__(kGroupThreads) group_rows(GroupArgs a) {
-    __shared__ int count[kGroupWaves][GMAX];
-    __shared__ int wave_sum[kGroupWaves];
+template <int GMAX, int WAVES, bool COUNT_ONLY>
+__global__ void __launch_bounds__(64 * WAVES) group_rows(GroupArgs a) {
+    constexpr int NT = 64 * WAVES, PER = kGroupSlots / NT, GROUPS = GMAX / NT;
+    static_assert(PER * NT == kGroupSlots && GROUPS * NT == GMAX, "whole registers, whole groups per thread");
+    __shared__ int count[WAVES][GMAX];
+    __shared__ int wave_sum[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int nwg = gridDim.x, wg = blockIdx.x;
-    const int64_t wg0 = (int64_t)wg * a.run;
-    const int64_t wg1 = wg0 + a.run < a.R ? wg0 + a.run : a.R;
-    const int per = ((a.run + kGroupWaves - 1) / kGroupWaves + 63) / 64 * 64;  // slots per wave
-    const int64_t s0 = wg0 + (int64_t)w * per < wg1 ? wg0 + (int64_t)w * per : wg1;
-    const int64_t s1 = s0 + per < wg1 ? s0 + per : wg1;
+    const int64_t begin = (int64_t)wg * a.run, end = begin + a.run < a.R ? begin + a.run : a.R;
     const int bits = 32 - __clz(a.G);  // ids up to G itself, which stands for none
-    auto id_of = [&](int64_t s) {
-        const int id = s < s1 ? a.ids[s] : a.G;
-        return (unsigned)id < (unsigned)a.G ? id : a.G;
-    };
     const unsigned long long below = (1ull << lane) - 1;
 
-    for (int i = lane; i < a.G; i += 64) count[w][i] = 0;
-    for (int64_t s = s0; s < s1; s += 64) {
-        const int id = id_of(s + lane);
-        const unsigned long long same = same_id(id, bits);
-        // the first lane of each id adds the number of its lanes
-        if (id < a.G && (same & below) == 0) count[w][id] += __popcll(same);
-    }
-    __syncthreads();
+    int id[PER], before[PER];  // a slot's id, and its group's slots earlier in the wave's run
+    auto read = [&](int64_t from) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t s = from + (w * PER + i) * 64 + lane;
+            id[i] = s < end ? a.ids[s] : a.G;
+            if ((unsigned)id[i] >= (unsigned)a.G) id[i] = a.G;
+        }
+    };
+    auto tally = [&]() {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const unsigned long long same = same_id(id[i], bits);
+            int n = 0;
+            if (id[i] < a.G) n = count[w][id[i]];  // every lane reads before the first one writes
+            __builtin_amdgcn_wave_barrier();
+            if (id[i] < a.G && (same & below) == 0) count[w][id[i]] = n + __popcll(same);
+            __builtin_amdgcn_wave_barrier();
+            before[i] = n + __popcll(same & below);
+        }
+    };
+    auto clear = [&]() {
+        for (int i = lane; i < a.G; i += 64) count[w][i] = 0;
+    };
+
     if constexpr (COUNT_ONLY) {
-        for (int g = tid; g < a.G; g += kGroupThreads) {
+        clear();
+        for (int64_t from = begin; from < end; from += kGroupSlots) {
+            read(from);
+            tally();
+        }
+        __syncthreads();
+        for (int g = tid; g < a.G; g += NT) {
             int n = 0;
 #pragma unroll
-            for (int i = 0; i < kGroupWaves; ++i) n += count[i][g];
+            for (int i = 0; i < WAVES; ++i) n += count[i][g];
             a.counts[(int64_t)wg * a.G + g] = n;
         }
         return;
     }
 
-    // thread i takes PER consecutive groups: their totals, what earlier
-    // workgroups and earlier waves hold of them, and the sum of all lower ones
-    constexpr int PER = (GMAX + kGroupThreads - 1) / kGroupThreads;
-    int total[PER], before[PER], sum = 0;
+    read(begin);
+    clear();
+    tally();
+    __syncthreads();
+    // thread i takes GROUPS consecutive groups: their totals, what earlier
+    // workgroups hold of them, and the sum of all lower ones
+    int at[GROUPS], total[GROUPS], sum = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int g = tid * PER + i;
-        total[i] = before[i] = 0;
+    for (int i = 0; i < GROUPS; ++i) {
+        const int g = tid * GROUPS + i;
+        total[i] = at[i] = 0;
         if (g < a.G) {
             if (nwg == 1) {
 #pragma unroll
-                for (int j = 0; j < kGroupWaves; ++j) total[i] += count[j][g];
+                for (int j = 0; j < WAVES; ++j) total[i] += count[j][g];
             } else {
                 for (int b = 0; b < nwg; ++b) {
                     const int n = a.counts[(int64_t)b * a.G + g];
                     total[i] += n;
-                    before[i] += b < wg ? n : 0;
+                    at[i] += b < wg ? n : 0;
                 }
             }
         }
@@ -419,35 +482,176 @@ __global__ void __launch_bounds__(kGroupThreads) group_rows(GroupArgs a) {
     int base = upto - sum;
     for (int i = 0; i < w; ++i) base += wave_sum[i];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int g = tid * PER + i;
+    for (int i = 0; i < GROUPS; ++i) {
+        const int g = tid * GROUPS + i;
         if (g >= a.G) break;
         if (wg == 0) {
             a.offsets[g] = base;
             if (g == a.G - 1) a.offsets[a.G] = base + total[i];
         }
-        int at = base + before[i];  // where this workgroup's first slot of g goes
-#pragma unroll
-        for (int j = 0; j < kGroupWaves; ++j) {
-            const int n = count[j][g];
-            count[j][g] = at;
-            at += n;
-        }
+        at[i] += base;
         base += total[i];
     }
-    __syncthreads();
-    for (int64_t s = s0; s < s1; s += 64) {
-        const int id = id_of(s + lane);
-        const unsigned long long same = same_id(id, bits);
-        int at = 0;
-        if (id < a.G) at = count[w][id];  // every lane reads before the first one writes
-        __builtin_amdgcn_wave_barrier();
-        if (id < a.G) {
-            a.rows[at + __popcll(same & below)] = (int)(s + lane);
-            if ((same & below) == 0) count[w][id] = at + __popcll(same);
+    for (int64_t from = begin;;) {
+        // each wave's first place in every group
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const int g = tid * GROUPS + i;
+            if (g >= a.G) break;
+#pragma unroll
+            for (int j = 0; j < WAVES; ++j) {
+                const int n = count[j][g];
+                count[j][g] = at[i];
+                at[i] += n;
+            }
         }
-        __builtin_amdgcn_wave_barrier();
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (id[i] < a.G) a.rows[count[w][id[i]] + before[i]] = (int)(from + (w * PER + i) * 64 + lane);
+        from += kGroupSlots;
+        if (from >= end) break;
+        read(from);
+        clear();  // (the wave's own counts, which it alone has just read)
+        tally();
+        __syncthreads();
     }
+}
+
+// Up to 64 slots (a token or two): one wave, a slot per lane, every place
+// counted from the other lanes' ids.
+__global__ void __launch_bounds__(64) group_few(GroupArgs a) {
+    const int lane = threadIdx.x;
+    int id = a.G;
+    if (lane < a.R) {
+        id = a.ids[lane];
+        if ((unsigned)id >= (unsigned)a.G) id = a.G;
+    }
+    int place = 0;
+    for (int j = 0; j < a.R; ++j) {
+        const int o = at_lane(id, j);
+        place += (o < id || (o == id && j < lane)) ? 1 : 0;
+    }
+    if (id < a.G) a.rows[place] = lane;
+    for (int g = lane; g <= a.G; g += 64) {
+        int n = 0;
+        for (int j = 0; j < a.R; ++j) n += at_lane(id, j) < g ? 1 : 0;
+        a.offsets[g] = n;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A row times its own adapter's U (K x rank), for few rows: a workgroup per row
+// and piece of K, four columns per lane, the lanes of a column group taking k in
+// turn; H holds the pieces' sums, [piece][row][rank].  And back: a wave per row and
+// 256 columns adds alpha h V_g to beta C.
+// ---------------------------------------------------------------------------
+struct ShrinkArgs {
+    int M, K, G, rank, parts;
+    const float *A, *U;
+    int64_t lda, ldu, stride_u;
+    const int *ids, *ranks;
+    float *H;
+};
+
+__global__ void __launch_bounds__(256) shrink_rows(ShrinkArgs a) {
+    __shared__ __attribute__((aligned(16))) float part[256 * 4];
+    const int m = blockIdx.x % a.M, piece = blockIdx.x / a.M;
+    const int id = a.ids[m];
+    if ((unsigned)id >= (unsigned)a.G) return;
+    int rank = a.rank;
+    if (a.ranks != nullptr) {
+        rank = a.ranks[id];
+        rank = rank < 0 ? 0 : (rank > a.rank ? a.rank : rank);
+    }
+    int quads = 1;  // column groups, rounded up to a power of two: at most 64
+    while (4 * quads < rank) quads *= 2;
+    const int tid = threadIdx.x, q = tid % quads, kl = tid / quads, step = 256 / quads;
+    const int k0 = (int)((int64_t)a.K * piece / a.parts), k1 = (int)((int64_t)a.K * (piece + 1) / a.parts);
+    // what lies past the piece's last k reads 0.0 (and columns past the rank, which
+    // go on into the next row, are not written)
+    const rsrc_t ra = whole_rsrc(a.A + (int64_t)m * a.lda + k0, (int64_t)(k1 - k0) * 4);
+    const rsrc_t ru = whole_rsrc(a.U + (int64_t)id * a.stride_u + (int64_t)k0 * a.ldu,
+                                 ((int64_t)(k1 - k0 - 1) * a.ldu + rank) * 4);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (4 * q < rank) {
+        for (int k = kl; k < k1 - k0; k += 8 * step) {  // eight in flight
+            f32x4 u[8];
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t at = (uint32_t)(k + i * step);
+                u[i] = sgk::raw_load_v4f32(ru, (at * (uint32_t)a.ldu + 4u * (uint32_t)q) * 4u, 0, 0);
+                x[i] = sgk::raw_load_f32(ra, at * 4u, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc = fma4(x[i], u[i], acc);
+        }
+    }
+    *reinterpret_cast<float4 *>(&part[4 * tid]) = make_float4(acc.x, acc.y, acc.z, acc.w);
+    for (int half = step / 2; half > 0; half /= 2) {  // pairs, always in the same order
+        __syncthreads();
+        if (kl < half) {
+            float4 &x = *reinterpret_cast<float4 *>(&part[4 * tid]);
+            const float4 y = *reinterpret_cast<const float4 *>(&part[4 * (tid + half * quads)]);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+        }
+    }
+    __syncthreads();
+    if (tid < rank) a.H[((int64_t)piece * a.M + m) * a.rank + tid] = part[tid];
+}
+
+struct ExpandArgs {
+    int M, N, G, rank, parts, chunks;  // chunks of 256 columns
+    float alpha, beta;
+    const float *H, *V, *scales;
+    int64_t ldv, stride_v, ldc;
+    const int *ids, *ranks;
+    float *C;
+};
+
+__global__ void __launch_bounds__(64) expand_rows(ExpandArgs a) {
+    constexpr int DEEP = 16;  // rows of V in flight
+    __shared__ float h[256];
+    const int m = blockIdx.x / a.chunks, lane = threadIdx.x;
+    const int c0 = (int)(blockIdx.x % a.chunks) * 256;  // first column
+    const int id = a.ids[m];
+    int rank = 0;
+    if ((unsigned)id < (unsigned)a.G) {
+        rank = a.rank;
+        if (a.ranks != nullptr) {
+            rank = a.ranks[id];
+            rank = rank < 0 ? 0 : (rank > a.rank ? a.rank : rank);
+        }
+        const float s = a.scales != nullptr ? a.alpha * a.scales[id] : a.alpha;
+        for (int k = lane; k < (rank + DEEP - 1) / DEEP * DEEP; k += 64) {
+            float v = 0.0f;
+            if (k < rank) {
+#pragma unroll 16
+                for (int i = 0; i < a.parts; ++i) v += a.H[((int64_t)i * a.M + m) * a.rank + k];
+            }
+            h[k] = k < rank ? s * v : 0.0f;
+        }
+    }
+    __syncthreads();
+    const int64_t bytes = (int64_t)(a.N - c0) * 4;
+    const uint32_t off = 16u * (uint32_t)lane;
+    const rsrc_t rc = whole_rsrc(a.C + (int64_t)m * a.ldc + c0, bytes);
+    const float *V = a.V + (int64_t)(rank > 0 ? id : 0) * a.stride_v + c0;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.beta != 0.0f) acc = fma4(a.beta, sgk::raw_load_v4f32(rc, off, 0, 0), acc);
+    for (int k = 0; k < rank; k += DEEP) {  // rows past the rank read 0.0, as h does
+        f32x4 v[DEEP];
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+            v[i] = sgk::raw_load_v4f32(whole_rsrc(V + (int64_t)(k + i) * a.ldv, k + i < rank ? bytes : 0), off, 0, 0);
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i) acc = fma4(h[k + i], v[i], acc);
+    }
+    sgk::raw_store_v4f32(acc, rc, off, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -465,71 +669,30 @@ struct CombineArgs {
     int64_t units;
 };
 
-__device__ __forceinline__ f32x4u load4(const float *p, int left) {
-    f32x4u v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (left >= 4) {
-        v = *reinterpret_cast<const f32x4u *>(p);
-    } else {
-        if (left > 0) v.x = p[0];
-        if (left > 1) v.y = p[1];
-        if (left > 2) v.z = p[2];
-    }
-    return v;
-}
-__device__ __forceinline__ void store4(float *p, int left, f32x4u v) {
-    if (left >= 4) {
-        *reinterpret_cast<f32x4u *>(p) = v;
-    } else {
-        if (left > 0) p[0] = v.x;
-        if (left > 1) p[1] = v.y;
-        if (left > 2) p[2] = v.z;
-    }
-}
-// (element by element: no packed FP32 instructions)
-__device__ __forceinline__ f32x4u fma4(float s, f32x4u a, f32x4u c) {
-    f32x4u r;
-    r.x = fmaf(s, a.x, c.x);
-    r.y = fmaf(s, a.y, c.y);
-    r.z = fmaf(s, a.z, c.z);
-    r.w = fmaf(s, a.w, c.w);
-    return r;
-}
-
 __global__ void __launch_bounds__(256) combine(CombineArgs a) {
     const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (unit >= a.units) return;
-    const int t = (int)(unit / a.chunks), chunk = (int)(unit - (int64_t)t * a.chunks);
-    const int c = chunk * 256 + 4 * (int)(threadIdx.x & 63);
-    const int left = a.N - c;
-    if (left <= 0) return;
-    const int64_t s0 = (int64_t)t * a.k;
-    f32x4u acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int t = (int)(unit / a.chunks), c0 = (int)(unit - (int64_t)t * a.chunks) * 256;
+    const int64_t s0 = (int64_t)t * a.k, bytes = (int64_t)(a.N - c0) * 4;
+    const uint32_t off = 16u * (threadIdx.x & 63);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int j0 = 0; j0 < a.k; j0 += 4) {
-        f32x4u y[4];
+        f32x4 y[4];
         float w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            w[j] = 0.0f;
-            y[j] = acc;
-            if (j0 + j < a.k) {
-                const int64_t s = s0 + j0 + j;
-                const bool there = a.ids == nullptr || (unsigned)a.ids[s] < (unsigned)a.E;
-                if (there) {
-                    w[j] = a.weights == nullptr ? 1.0f : a.weights[s];
-                    y[j] = load4(a.Y + s * a.ldy + c, left);
-                } else {
-                    y[j] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
-                }
-            } else {
-                y[j] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
-            }
+            const int64_t s = s0 + (j0 + j < a.k ? j0 + j : 0);
+            const bool there = j0 + j < a.k && (a.ids == nullptr || (unsigned)a.ids[s] < (unsigned)a.E);
+            w[j] = !there ? 0.0f : a.weights == nullptr ? 1.0f : a.weights[s];
+            // a slot that is not there reads 0.0 from an empty descriptor
+            y[j] = sgk::raw_load_v4f32(whole_rsrc(a.Y + s * a.ldy + c0, there ? bytes : 0), off, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc = fma4(w[j], y[j], acc);
     }
-    float *out = a.out + (int64_t)t * a.ldo + c;
-    if (a.beta != 0.0f) acc = fma4(a.beta, load4(out, left), acc);
-    store4(out, left, acc);
+    const rsrc_t ro = whole_rsrc(a.out + (int64_t)t * a.ldo + c0, bytes);
+    if (a.beta != 0.0f) acc = fma4(a.beta, sgk::raw_load_v4f32(ro, off, 0, 0), acc);
+    sgk::raw_store_v4f32(acc, ro, off, 0, 0);
 }
 
 // Its gradient: a workgroup per token, dout read once per eight slots.
@@ -546,7 +709,7 @@ __global__ void __launch_bounds__(256) combine_grad(CombineGradArgs a) {
     __shared__ float part[4][J];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int t = blockIdx.x;
-    const float *dout = a.dout + (int64_t)t * a.ldd;
+    const bool dots = a.dweights != nullptr, rows = a.dY != nullptr;
     for (int j0 = 0; j0 < a.k; j0 += J) {
         const int nj = a.k - j0 < J ? a.k - j0 : J;
         const int64_t s0 = (int64_t)t * a.k + j0;
@@ -558,27 +721,31 @@ __global__ void __launch_bounds__(256) combine_grad(CombineGradArgs a) {
             there[j] = j < nj && (a.ids == nullptr || (unsigned)a.ids[s0 + (j < nj ? j : 0)] < (unsigned)a.E);
             wt[j] = !there[j] ? 0.0f : a.weights == nullptr ? 1.0f : a.weights[s0 + j];
         }
-        for (int c = 4 * tid; c < a.N; c += 1024) {
-            const int left = a.N - c;
-            const f32x4u d = load4(dout + c, left);
+        for (int c0 = 0; c0 < a.N; c0 += 1024) {
+            const int64_t bytes = (int64_t)(a.N - c0) * 4;
+            const uint32_t off = 16u * (uint32_t)tid;
+            const f32x4 d = sgk::raw_load_v4f32(whole_rsrc(a.dout + (int64_t)t * a.ldd + c0, bytes), off, 0, 0);
+            f32x4 y[J];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (j >= nj) break;
-                if (a.dweights != nullptr && there[j]) {
-                    const f32x4u y = load4(a.Y + (s0 + j) * a.ldy + c, left);
-                    dot[j] = fmaf(d.x, y.x, fmaf(d.y, y.y, fmaf(d.z, y.z, fmaf(d.w, y.w, dot[j]))));
-                }
-                if (a.dY != nullptr) {
-                    f32x4u g = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < J; ++j)  // (nothing is read through an empty descriptor)
+                if (dots && j < nj)
+                    y[j] = sgk::raw_load_v4f32(whole_rsrc(a.Y + (s0 + j) * a.ldy + c0, there[j] ? bytes : 0), off, 0, 0);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (rows && j < nj) {
+                    f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f};
                     if (there[j]) {
                         g.x = wt[j] * d.x;
                         g.y = wt[j] * d.y;
                         g.z = wt[j] * d.z;
                         g.w = wt[j] * d.w;
                     }
-                    store4(a.dY + (s0 + j) * a.lddy + c, left, g);
+                    sgk::raw_store_v4f32(g, whole_rsrc(a.dY + (s0 + j) * a.lddy + c0, bytes), off, 0, 0);
                 }
-            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (dots && there[j])
+                    dot[j] = fmaf(d.x, y[j].x, fmaf(d.y, y[j].y, fmaf(d.z, y[j].z, fmaf(d.w, y[j].w, dot[j]))));
         }
         if (a.dweights == nullptr) continue;
 #pragma unroll

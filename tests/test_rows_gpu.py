@@ -427,6 +427,7 @@ ADAPTERS = [
     (1, 1, 1, 1, 1), (1, 64, 32, 3, 4), (1, 257, 130, 2, 16), (3, 33, 65, 5, 7), (16, 100, 96, 16, 8),
     (17, 63, 64, 2, 3), (29, 255, 200, 32, 64), (40, 130, 70, 4, 33), (64, 96, 128, 1, 16), (70, 65, 33, 6, 256),
     (150, 140, 132, 7, 16), (300, 68, 257, 3, 24), (8, 2060, 40, 4, 5), (5, 40, 2100, 3, 12), (260, 300, 64, 200, 8),
+    (64, 33, 700, 64, 40), (65, 200, 4100, 1, 20), (200, 190, 4100, 2, 9), (640, 100, 90, 1, 96), (33, 16500, 48, 9, 50),
 ]
 
 
@@ -506,6 +507,63 @@ def test_adapters_grad(case, full):
             within(dU.read(), ou, su, 1e-5, "dU")
             within(dV.read(), ov, sv, 1e-5, "dV")
         assert (ws[need:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("M,N,K,G,rank", [(8200, 2052, 100, 5, 24), (2048, 8200, 516, 3, 130)])
+def test_adapters_of_many_rows(M, N, K, G, rank):
+    """The tiles that only large products take, against float64 on the GPU."""
+    gu.say("adapters of many rows", M, N, K, G, rank)
+    f, ids, ranks, scales, (U, u), (V, v) = adapter_inputs(M, N, K, G, rank, False)
+    cu = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    a, b, i, r, s, U, V = map(cu, (f(M, K), f(K, N), ids, ranks, scales, U, V))
+    dc = cu(f(M, N))
+    c, da, du, dv = (torch.full(x, NAN, device="cuda") for x in ((M, N), (M, K), (G, K, rank), (G, rank, N)))
+    ws = torch.empty(max(g.sgemm_adapters_workspace_size(M, N, K, G, rank),
+                         g.sgemm_adapters_grad_workspace_size(M, N, K, G, rank)), dtype=torch.uint8, device="cuda")
+    g.sgemm_adapters(M, N, K, 1.25, a, K, b, N, 0.0, c, N, G, rank, i, r, s, U, rank, K * rank, V, N, rank * N, ws)
+    g.sgemm_adapters_grad(M, N, K, 1.25, a, K, b, N, dc, N, G, rank, i, r, s, U, rank, K * rank, V, N, rank * N, 0.0,
+                          da, K, du, rank, K * rank, dv, N, rank * N, ws)
+    torch.cuda.synchronize()
+    a, b, dc, u, v, s = (x.double() for x in (a, b, dc, cu(u), cu(v), s))
+    want, size = a @ b, a.abs() @ b.abs()
+    wa, sa = dc @ b.t(), dc.abs() @ b.t().abs()
+    for e in range(G):
+        m = torch.nonzero(i == e).reshape(-1)
+        h, ha = a[m] @ u[e] * s[e], a[m].abs() @ u[e].abs() * s[e].abs()
+        d, da_ = dc[m] @ v[e].t() * s[e], dc[m].abs() @ v[e].t().abs() * s[e].abs()
+        want[m] += h @ v[e]
+        size[m] += 2 * ha @ v[e].abs()
+        wa[m] += d @ u[e].t()
+        sa[m] += 2 * da_ @ u[e].t().abs()
+        within(du[e].cpu().numpy(), (1.25 * a[m].t() @ d).cpu().numpy(), (2.5 * a[m].t().abs() @ da_).cpu().numpy(), 1e-5, "dU")
+        within(dv[e].cpu().numpy(), (1.25 * h.t() @ dc[m]).cpu().numpy(), (2.5 * ha.t() @ dc[m].abs()).cpu().numpy(), 1e-5, "dV")
+    within(c.cpu().numpy(), 1.25 * want.cpu().numpy(), 1.25 * size.cpu().numpy(), 1e-5, "C")
+    within(da.cpu().numpy(), 1.25 * wa.cpu().numpy(), 1.25 * sa.cpu().numpy(), 1e-5, "dA")
+
+
+@pytest.mark.parametrize("trans", [False, True], ids=["nn", "nt"])
+@pytest.mark.parametrize("R,G,N,K", [(40000, 3, 260, 130), (9000, 70, 515, 70), (20000, 7, 1027, 40)])
+def test_grouped_of_many_rows(R, G, N, K, trans):
+    """The tiles that only many rows take, and the gradients by B, against float64 on the GPU."""
+    gu.say("grouped of many rows", R, G, N, K, trans)
+    gen = torch.Generator(device="cuda").manual_seed(R + trans)
+    ids = torch.randint(-1, G, (R,), generator=gen, device="cuda", dtype=torch.int32)
+    f = lambda *s: torch.rand(*s, generator=gen, device="cuda") * 2 - 1  # noqa: E731
+    a, b = f(R, K), f(G, N, K) if trans else f(G, K, N)
+    c, db = torch.full((R, N), NAN, device="cuda"), torch.full((G, K, N), NAN, device="cuda")
+    off, rows = torch.empty(G + 1, dtype=torch.int32, device="cuda"), torch.empty(R, dtype=torch.int32, device="cuda")
+    ws = torch.empty(g.sgemm_group_rows_workspace_size(R, G), dtype=torch.uint8, device="cuda")
+    g.sgemm_group_rows(R, G, ids, off, rows, ws)
+    g.sgemm_grouped(G, R, N, K, 1.0, a, K, 1, b, b.shape[2], N * K, trans, 0.0, c, N, True, off, rows)
+    y = f(R, N)
+    g.sgemm_grouped_tn(G, R, K, N, 1.0, a, K, 1, y, N, 1, 0.0, db, N, K * N, off, rows)
+    torch.cuda.synchronize()
+    for e in range(G):
+        m = torch.nonzero(ids == e).reshape(-1)
+        x, w, z = a[m].double(), (b[e].t() if trans else b[e]).double(), y[m].double()
+        within(c[m].cpu().numpy(), (x @ w).cpu().numpy(), (x.abs() @ w.abs()).cpu().numpy(), 1e-5, "C")
+        within(db[e].cpu().numpy(), (x.t() @ z).cpu().numpy(), (x.t().abs() @ z.abs()).cpu().numpy(), 1e-5, "dB")
+    assert torch.isnan(c[ids < 0]).all()
 
 
 def test_adapters_without_a_product():
