@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     // K x N: rows from the group's first to K; N x K: from row n0 to the last
     const float *b_base = TRANS_B ? B + (int64_t)n0 * a.ldb : B + n0;
     const int64_t b_bytes = TRANS_B ? ((int64_t)(a.N - n0 - 1) * a.ldb + a.K) * 4 : ((int64_t)(K - 1) * a.ldb + (a.N - n0)) * 4;
+    const uint32_t ldb4 = (uint32_t)a.ldb * 4u;
     constexpr int BL = TRANS_B ? VW : 4;  // loads of B per 16 k
 
     floatx4 acc[MB][VW];
@@ -346,7 +347,6 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
         static_assert(D >= 2, "steps in flight");
         const int last = (K + 16 * H - 1) / (16 * H);
         const int u0 = s0 * (2 / H), u1 = s1 * (2 / H) < last ? s1 * (2 / H) : last;
-        const uint32_t ldb4 = (uint32_t)a.ldb * 4u;
         uint32_t al[L], bl[BL];
 #pragma unroll
         for (int i = 0; i < L; ++i) al[i] = aoff[i] + (uint32_t)(16 * H * lk);
@@ -360,12 +360,19 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
         // A step's place goes into the descriptors (scalar instructions), so the
         // lanes' offsets never change: vector instructions would take the place
         // of MFMAs (with 0.7 of them per MFMA the matrix cores were busy 84% of
-        // the time).  Past the wave's last step that one is read again.
-        auto fetch = [&](int d, int u) {
-            u = u < u1 ? u : u1 - 1;
+        // the time).  Past the wave's last step the descriptors are empty and nothing
+        // is read, in a round of its own behind the loop (37 x 4 rows, 64 groups:
+        // 112 us, 115 with the last step read again); the tall tiles' loops, whose
+        // code is large, read it again (16 x 512 rows: 1080 us, 1103 with the round).
+        constexpr bool AGAIN = MB > 2;
+        auto fetch = [&](int d, int u, bool there) __attribute__((always_inline)) {
+            if constexpr (AGAIN) {
+                u = u < u1 ? u : u1 - 1;
+                there = true;
+            }
             const int64_t k0 = 16 * H * (int64_t)u, b_at = TRANS_B ? k0 : k0 * a.ldb;
-            const rsrc_t rb = whole_rsrc(b_base + b_at, b_bytes - 4 * b_at);
-            const rsrc_t ra = whole_rsrc(a_from + k0, a_bytes - 4 * k0);
+            const rsrc_t rb = whole_rsrc(b_base + b_at, there ? b_bytes - 4 * b_at : 0);
+            const rsrc_t ra = whole_rsrc(a_from + k0, there ? a_bytes - 4 * k0 : 0);
 #pragma unroll
             for (int i = 0; i < BL; ++i)
 #pragma unroll
@@ -415,14 +422,22 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
         // follows it (so does B's as N x K), which is cleared
         const int whole = (int64_t)u1 * 16 * H > K ? u1 - 1 : u1;
 #pragma unroll
-        for (int d = 0; d < D; ++d) fetch(d, u0 + d);
+        for (int d = 0; d < D; ++d) fetch(d, u0 + d, u0 + d < u1);
         int u = u0;
-        for (; u + D <= whole; u += D) {
+        for (; u + (AGAIN ? D : 2 * D) <= (AGAIN ? whole : u1); u += D) {
 #pragma unroll
             for (int d = 0; d < D; ++d) {
                 multiply(d);
-                fetch(d, u + d + D);
+                fetch(d, u + d + D, true);
             }
+        }
+        if (!AGAIN && u + D <= whole) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                multiply(d);
+                fetch(d, u + d + D, u + d + D < u1);
+            }
+            u += D;
         }
 #pragma unroll
         for (int d = 0; d < D; ++d) {

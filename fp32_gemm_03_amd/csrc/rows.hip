@@ -51,9 +51,11 @@ const RouteKernel &route_kernel(int E, int k) {
 }
 
 // ---- products over groups of rows -------------------------------------------
-// The row tiles that groups of R rows in all can need at most.
+// The row tiles that groups of R rows in all can need at most: one for each
+// group's first row and one for every further bm rows.
 long long row_tiles(const GroupedArgs &a, int bm) {
-    return a.R / bm + (a.offsets == nullptr ? 1 : (a.G < a.R ? a.G : a.R));
+    const long long groups = a.offsets == nullptr ? 1 : (a.G < a.R ? a.G : a.R);
+    return (a.R - groups) / bm + groups;
 }
 
 typedef void (*GroupedFn)(GroupedArgs);
@@ -68,24 +70,38 @@ bool within_reach(long long rows, int div, int ld, long long tile_rows) {
 
 struct Block {
     int bm, bn, threads;
-    GroupedFn nn, nt;
+    GroupedFn fn;
 };
-#define THIN(MB, VW, WK, WN, WPE) \
-    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, rowk::thin<MB, VW, WK, WN, WPE, true>}
-// rows x columns of a tile; waves over K x waves over columns
-const Block kTall = THIN(4, 4, 2, 2, 2);      // 64 x 128, 2 x 2
-const Block kTallDeep = THIN(4, 4, 4, 1, 2);  // 64 x 64, 4 x 1
-const Block kLow = THIN(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
-const Block kLowFlat = THIN(2, 4, 1, 1, 4);   // 32 x 64, one wave
-const Block kNarrow = THIN(2, 2, 4, 1, 4);    // 32 x 32, 4 x 1
-const Block kNarrower = THIN(2, 1, 4, 1, 4);  // 32 x 16, 4 x 1
+#define THIN_NN(MB, VW, WK, WN, WPE) \
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>}
+#define THIN_NT(MB, VW, WK, WN, WPE) \
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, true>}
+// rows x columns of a tile; waves over K x waves over columns.  B as K x N:
+const Block kTall = THIN_NN(4, 4, 2, 2, 2);      // 64 x 128, 2 x 2
+const Block kLow = THIN_NN(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
+const Block kLowFlat = THIN_NN(2, 4, 1, 1, 4);   // 32 x 64, one wave
+const Block kNarrow = THIN_NN(2, 2, 4, 1, 4);    // 32 x 32, 4 x 1
+const Block kLeast = THIN_NN(1, 2, 4, 1, 4);     // 16 x 32, 4 x 1
+const Block kSquare = THIN_NN(1, 1, 4, 1, 4);    // 16 x 16, 4 x 1
+// and as N x K:
+const Block kTallT = THIN_NT(4, 4, 4, 1, 2);     // 64 x 64, 4 x 1
+const Block kLowT = THIN_NT(2, 4, 4, 1, 4);      // 32 x 64, 4 x 1
+const Block kLowFlatT = THIN_NT(2, 4, 1, 1, 4);  // 32 x 64, one wave
+const Block kNarrowT = THIN_NT(2, 1, 4, 1, 4);   // 32 x 16, 4 x 1
+const Block kSquareT = THIN_NT(1, 1, 4, 1, 4);   // 16 x 16, 4 x 1
 
 // Measured (us; groups x rows in all, N x K):
 //   K up to 64: one wave per tile, nothing to split (11 x 4096, 4096 x 32:
 //     24 against 44 on four waves).
-//   Few tiles of 32 x 64: narrower columns, so that more CUs read B (one row, 4096
-//     x 4096: 14.4 at 32 columns and 20.6 at 64; B as N x K, where a narrow tile's
-//     lines are still whole, 13.5 at 16 and 20.1 at 32).
+//   So few tiles that each has a CU to itself (256 of them): 16 rows (9 x 2000, 16 x
+//     1024: 5.9 on 16 x 16 against 9.6 on 32 x 32; 4 x 3000, 32 x 2048: 10.9 on
+//     16 x 32 against 15.4; with more tiles they lose: 11 x 4096, 32 x 2048: 19.1
+//     against 15.8).  16 columns only where B is read for several row tiles
+//     anyway: its lines are 128 bytes (16 x 2, 1024 x 2048: 9.5 against 8.8 on
+//     32 columns), or no more are there (9 x 20000, 16 x 1024: 20.6 against 28).
+//   Fewer than 256 tiles of 32 x 64: narrower columns, so that more CUs read B (one
+//     row, 4096 x 4096: 14.4 at 32 columns and 20.6 at 64; B as N x K, where a
+//     narrow tile's lines are still whole, 13.5 at 16 and 20.1 at 32).
 //   Many rows per group: 64 rows, read fewer times (16 x 8192, 4096 x 2048: 1024
 //     against 1100 on 32 rows; N x K 1110 against 1494), for K x N only where
 //     64 x 128 tiles fill the chip often enough (8 x 4022, 2048 x 1024, 1100 tiles:
@@ -93,9 +109,18 @@ const Block kNarrower = THIN(2, 1, 4, 1, 4);  // 32 x 16, 4 x 1
 //   Else 32 x 64 with four waves over K (64 x 136, 1280 x 2048: 112, 5.4 TB/s).
 const Block &choose_block(const GroupedArgs &a, bool trans_b) {
     const long long groups = a.offsets == nullptr ? 1 : a.G;
+    const long long squares = row_tiles(a, 16) * ceil_div(a.N, 16);
+    const bool few = row_tiles(a, 32) * ceil_div(a.N, 64) < 256;
+    if (trans_b) {
+        if (a.K <= 64) return kLowFlatT;
+        if (squares <= 256) return kSquareT;
+        if (few) return kNarrowT;
+        return a.R > 64 * groups ? kTallT : kLowT;
+    }
     if (a.K <= 64) return kLowFlat;
-    if (row_tiles(a, 32) * ceil_div(a.N, 64) < 256) return trans_b ? kNarrower : kNarrow;
-    if (trans_b) return a.R > 64 * groups ? kTallDeep : kLow;
+    if (a.N <= 16 || (squares <= 256 && a.R > 16 * groups)) return kSquare;
+    if (row_tiles(a, 16) * ceil_div(a.N, 32) <= 256) return kLeast;
+    if (few) return kNarrow;
     return row_tiles(a, 64) * ceil_div(a.N, 128) >= 2048 && a.R > 64 * groups ? kTall : kLow;
 }
 
@@ -109,11 +134,11 @@ int xcd_shift(long long columns) {
     return columns < xcds ? 0 : shift;
 }
 
-int launch_block(const Block &b, GroupedFn fn, bool dealt, GroupedArgs a, hipStream_t stream) {
+int launch_block(const Block &b, bool dealt, GroupedArgs a, hipStream_t stream) {
     a.xcd_shift = dealt ? xcd_shift(ceil_div(a.N, b.bn)) : 0;
     // every XCD's share of the tile columns, rounded up in every row of tiles
     const long long columns = ceil_div(ceil_div(a.N, b.bn), 1LL << a.xcd_shift) << a.xcd_shift;
-    return enqueue(fn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
+    return enqueue(b.fn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
 }
 
 int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
@@ -124,9 +149,9 @@ int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
     const bool reach = within_reach(a.R, a.a_div, a.lda, 256) &&
                        (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
-    const Block simple = {32, 32, 256, rowk::grouped_simple<false>, rowk::grouped_simple<true>};
-    const Block &b = reach ? choose_block(a, trans_b) : simple;
-    return launch_block(b, trans_b ? b.nt : b.nn, reach, a, stream);
+    if (reach) return launch_block(choose_block(a, trans_b), true, a, stream);
+    const Block simple = {32, 32, 256, trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>};
+    return launch_block(simple, false, a, stream);
 }
 
 struct BlockTN {
@@ -569,8 +594,8 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h);
     int rc;
-    // (a piece of U within 32-bit offsets)
-    if (M <= kFewRows && ceil_div(K, shrink_parts(K)) + 1 <= kReach / 4 / ldu) {
+    // (a piece of U within 32-bit offsets, with the steps that overrun its end)
+    if (M <= kFewRows && ceil_div(K, shrink_parts(K)) + 8 * 256 <= kReach / 4 / ldu) {
         rowk::ShrinkArgs h;
         h.M = M;
         h.K = K;

@@ -23,16 +23,21 @@ using sgk::rsrc_t;
 // A descriptor over [base, base + bytes), at most kOut bytes; an access at
 // kOut is outside every one (and its 16 bytes do not wrap).
 constexpr uint32_t kOut = 0xfffffff0u;
+__device__ __forceinline__ uint32_t records(int64_t bytes) {
+    return bytes <= 0 ? 0u : (bytes >= (int64_t)kOut ? kOut : (uint32_t)bytes);
+}
+__device__ __forceinline__ rsrc_t exact_rsrc(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, sgk::kRsrcWord3);
+}
 __device__ __forceinline__ rsrc_t whole_rsrc(const void *base, int64_t bytes) {
-    const uint32_t n = bytes <= 0 ? 0u : (bytes >= (int64_t)kOut ? kOut : (uint32_t)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, sgk::kRsrcWord3);
+    return exact_rsrc(base, records(bytes));
 }
 
 // ---------------------------------------------------------------------------
 // Lane exchange inside a 16-lane DPP row and across a wave's four rows.
 // ---------------------------------------------------------------------------
 template <int CTRL> __device__ __forceinline__ int dpp(int v) {
-    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false);
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(dpp<CTRL>(__float_as_int(v)));
@@ -124,9 +129,11 @@ struct RouteArgs {
     float *weights;
 };
 
-// exp(x - m) with m the row's maximum; equal values (infinities too) give 1
-__device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
-__device__ __forceinline__ double exp_below(double x, double m) { return x == m ? 1.0 : exp(x - m); }
+// exp(x - m) with m the row's maximum; equal values (infinities too) give 1.
+// (No branches here or below: around each element they kept the elements' loads
+// and exponentials from overlapping.)
+__device__ __forceinline__ float exp_below(float x, float m) { return expf(x == m ? 0.0f : x - m); }
+__device__ __forceinline__ double exp_below(double x, double m) { return exp(x == m ? 0.0 : x - m); }
 
 constexpr int kRouteThreads = 256;
 
@@ -143,13 +150,21 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
     const bool in = t < a.T;
     const float *row = a.logits + (int64_t)(in ? t : 0) * a.ldl;
 
-    float x[V];
+    float x[V], bias[V];
     float top = -INFINITY;
     bool nan = false;
 #pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = row[l + L * v < a.E ? l + L * v : 0];
+    if (WIDE && a.bias != nullptr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = a.bias[l + L * v < a.E ? l + L * v : 0];
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = 0.0f;
+    }
+#pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = l + L * v;
-        x[v] = in && e < a.E ? row[e] : -INFINITY;
+        x[v] = in && l + L * v < a.E ? x[v] : -INFINITY;
         nan |= x[v] != x[v];
         top = fmaxf(top, x[v]);  // a NaN is passed over
     }
@@ -159,28 +174,33 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
     Key key[V];
     double total = 0.0;
     if constexpr (WIDE) {
-        if (!a.sigmoid) {
+        if (a.sigmoid) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+        } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 key[v] = exp_below((double)x[v], (double)top);
-                if (!(x[v] > -INFINITY)) key[v] = 0.0;
+                key[v] = x[v] > -INFINITY ? key[v] : 0.0;
                 total += key[v];
             }
             total = reduce<L>(total, Add());
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] /= total;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = l + L * v;
-            double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[v])) : key[v] / total;
-            if (a.bias != nullptr && e < a.E) s += (double)a.bias[e];
+            const double s = key[v] + (double)bias[v];
             key[v] = x[v] > -INFINITY && s == s ? s : NONE;
         }
     } else {
         if (!a.sigmoid && !a.renorm) {
             float sum = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (x[v] > -INFINITY) sum += exp_below(x[v], top);
+            for (int v = 0; v < V; ++v) {
+                const float p = exp_below(x[v], top);
+                sum += x[v] > -INFINITY ? p : 0.0f;
+            }
             total = (double)reduce<L>(sum, Add());
         }
 #pragma unroll
@@ -188,22 +208,43 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
     }
 
     if (a.groups > 1) {
-        // each group's worth, one lane per group from the keys in LDS; a group
-        // is kept when fewer than top_groups are worth more (or as much, with a
-        // lower index)
+        // each group's worth from the keys in LDS: the row's lanes together, group
+        // after group, or one lane per group where a group has fewer elements than
+        // the row has lanes; a group is kept when fewer than top_groups are worth
+        // more (or as much, with a lower index)
         const int per = a.E / a.groups;
 #pragma unroll
         for (int v = 0; v < V; ++v) keys[r][l + L * v] = key[v];
         __syncthreads();
-        for (int g = l; g < a.groups; g += L) {
-            Key b0 = NONE, b1 = NONE;
-            for (int i = 0; i < per; ++i) {
-                const Key q = keys[r][g * per + i];
-                b1 = q > b0 ? b0 : (q > b1 ? q : b1);
-                b0 = q > b0 ? q : b0;
+        // the two highest of two pairs, b0 >= b1 and q0 >= q1
+        auto join = [](Key &b0, Key &b1, Key q0, Key q1) {
+            b1 = fmax(fmin(b0, q0), fmax(b1, q1));
+            b0 = fmax(b0, q0);
+        };
+        // (no sum where the second is missing: -inf counts nothing)
+        auto value = [&](Key b0, Key b1) { return a.group_best == 2 && b1 > NONE ? b0 + b1 : b0; };
+        if (per >= L) {
+            for (int g = 0; g < a.groups; ++g) {
+                Key b0 = NONE, b1 = NONE;
+                for (int i = l; i < per; i += L) join(b0, b1, keys[r][g * per + i], NONE);
+                join(b0, b1, dpp<0x128>(b0), dpp<0x128>(b1));
+                join(b0, b1, dpp<0x124>(b0), dpp<0x124>(b1));
+                join(b0, b1, dpp<0x122>(b0), dpp<0x122>(b1));
+                join(b0, b1, dpp<0x121>(b0), dpp<0x121>(b1));
+                if constexpr (L == 64) {
+                    Key c0 = at_lane(b0, 0), c1 = at_lane(b1, 0);
+                    for (int i = 16; i < 64; i += 16) join(c0, c1, at_lane(b0, i), at_lane(b1, i));
+                    b0 = c0;
+                    b1 = c1;
+                }
+                if (l == 0) worth[r][g] = value(b0, b1);
             }
-            // (no sum where the second is missing: -inf counts nothing)
-            worth[r][g] = a.group_best == 2 && b1 > NONE ? b0 + b1 : b0;
+        } else {
+            for (int g = l; g < a.groups; g += L) {
+                Key b0 = NONE, b1 = NONE;
+                for (int i = 0; i < per; ++i) join(b0, b1, keys[r][g * per + i], NONE);
+                worth[r][g] = value(b0, b1);
+            }
         }
         __syncthreads();
         for (int g = l; g < a.groups; g += L) {
@@ -218,25 +259,23 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = l + L * v;
+            const int e = l + L * v < a.E ? l + L * v : 0;  // (past E there is nothing anyway)
             // exact: e < 1024, and (e + 1/2) / per is at least 1 / (2 per) from a whole number
             const int g = (int)(((float)e + 0.5f) * a.inv_per);
-            if (e < a.E && !kept[r][g]) key[v] = NONE;
+            key[v] = kept[r][g] ? key[v] : NONE;
         }
     }
 
     int mine = -1;  // lane j keeps choice j
     for (int j = 0; j < a.k; ++j) {
-        Key best = NONE;
+        Key best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = fmax(best, key[v]);
+        const Key most = reduce<L>(best, Max());
         int at = INT_MAX;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = l + L * v;
-            }
-        const Key most = reduce<L>(best, Max());
-        const int first = reduce<L>(best == most && most > NONE ? at : INT_MAX, Min());
+        for (int v = V - 1; v >= 0; --v) at = key[v] == most ? l + L * v : at;
+        const int first = reduce<L>(most > NONE ? at : INT_MAX, Min());
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (l + L * v == first) key[v] = NONE;
