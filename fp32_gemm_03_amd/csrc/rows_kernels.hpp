@@ -119,6 +119,10 @@ template <class V> __device__ __forceinline__ V fma4(float s, V a, V c) {
 // rise with the logits, and those are compared as they are.  The chosen
 // weights are computed in 64 bits either way (one lane per choice) and rounded
 // once.
+//
+// The instructions issued bound it where there is a bias: 8191 x 256 with 8 groups
+// takes 11.4 us (8.4 MB of logits: 2), of which the 64-bit exponentials and the 8
+// rounds are a third each.  16384 x 64 without: 4.4 us, of which 2.2 are the launch.
 // ---------------------------------------------------------------------------
 struct RouteArgs {
     int T, E, k, sigmoid, groups, top_groups, group_best, renorm;
@@ -137,14 +141,50 @@ __device__ __forceinline__ double exp_below(double x, double m) { return exp(x =
 
 constexpr int kRouteThreads = 256;
 
+// A key that stands for nothing, and taking a key out: of a double the upper
+// half alone is replaced, which leaves at most -1.79e308.
+template <class Key> constexpr Key kNothing = -INFINITY;
+template <> constexpr double kNothing<double> = -1.79e308;
+__device__ __forceinline__ bool something(float key) { return key > -INFINITY; }
+__device__ __forceinline__ bool something(double key) { return key > -1.78e308; }
+__device__ __forceinline__ void take_out(float &key, bool it) { key = it ? -INFINITY : key; }
+__device__ __forceinline__ void take_out(double &key, bool it) {
+    key = __hiloint2double(it ? (int)0xffefffff : __double2hiint(key), __double2loint(key));
+}
+
+// k rounds of an arg-max over the L V keys of a row, element l + L v in register
+// v of lane l; lane j keeps the j-th choice, or -1.
+template <int L, int V, class Key> __device__ __forceinline__ int choose(Key (&key)[V], int k, int l) {
+    int mine = -1;
+    for (int j = 0; j < k; ++j) {
+        Key best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = fmax(best, key[v]);
+        const Key most = reduce<L>(best, Max());
+        int at[V];  // (apart, so that no compare waits for the select before it)
+#pragma unroll
+        for (int v = 0; v < V; ++v) at[v] = key[v] == most ? l + L * v : INT_MAX;
+#pragma unroll
+        for (int n = V; n > 1; n = (n + 1) / 2)
+#pragma unroll
+            for (int v = 0; v < n / 2; ++v) at[v] = Min()(at[v], at[n - 1 - v]);
+        const int first = reduce<L>(something(most) ? at[0] : INT_MAX, Min());
+#pragma unroll
+        for (int v = 0; v < V; ++v) take_out(key[v], l + L * v == first);
+        if (l == j) mine = first == INT_MAX ? -1 : first;
+    }
+    return mine;
+}
+
 template <int L, int V, bool WIDE>
 __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
     typedef typename std::conditional<WIDE, double, float>::type Key;
     constexpr int ROWS = kRouteThreads / L;
-    const Key NONE = -INFINITY;
-    __shared__ Key keys[ROWS][L * V + 1];
-    __shared__ Key worth[ROWS][L * V < 64 ? L * V : 64];
-    __shared__ int kept[ROWS][L * V < 64 ? L * V : 64];
+    constexpr Key NONE = kNothing<Key>;
+    constexpr int GROUPS = L * V < 64 ? L * V : 64;  // at most
+    __shared__ Key keys[ROWS][L * V + L * V / 32 + 1];
+    __shared__ Key worth[ROWS][GROUPS];
+    __shared__ int kept[ROWS][GROUPS];
     const int l = threadIdx.x % L, r = threadIdx.x / L;
     const int t = (int)blockIdx.x * ROWS + r;
     const bool in = t < a.T;
@@ -191,7 +231,7 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const double s = key[v] + (double)bias[v];
-            key[v] = x[v] > -INFINITY && s == s ? s : NONE;
+            key[v] = x[v] > -INFINITY && s > NONE ? s : NONE;  // (neither NaN nor -inf)
         }
     } else {
         if (!a.sigmoid && !a.renorm) {
@@ -207,26 +247,28 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
         for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? x[v] : NONE;
     }
 
+    int mine;  // lane j keeps choice j
     if (a.groups > 1) {
-        // each group's worth from the keys in LDS: the row's lanes together, group
-        // after group, or one lane per group where a group has fewer elements than
-        // the row has lanes; a group is kept when fewer than top_groups are worth
-        // more (or as much, with a lower index)
+        // Each group's worth from the keys in LDS: a lane per group (the rows of 32
+        // keys a bank apart), or the row's lanes together where groups are long.  A
+        // group is kept when fewer than top_groups are worth more (or as much, with
+        // a lower index).
         const int per = a.E / a.groups;
+        auto place = [](int e) { return e + (e >> 5); };
 #pragma unroll
-        for (int v = 0; v < V; ++v) keys[r][l + L * v] = key[v];
+        for (int v = 0; v < V; ++v) keys[r][place(l + L * v)] = key[v];
         __syncthreads();
         // the two highest of two pairs, b0 >= b1 and q0 >= q1
         auto join = [](Key &b0, Key &b1, Key q0, Key q1) {
             b1 = fmax(fmin(b0, q0), fmax(b1, q1));
             b0 = fmax(b0, q0);
         };
-        // (no sum where the second is missing: -inf counts nothing)
-        auto value = [&](Key b0, Key b1) { return a.group_best == 2 && b1 > NONE ? b0 + b1 : b0; };
-        if (per >= L) {
+        // (no sum where the second is missing)
+        auto value = [&](Key b0, Key b1) { return a.group_best == 2 && something(b1) ? b0 + b1 : b0; };
+        if (per > 4 * L) {
             for (int g = 0; g < a.groups; ++g) {
                 Key b0 = NONE, b1 = NONE;
-                for (int i = l; i < per; i += L) join(b0, b1, keys[r][g * per + i], NONE);
+                for (int i = l; i < per; i += L) join(b0, b1, keys[r][place(g * per + i)], NONE);
                 join(b0, b1, dpp<0x128>(b0), dpp<0x128>(b1));
                 join(b0, b1, dpp<0x124>(b0), dpp<0x124>(b1));
                 join(b0, b1, dpp<0x122>(b0), dpp<0x122>(b1));
@@ -242,11 +284,17 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
         } else {
             for (int g = l; g < a.groups; g += L) {
                 Key b0 = NONE, b1 = NONE;
-                for (int i = 0; i < per; ++i) join(b0, b1, keys[r][g * per + i], NONE);
+#pragma unroll 8
+                for (int i = 0; i < per; ++i) {
+                    const Key q = keys[r][place(g * per + i)];
+                    b1 = fmax(b1, fmin(b0, q));
+                    b0 = fmax(b0, q);
+                }
                 worth[r][g] = value(b0, b1);
             }
         }
         __syncthreads();
+        // the kept groups in their order, and with them their elements
         for (int g = l; g < a.groups; g += L) {
             const Key w = worth[r][g];
             int above = 0;
@@ -257,29 +305,40 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
             kept[r][g] = above < a.top_groups ? 1 : 0;
         }
         __syncthreads();
+        int place_of[GROUPS / L > 0 ? GROUPS / L : 1];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = l + L * v < a.E ? l + L * v : 0;  // (past E there is nothing anyway)
-            // exact: e < 1024, and (e + 1/2) / per is at least 1 / (2 per) from a whole number
-            const int g = (int)(((float)e + 0.5f) * a.inv_per);
-            key[v] = kept[r][g] ? key[v] : NONE;
+        for (int i = 0; i < GROUPS / L; ++i) {
+            int n = 0;
+            for (int h = 0; h < l + L * i && h < a.groups; ++h) n += kept[r][h];
+            place_of[i] = l + L * i < a.groups && kept[r][l + L * i] ? n : -1;
         }
-    }
-
-    int mine = -1;  // lane j keeps choice j
-    for (int j = 0; j < a.k; ++j) {
-        Key best = key[0];
+        __syncthreads();
 #pragma unroll
-        for (int v = 1; v < V; ++v) best = fmax(best, key[v]);
-        const Key most = reduce<L>(best, Max());
-        int at = INT_MAX;
+        for (int i = 0; i < GROUPS / L; ++i)
+            if (place_of[i] >= 0) kept[r][place_of[i]] = l + L * i;
+        __syncthreads();
+        const int count = a.top_groups * per;
+        auto element = [&](int i) {
+            // exact: i < 1024, and (i + 1/2) / per is at least 1 / (2 per) from a whole number
+            const int q = (int)(((float)i + 0.5f) * a.inv_per);
+            return kept[r][q] * per + (i - q * per);
+        };
+        auto some = [&](auto registers) __attribute__((always_inline)) {
+            constexpr int VV = decltype(registers)::value;
+            Key left[VV];
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v) at = key[v] == most ? l + L * v : at;
-        const int first = reduce<L>(most > NONE ? at : INT_MAX, Min());
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (l + L * v == first) key[v] = NONE;
-        if (l == j) mine = first == INT_MAX ? -1 : first;
+            for (int v = 0; v < VV; ++v) {
+                const int i = l + L * v;
+                const Key q = keys[r][place(element(i < count ? i : 0))];
+                left[v] = i < count ? q : NONE;
+            }
+            return choose<L>(left, a.k, l);
+        };
+        if (count <= L * (V / 2)) mine = some(std::integral_constant<int, V / 2 ? V / 2 : 1>());
+        else mine = some(std::integral_constant<int, V>());
+        if (mine >= 0) mine = element(mine);
+    } else {
+        mine = choose<L>(key, a.k, l);
     }
 
     const bool found = mine >= 0;
