@@ -560,7 +560,9 @@ size_t sgemm_adapters_workspace_size(int M, int N, int K, int G, int rank) {
 
 size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank) {
     if (M < 0 || N < 0 || K < 0 || G < 1 || G > SGEMM_MAX_GROUPS || rank < 1 || rank > SGEMM_MAX_RANK) return 0;
-    return AdapterSpace(M, N, K, G, rank, true).end;
+    // (at least the forward's, so that a training step keeps one workspace)
+    const size_t forward = AdapterSpace(M, N, K, G, rank, false).end, back = AdapterSpace(M, N, K, G, rank, true).end;
+    return forward > back ? forward : back;
 }
 
 int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta,
@@ -679,7 +681,8 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
     NEED(29, lddv >= (N > 1 ? N : 1));
     NEED(30, G == 1 || N == 0 || stride_dv >= (long long)(rank - 1) * lddv + N);
     const AdapterSpace at(M, N, K, G, rank, true);
-    if (!workspace_ok(workspace, workspace_bytes, at.end)) return SGEMM_ERR_WORKSPACE;
+    if (!workspace_ok(workspace, workspace_bytes, sgemm_adapters_grad_workspace_size(M, N, K, G, rank)))
+        return SGEMM_ERR_WORKSPACE;
     char *w = static_cast<char *>(workspace);
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h), *dH = reinterpret_cast<float *>(w + at.dh);

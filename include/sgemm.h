@@ -523,7 +523,8 @@ size_t sgemm_adapters_workspace_size(int M, int N, int K, int G, int rank);
  * (rank x N) are written whole for every g, with no contribution beyond
  * ranks[g] and for adapters no row uses.  dA, or dU and dV together, may be
  * NULL (not wanted).  Workspace as above, at least
- * sgemm_adapters_grad_workspace_size() bytes. */
+ * sgemm_adapters_grad_workspace_size() bytes, which are at least
+ * sgemm_adapters_workspace_size()'s: a training step needs one of them. */
 int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
                         const float *dC, int lddc, int G, int rank, const int *ids, const int *ranks,
                         const float *scales, const float *U, int ldu, long long stride_u, const float *V,

@@ -163,6 +163,15 @@ def test_adapters_grad_refuses(bad, position):
     refuse(g.sgemm_adapters_grad, AGRAD, bad, position)
 
 
+@pytest.mark.parametrize("M", [0, 1, 29, 64, 65, 512, 513, 2011, 40000])
+def test_one_adapters_workspace_for_a_training_step(M):
+    for N in (1, 64, 1037, 4096):
+        for K in (1, 100, 4096, 20000):
+            for G, rank in ((1, 1), (7, 16), (64, 255)):
+                assert (g.sgemm_adapters_grad_workspace_size(M, N, K, G, rank)
+                        >= g.sgemm_adapters_workspace_size(M, N, K, G, rank) > 0)
+
+
 def test_adapters_refuse_a_workspace():
     for fn, base, size in ((g.sgemm_adapters, ADAPT, g.sgemm_adapters_workspace_size),
                            (g.sgemm_adapters_grad, AGRAD, g.sgemm_adapters_grad_workspace_size)):
