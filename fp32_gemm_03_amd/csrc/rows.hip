@@ -159,15 +159,34 @@ struct BlockTN {
     GroupedFn fn;
 };
 #define OUTER(VM, VN, WK, WPE) {16 * VM, 16 * VN, WK * 64, rowk::outer<VM, VN, WK, WPE>}
-const BlockTN kOuter = OUTER(4, 4, 1, 2), kOuterDeep = OUTER(4, 4, 4, 2);
-const BlockTN kOuterLow = OUTER(1, 4, 4, 4), kOuterNarrow = OUTER(4, 1, 4, 4);
+// rows x columns of a tile; waves over the slots
+const BlockTN kOuter = OUTER(4, 4, 1, 2);           // 64 x 64, one wave
+const BlockTN kOuterDeep = OUTER(4, 4, 4, 2);       // 64 x 64, 4
+const BlockTN kSlim[2] = {OUTER(4, 1, 4, 4), OUTER(1, 4, 4, 4)};      // 64 x 16 and 16 x 64, 4
+const BlockTN kSlimDeep[2] = {OUTER(4, 1, 8, 4), OUTER(1, 4, 8, 4)};  // the same, 8
+const BlockTN kSlimLow[2] = {OUTER(2, 1, 8, 4), OUTER(1, 2, 8, 4)};   // 32 x 16 and 16 x 32, 8
+const BlockTN kOuterLeast = OUTER(1, 1, 16, 4);     // 16 x 16, 16
 
-// 64 x 64 tiles, each of one wave where they fill the chip and of four that share
-// the slots below; 16 rows or columns (an adapter's rank) take tiles of 16.
+// Each group's slots are summed by the waves of one workgroup, so the fewer tiles
+// there are, the narrower they are and the more waves share the slots.  Measured
+// (us; groups x slots in all, M x N):
+//   1024 tiles of 64 x 64 and more: one wave each (1 x 300, 4096 x 4096: 88 against
+//     128 on four); from 256 four waves (2 x 3000, 1024 x 1024: 55 against 71 on
+//     64 x 16; with 144 tiles, 768 x 768, 58 against 48).
+//   Then 64 x 16 along the longer side (16 x 2000, 4096 x 16: 9.7 on four waves, 14.3
+//     on eight; 1 x 8192, 64 x 4096, long and 256 tiles: 57 on four, 49 on eight;
+//     3 x 900, 4096 x 16, 192 tiles: 5.8 against 7.4 on 32 x 16).
+//   Up to 128 of them: 32 x 16 on eight waves (1 x 16000, 8192 x 16: 110 against 131;
+//     1 x 2000, 2048 x 64: 10 against 15 on four waves of 64 x 16).
+//   Both sides short: 16 x 16 on 16 waves (1 x 4000, 128 x 128: 9.9 against 16, and
+//     68 on 64 x 64; 256 x 256: 16 against 20).
 const BlockTN &choose_tn(const GroupedArgs &a) {
-    if (a.M <= 32) return kOuterLow;
-    if (a.N <= 32) return kOuterNarrow;
-    return a.G * ceil_div(a.M, 64) * ceil_div(a.N, 64) >= 1024 ? kOuter : kOuterDeep;
+    const int longer = a.M >= a.N ? a.M : a.N, shorter = a.M >= a.N ? a.N : a.M, turned = a.M >= a.N ? 0 : 1;
+    const long long tiles = a.G * ceil_div(longer, 64) * ceil_div(shorter, 64);
+    if (shorter > 32 && tiles >= 256) return tiles >= 1024 ? kOuter : kOuterDeep;
+    const long long slim = a.G * ceil_div(longer, 64) * ceil_div(shorter, 16);
+    if (slim > 128) return slim < 512 && a.R >= 512LL * a.G ? kSlimDeep[turned] : kSlim[turned];
+    return shorter > 32 && slim <= 64 ? kOuterLeast : kSlimLow[turned];
 }
 
 int grouped_tn(GroupedArgs a, hipStream_t stream) {

@@ -296,6 +296,58 @@ def test_grouped_tn(case, divs):
         within(C.read(), want, size, 1e-5, "C")
 
 
+# tiles of every form the sums of outer products take: rows per group, M, N
+OUTER = [
+    ([1, 0, 3] * 43, 260, 300), ([90] * 7, 390, 321),  # 64 x 64 on one wave, on four
+    ([40] * 9, 1000, 61), ([40] * 9, 61, 1000), ([300, 0] * 6, 643, 16), ([17] * 14, 7, 701),  # 64 x 16 on four
+    ([1100], 1027, 250), ([1300, 700], 250, 515), ([0, 1600, 2], 64, 900),  # 64 x 16 on eight
+    ([1, 50, 333], 130, 33), ([33, 2], 20, 515), ([700], 900, 3), ([0, 0], 70, 5),  # 32 x 16
+    ([900], 33, 200), ([5, 0, 261], 65, 64), ([256], 100, 100),  # 16 x 16
+]
+
+
+@pytest.mark.parametrize("case", OUTER, ids=lambda c: f"{len(c[0])}g{sum(c[0])}r{c[1]}x{c[2]}")
+def test_grouped_tn_tiles(case):
+    sizes, M, N = case
+    gu.say("grouped_tn tiles", case)
+    R, G, offsets, rows, _, f = grouped_case(sizes, 3, N, M, 1, 1, 3)
+    a, b, c0 = f(R, M), f(-(-R // 2), N), f(G, M, N)
+    off, rw = Buffer(offsets), Buffer(rows)
+    for alpha, beta, pad, mis in ((1.0, 0.0, 0, 0), (-1.5, 0.5, 3, 1)):
+        A, B = Buffer(a, M + pad, mis), Buffer(b, N + pad, mis)
+        C = Buffer(c0 if beta != 0 else np.full_like(c0, np.nan), N + pad, mis, stride=M * (N + pad) + 5 * pad)
+        g.sgemm_grouped_tn(G, R, M, N, alpha, A.ptr, A.ld, 1, B.ptr, B.ld, 2, beta, C.ptr, C.ld, C.stride, off.ptr, rw.ptr)
+        torch.cuda.synchronize()
+        want, size = ro.grouped_tn(offsets, rows, alpha, a, 1, b, 2, beta, c0)
+        within(C.read(), want, size, 1e-5, "C")
+
+
+# and those of the products: rows per group, N, K
+TILES = [
+    ([33, 0, 50], 16, 400), ([200, 17], 40, 130), ([5] * 12, 64, 300),  # 16 x 16, 16 x 32
+    ([2600, 1700], 16, 70), ([1500, 900], 64, 90),  # more of them, 32 x 32
+    ([90, 0, 70] * 7, 700, 66), ([20] * 40, 450, 100), ([700] * 3, 1500, 80),  # 32 x 64, 64 rows
+]
+
+
+@pytest.mark.parametrize("trans", [False, True], ids=["nn", "nt"])
+@pytest.mark.parametrize("case", TILES, ids=lambda c: f"{len(c[0])}g{sum(c[0])}r{c[1]}x{c[2]}")
+def test_grouped_tiles(case, trans):
+    sizes, N, K = case
+    gu.say("grouped tiles", case, trans)
+    R, G, offsets, rows, ar, f = grouped_case(sizes, 2, N, K, 2, 1, 4)
+    a, b, c0 = f(-(-R // 2), K), f(G, N, K) if trans else f(G, K, N), f(R, N)
+    off, rw = Buffer(offsets), Buffer(rows)
+    for alpha, beta, pad, mis in ((1.0, 1.0, 0, 0), (-1.5, 0.5, 3, 1)):
+        A, B, C = Buffer(a, K + pad, mis), Buffer(b, b.shape[2] + pad, mis, stride=b.shape[1] * (b.shape[2] + pad) + pad), Buffer(c0, N + pad, mis)
+        g.sgemm_grouped(G, R, N, K, alpha, A.ptr, A.ld, 2, B.ptr, B.ld, B.stride, trans, beta, C.ptr, C.ld, True, off.ptr, rw.ptr)
+        torch.cuda.synchronize()
+        want, size = ro.grouped(offsets, rows, N, K, alpha, a, 2, b, trans, beta, c0, True)
+        got, touched = C.read(), ~np.isnan(size)
+        assert np.array_equal(got[~touched], c0[~touched])
+        within(got[touched], want[touched], size[touched], 1e-5, "C")
+
+
 def test_grouped_without_a_product():
     """alpha 0 or K 0: C = beta C for the placed rows, A and B not read."""
     for K, alpha in ((0, 1.0), (4, 0.0)):
