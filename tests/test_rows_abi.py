@@ -264,3 +264,18 @@ def test_adapter_and_product_gradients_are_slopes():
         up[i] += h
         down[i] -= h
         assert abs((product(up) - product(down)) / (2 * h) - got[i]) < 1e-8
+
+
+def test_no_kernel_of_these_uses_scratch():
+    """Their kernels too keep their state in registers and LDS (see the library's own such test)."""
+    from fp32_gemm_03_amd import build as b
+    try:
+        res = b.kernel_resources(source=1)
+    except (RuntimeError, OSError) as e:
+        pytest.skip(f"cannot read the code object: {e}")
+    names = dict(zip(res, b.demangle(res)))
+    assert any("thin" in n for n in names.values()) and any("route" in n for n in names.values())
+    bad = {names[k]: r for k, r in res.items()
+           if r.get("private_segment_fixed_size", -1) != 0 or r.get("vgpr_spill_count", -1) != 0}
+    assert not bad, bad
+    assert all(0 <= r["group_segment_fixed_size"] <= 160 * 1024 for r in res.values())
