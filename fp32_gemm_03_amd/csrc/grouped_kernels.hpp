@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     const int li = lane & 15, lk = lane >> 4;
     const int live = p1 - p0 < ROWS ? (p1 - p0 + 15) / 16 : MB;  // 16-row blocks
     int my_row = -1;  // of C: thread m holds the tile's row m
-    if (tid < ROWS && p0 + tid < p1) my_row = (int)row_of(a, p0 + tid, a.c_scatter);
+    if (tid < ROWS && p0 + tid < p1) my_row = (int)c_row_of(a, p0 + tid);
 
     const int K = a.rank_k ? __builtin_amdgcn_readfirstlane(group_rank(a, g, a.K)) : a.K;
     const int steps = (K + 31) / 32;

@@ -928,6 +928,13 @@ __device__ __forceinline__ int64_t row_of(const GroupedArgs &a, int p, int div) 
     return div == 1 ? s : s / div;
 }
 
+// C's row of place p: none where the place's slot is asked for and is not one
+__device__ __forceinline__ int64_t c_row_of(const GroupedArgs &a, int p) {
+    if (a.a_div == 0 && a.c_scatter == 0) return p;
+    const int64_t slot = row_of(a, p, 1);
+    return slot < 0 || a.c_scatter != 0 ? slot : p;
+}
+
 __device__ __forceinline__ float group_alpha(const GroupedArgs &a, int g) {
     return a.scales != nullptr ? a.alpha * a.scales[g] : a.alpha;
 }
@@ -973,7 +980,7 @@ __global__ void __launch_bounds__(256) grouped_simple(GroupedArgs a) {
     for (int i = 0; i < 4; ++i) {
         const int p = p0 + ty + 8 * i;
         if (p >= p1 || n0 + tx >= a.N) continue;
-        const int64_t cr = row_of(a, p, a.c_scatter);
+        const int64_t cr = c_row_of(a, p);
         if (cr < 0) continue;
         float *q = a.C + cr * a.ldc + n0 + tx;
         *q = a.beta != 0.0f ? fmaf(a.beta, *q, al * acc[i]) : al * acc[i];

@@ -465,8 +465,8 @@ size_t sgemm_group_rows_workspace_size(int R, int G);
  * or ceil(R / a_div), C's are R.  Rows of C that no placed slot names are not
  * touched; beta == 0 does not read C, alpha == 0 or K == 0 read neither A nor
  * B.  offsets and rows are device arrays as sgemm_group_rows() writes them
- * (rows may be NULL when neither a_div nor c_scatter uses it; a value outside
- * [0, R) is skipped, and each slot may be there once).  Offsets outside [0, R]
+ * (rows may be NULL when neither a_div nor c_scatter uses it; else a place whose
+ * value is outside [0, R) is skipped, and each slot may be there once).  Offsets outside [0, R]
  * are taken as the nearer end.  B's groups may overlap (stride_b 0 is one B for
  * all).  Any 4-byte alignment and any leading dimensions; small ones (rows of
  * A and a group's B within 4 GiB) take the fast kernels. */

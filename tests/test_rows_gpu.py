@@ -393,6 +393,35 @@ def test_grouped_skips_values_outside_and_takes_offsets_within():
         within(got[e], a[slots].astype(np.float64).T @ y[slots], np.abs(a[slots]).T @ np.abs(y[slots]), 1e-5)
 
 
+@pytest.mark.parametrize("R", [6, 500])
+@pytest.mark.parametrize("trans", [False, True], ids=["nn", "nt"])
+@pytest.mark.parametrize("a_div,scatter", [(1, 0), (2, 0), (2, 1), (0, 1), (0, 0)])
+def test_grouped_leaves_out_a_place_without_a_slot(a_div, scatter, trans, R):
+    """Places in order whose slot is outside [0, R): C's row is left as it was, unless no slot is asked for."""
+    N, K = 40, 100
+    gu.say("grouped without a slot", a_div, scatter, trans, R)
+    r = rng_of(16, R)
+    a = r.uniform(-1, 1, (-(-R // a_div) if a_div else R, K)).astype(np.float32)
+    b = r.uniform(-1, 1, (2, N, K) if trans else (2, K, N)).astype(np.float32)
+    rows = r.permutation(R).astype(np.int32)
+    rows[[1, R // 2]] = -3, R
+    offsets = np.array([0, R // 3, R], np.int32)
+    A, B, C = Buffer(a), Buffer(b), Buffer(np.full((R, N), 3.0, np.float32))
+    off, rw = Buffer(offsets), Buffer(rows)
+    g.sgemm_grouped(2, R, N, K, 1.0, A.ptr, K, a_div, B.ptr, b.shape[2], N * K, trans, 0.5, C.ptr, N, scatter, off.ptr, rw.ptr)
+    torch.cuda.synchronize()
+    want, size = np.full((R, N), 3.0), np.full((R, N), 3.0)
+    for p in range(R):
+        if (a_div or scatter) and not 0 <= rows[p] < R:
+            continue
+        x = a[rows[p] // a_div if a_div else p].astype(np.float64)
+        e = b[0 if p < offsets[1] else 1].astype(np.float64)
+        c = rows[p] if scatter else p
+        want[c] = x @ (e.T if trans else e) + 1.5
+        size[c] = np.abs(x) @ np.abs(e.T if trans else e) + 1.5
+    within(C.read(), want, size, 1e-5, "C")
+
+
 @pytest.mark.parametrize("trans", [False, True], ids=["nn", "nt"])
 def test_grouped_rows_beyond_4_gib(trans):
     """Rows 1.5 GiB apart: offsets beyond 32 bits in A and in C, gathered and scattered."""
