@@ -360,13 +360,14 @@ int sgemm_route(int T, int E, int k, int scoring, const float *logits, int ldl, 
     NEED(2, E >= 1 && E <= SGEMM_ROUTE_MAX_EXPERTS);
     NEED(3, k >= 1 && k <= E && k <= SGEMM_ROUTE_MAX_K);
     NEED(4, scoring == SGEMM_SCORE_SOFTMAX || scoring == SGEMM_SCORE_SIGMOID);
-    NEED(5, T == 0 || logits != nullptr);
+    NEED(5, (T == 0 || logits != nullptr) && aligned4(logits));
     NEED(6, ldl >= E);
+    NEED(7, aligned4(bias));
     NEED(8, groups >= 1 && groups <= 64 && E % groups == 0);
     NEED(9, top_groups >= 1 && top_groups <= groups);
     NEED(10, group_best == 1 || group_best == 2);
-    NEED(13, T == 0 || ids != nullptr);
-    NEED(14, T == 0 || weights != nullptr);
+    NEED(13, (T == 0 || ids != nullptr) && aligned4(ids));
+    NEED(14, (T == 0 || weights != nullptr) && aligned4(weights));
     rowk::RouteArgs a;
     a.T = T;
     a.E = E;
@@ -395,11 +396,11 @@ int sgemm_route_grad(int T, int E, int k, int scoring, const float *logits, int 
     NEED(2, E >= 1 && E <= SGEMM_ROUTE_MAX_EXPERTS);
     NEED(3, k >= 1 && k <= E && k <= SGEMM_ROUTE_MAX_K);
     NEED(4, scoring == SGEMM_SCORE_SOFTMAX || scoring == SGEMM_SCORE_SIGMOID);
-    NEED(5, T == 0 || logits != nullptr);
+    NEED(5, (T == 0 || logits != nullptr) && aligned4(logits));
     NEED(6, ldl >= E);
-    NEED(9, T == 0 || ids != nullptr);
-    NEED(10, T == 0 || dweights != nullptr);
-    NEED(11, T == 0 || dlogits != nullptr);
+    NEED(9, (T == 0 || ids != nullptr) && aligned4(ids));
+    NEED(10, (T == 0 || dweights != nullptr) && aligned4(dweights));
+    NEED(11, (T == 0 || dlogits != nullptr) && aligned4(dlogits));
     NEED(12, lddl >= E);
     rowk::RouteGradArgs a;
     a.T = T;
@@ -426,9 +427,9 @@ int sgemm_group_rows(int R, int G, const int *ids, int *offsets, int *rows, void
                      size_t workspace_bytes, hipStream_t stream) {
     NEED(1, R >= 0);
     NEED(2, G >= 1 && G <= SGEMM_MAX_GROUPS);
-    NEED(3, R == 0 || ids != nullptr);
-    NEED(4, offsets != nullptr);
-    NEED(5, R == 0 || rows != nullptr);
+    NEED(3, (R == 0 || ids != nullptr) && aligned4(ids));
+    NEED(4, offsets != nullptr && aligned4(offsets));
+    NEED(5, (R == 0 || rows != nullptr) && aligned4(rows));
     if (!workspace_ok(workspace, workspace_bytes, group_bytes(R, G))) return SGEMM_ERR_WORKSPACE;
     return group(R, G, ids, offsets, rows, workspace, stream);
 }
@@ -450,8 +451,8 @@ int sgemm_grouped(int G, int R, int N, int K, float alpha, const float *A, int l
     NEED(11, stride_b >= 0);
     NEED(14, (empty || C != nullptr) && aligned4(C));
     NEED(15, ldc >= (N > 1 ? N : 1));
-    NEED(17, empty || offsets != nullptr);
-    NEED(18, empty || rows != nullptr || (a_div == 0 && c_scatter == 0));
+    NEED(17, (empty || offsets != nullptr) && aligned4(offsets));
+    NEED(18, (empty || rows != nullptr || (a_div == 0 && c_scatter == 0)) && aligned4(rows));
     GroupedArgs a = blank(G, R);
     a.N = N;
     a.K = K;
@@ -489,8 +490,8 @@ int sgemm_grouped_tn(int G, int R, int M, int N, float alpha, const float *A, in
     NEED(13, (empty || C != nullptr) && aligned4(C));
     NEED(14, ldc >= (N > 1 ? N : 1));
     NEED(15, G <= 1 || empty || stride_c >= (long long)(M - 1) * ldc + N);
-    NEED(16, !product || offsets != nullptr);
-    NEED(17, !product || rows != nullptr || (a_div == 0 && b_div == 0));
+    NEED(16, (!product || offsets != nullptr) && aligned4(offsets));
+    NEED(17, (!product || rows != nullptr || (a_div == 0 && b_div == 0)) && aligned4(rows));
     GroupedArgs a = blank(G, R);
     a.M = M;
     a.N = N;
@@ -518,6 +519,8 @@ int sgemm_combine(int T, int k, int N, int E, const int *ids, const float *weigh
     NEED(3, N >= 0);
     NEED(4, E >= 0);
     const bool empty = T == 0 || N == 0;
+    NEED(5, aligned4(ids));
+    NEED(6, aligned4(weights));
     NEED(7, (empty || Y != nullptr) && aligned4(Y));
     NEED(8, ldy >= (N > 1 ? N : 1));
     NEED(10, (empty || out != nullptr) && aligned4(out));
@@ -548,12 +551,15 @@ int sgemm_combine_grad(int T, int k, int N, int E, const int *ids, const float *
     NEED(3, N >= 0);
     NEED(4, E >= 0);
     const bool empty = T == 0 || N == 0;
+    NEED(5, aligned4(ids));
+    NEED(6, aligned4(weights));
     NEED(7, (empty || dout != nullptr) && aligned4(dout));
     NEED(8, ldd >= (N > 1 ? N : 1));
     NEED(9, (empty || dweights == nullptr || Y != nullptr) && aligned4(Y));
     NEED(10, ldy >= (N > 1 ? N : 1));
     NEED(11, aligned4(dY));
     NEED(12, lddy >= (N > 1 ? N : 1));
+    NEED(13, aligned4(dweights));
     if (T == 0 || (dweights == nullptr && (dY == nullptr || N == 0))) return SGEMM_OK;
     rowk::CombineGradArgs a;
     a.T = T;
@@ -601,7 +607,9 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
     NEED(11, ldc >= (N > 1 ? N : 1));
     NEED(12, G >= 1 && G <= SGEMM_MAX_GROUPS);
     NEED(13, rank >= 1 && rank <= SGEMM_MAX_RANK);
-    NEED(14, !product || ids != nullptr);
+    NEED(14, (!product || ids != nullptr) && aligned4(ids));
+    NEED(15, aligned4(ranks));
+    NEED(16, aligned4(scales));
     NEED(17, (!product || U != nullptr) && aligned4(U));
     NEED(18, ldu >= rank);
     NEED(19, stride_u >= 0);
@@ -684,7 +692,9 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
     NEED(10, lddc >= (N > 1 ? N : 1));
     NEED(11, G >= 1 && G <= SGEMM_MAX_GROUPS);
     NEED(12, rank >= 1 && rank <= SGEMM_MAX_RANK);
-    NEED(13, !product || ids != nullptr);
+    NEED(13, (!product || ids != nullptr) && aligned4(ids));
+    NEED(14, aligned4(ranks));
+    NEED(15, aligned4(scales));
     NEED(16, (!product || K == 0 || U != nullptr) && aligned4(U));
     NEED(17, ldu >= rank);
     NEED(18, stride_u >= 0);

@@ -402,9 +402,10 @@ int sgemm_device_fp32_peak(int device, int *compute_units, int *clock_khz, doubl
  * Return value.  0; SGEMM_ERR_WORKSPACE; SGEMM_ERR_TOO_LARGE (a grid beyond
  * one launch); a positive hipError_t; or -(100 + position) for an invalid
  * argument, numbered by its position in that call from 1 (-101 the first).
- * Checks run before any HIP call and the first bad argument wins.  Sizes of
- * zero are allowed where nothing is said: such a call launches nothing that
- * would read or write through a pointer of an empty operand. */
+ * Checks run before any HIP call and the first bad argument wins; every pointer
+ * has to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed
+ * where nothing is said: such a call launches nothing that would read or write
+ * through a pointer of an empty operand. */
 #define SGEMM_ERR_ARGUMENT (-100) /* minus the argument's position in its call */
 
 #define SGEMM_SCORE_SOFTMAX 0 /* s = exp(l) / sum exp(l) over the row */

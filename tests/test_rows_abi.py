@@ -266,6 +266,17 @@ def test_adapter_and_product_gradients_are_slopes():
         assert abs((product(up) - product(down)) / (2 * h) - got[i]) < 1e-8
 
 
+@pytest.mark.parametrize("fn,base", [
+    (g.sgemm_route, ROUTE), (g.sgemm_route_grad, GRAD), (g.sgemm_group_rows, GROUP), (g.sgemm_grouped, GROUPED),
+    (g.sgemm_grouped_tn, TN), (g.sgemm_combine, COMBINE), (g.sgemm_combine_grad, CGRAD), (g.sgemm_adapters, ADAPT),
+    (g.sgemm_adapters_grad, AGRAD)], ids=lambda x: getattr(x, "__name__", ""))
+def test_every_pointer_is_4_byte_aligned(fn, base):
+    pointers = [n for n in base if (base[n] == P or n in ("bias", "ranks", "scales")) and n != "workspace"]
+    assert len(pointers) >= 3
+    for n in pointers:
+        refuse(fn, base, {n: P + 2}, list(base).index(n) + 1)
+
+
 def test_no_kernel_of_these_uses_scratch():
     """Their kernels too keep their state in registers and LDS (see the library's own such test)."""
     from fp32_gemm_03_amd import build as b
