@@ -456,24 +456,33 @@ def variants():
 # where it serves single tokens, so the usual case (a contiguous tensor, torch's
 # current stream) takes the shortest way here: four queries per tensor, and the
 # stream's handle without a Stream object around it.
-_F32 = _I32 = None  # torch's types, once it is imported (_begin)
-_raw_stream = None
+_torch = _F32 = _I32 = _raw_stream = _get_device = None  # (_start)
+_on_gpu = False  # torch has begun to use a GPU, and so goes on
+
+
+def _start():
+    """What the calls below ask torch for, looked up once."""
+    global _F32, _I32, _raw_stream, _get_device, _torch
+    import torch
+    _I32, _F32 = torch.int32, torch.float32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
+    _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _begin(stream):
     """The current device (-1: no GPU in use) and the stream's handle."""
-    global _F32, _I32, _raw_stream
-    if _F32 is None:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _I32, _F32 = torch.int32, torch.float32
-    import torch
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    global _on_gpu
+    if not _on_gpu:
+        if _torch is None:
+            _start()
+        _on_gpu = _torch.cuda.is_initialized()
+    device = _get_device() if _on_gpu else -1
     if stream is None:
         if device >= 0 and _raw_stream is not None:
             return device, _raw_stream(device)
-        stream = torch.cuda.current_stream()
-        return torch.cuda.current_device(), stream.cuda_stream
+        stream = _torch.cuda.current_stream()
+        return _torch.cuda.current_device(), stream.cuda_stream
     if isinstance(stream, int):
         return device, stream
     if stream.device.index != device:
@@ -485,9 +494,6 @@ def _address(what, x, kind, need, device, rows_apart=False):
     """The address of a tensor of at least ``need`` elements of type ``kind``."""
     if x is None or x.__class__ is int:
         return x
-    if (getattr(x, "dtype", None) is kind and 0 <= device == x.get_device() and x.is_contiguous()
-            and x.numel() >= need):
-        return x.data_ptr()
     p = _ptr(x)
     if isinstance(x, int):
         return p
@@ -507,23 +513,35 @@ def _address(what, x, kind, need, device, rows_apart=False):
     return p
 
 
+# (each first tries what nearly every call gives: a tensor without gaps on the current device)
 def _matrix(what, x, rows, cols, ld, device, groups=1, stride=0):
     """groups matrices of rows x cols, rows ld apart and matrices stride apart."""
     need = (groups - 1) * stride + (rows - 1) * ld + cols if groups > 0 and rows > 0 and cols > 0 else 0
+    if (x.__class__ is _torch.Tensor and x.dtype is _F32 and x.get_device() == device >= 0 and x.is_contiguous()
+            and x.numel() >= need):
+        return x.data_ptr()
     return _address(what, x, _F32, need, device, True)
 
 
 def _floats(what, x, n, device):
+    if (x.__class__ is _torch.Tensor and x.dtype is _F32 and x.get_device() == device >= 0 and x.is_contiguous()
+            and x.numel() >= n):
+        return x.data_ptr()
     return _address(what, x, _F32, n, device)
 
 
 def _ints(what, x, n, device):
+    if (x.__class__ is _torch.Tensor and x.dtype is _I32 and x.get_device() == device >= 0 and x.is_contiguous()
+            and x.numel() >= n):
+        return x.data_ptr()
     return _address(what, x, _I32, n, device)
 
 
 def _space(x, nbytes, device):
     if x is None or isinstance(x, int):
         return x, int(nbytes or 0)
+    if nbytes is None and x.__class__ is _torch.Tensor and x.get_device() == device >= 0 and x.is_contiguous():
+        return x.data_ptr(), x.nbytes
     p = _ptr(x)
     if not x.is_contiguous():
         raise ValueError("workspace must be laid out without gaps")
