@@ -102,10 +102,13 @@ const Block kSquareT = THIN_NT(1, 1, 4, 1, 4);   // 16 x 16, 4 x 1
 //   Fewer than 256 tiles of 32 x 64: narrower columns, so that more CUs read B (one
 //     row, 4096 x 4096: 14.4 at 32 columns and 20.6 at 64; B as N x K, where a
 //     narrow tile's lines are still whole, 13.5 at 16 and 20.1 at 32).
+//     The same for as few columns as an adapter's rank (1 x 8192, 32 x 4096: 26
+//     against 39; N x K, 16 x 4096: 25 against 35 on 32 x 64 and 65 on 64 x 64).
 //   Many rows per group: 64 rows, read fewer times (16 x 8192, 4096 x 2048: 1024
 //     against 1100 on 32 rows; N x K 1110 against 1494), for K x N only where
 //     64 x 128 tiles fill the chip often enough (8 x 4022, 2048 x 1024, 1100 tiles:
-//     161 against 146 on 32 x 64).
+//     161 against 146 on 32 x 64), for N x K where every CU has a tile (1 x 8192,
+//     64 x 4096, 128 tiles: 66 against 47).
 //   Else 32 x 64 with four waves over K (64 x 136, 1280 x 2048: 112, 5.4 TB/s).
 const Block &choose_block(const GroupedArgs &a, bool trans_b) {
     const long long groups = a.offsets == nullptr ? 1 : a.G;
@@ -114,13 +117,13 @@ const Block &choose_block(const GroupedArgs &a, bool trans_b) {
     if (trans_b) {
         if (a.K <= 64) return kLowFlatT;
         if (squares <= 256) return kSquareT;
-        if (few) return kNarrowT;
-        return a.R > 64 * groups ? kTallT : kLowT;
+        if (few || a.N <= 16) return kNarrowT;
+        return a.R > 64 * groups && a.N > 32 && row_tiles(a, 64) * ceil_div(a.N, 64) >= 256 ? kTallT : kLowT;
     }
     if (a.K <= 64) return kLowFlat;
     if (a.N <= 16 || (squares <= 256 && a.R > 16 * groups)) return kSquare;
     if (row_tiles(a, 16) * ceil_div(a.N, 32) <= 256) return kLeast;
-    if (few) return kNarrow;
+    if (few || a.N <= 32) return kNarrow;
     return row_tiles(a, 64) * ceil_div(a.N, 128) >= 2048 && a.R > 64 * groups ? kTall : kLow;
 }
 

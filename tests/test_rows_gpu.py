@@ -327,6 +327,7 @@ TILES = [
     ([33, 0, 50], 16, 400), ([200, 17], 40, 130), ([5] * 12, 64, 300),  # 16 x 16, 16 x 32
     ([2600, 1700], 16, 70), ([1500, 900], 64, 90),  # more of them, 32 x 32
     ([90, 0, 70] * 7, 700, 66), ([20] * 40, 450, 100), ([700] * 3, 1500, 80),  # 32 x 64, 64 rows
+    ([9000, 200], 13, 70), ([8000, 500], 31, 70), ([16500, 90], 40, 70),  # many rows, few columns
 ]
 
 
