@@ -46,12 +46,12 @@ struct Tile {
     int g, p0, p1, bn;  // group, first row, the group's end, first column
 };
 
-__device__ __forceinline__ bool place_tile(const GroupedArgs &a, int bm, int bn, Tile &t) {
+__device__ __forceinline__ bool place_tile(const GroupedArgs &a, int bm, int bn, int block, Tile &t) {
     const int lane = threadIdx.x & 63;
     const int nbn = (a.N + bn - 1) / bn;
     const int groups = a.offsets != nullptr ? a.G : 1;
-    const int X = 1 << a.xcd_shift, x = (int)blockIdx.x & (X - 1);
-    int left = (int)(blockIdx.x >> a.xcd_shift);  // tiles of XCD x before this one
+    const int X = 1 << a.xcd_shift, x = block & (X - 1);
+    int left = block >> a.xcd_shift;  // tiles of XCD x before this one
     for (int base = 0; base < groups; base += 64) {
         int lo, hi;
         const int n = tiles_of(a, base + lane, bm, lo, hi);
@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 // 16 groups of 512 rows, 4096 x 2048: 1035 us, 133 TFLOP/s, matrix cores busy 92%.
 // ---------------------------------------------------------------------------
 template <int MB, int VW, int WK, int WN, int WPE, bool TRANS_B>
-__global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_eu(WPE))) thin(GroupedArgs a) {
+__device__ __forceinline__ void thin_tile(const GroupedArgs &a, int block) {
     constexpr int ROWS = 16 * MB, COLS = 16 * VW, NT = WK * WN * 64;
     __shared__ __attribute__((aligned(16))) float part[WK > 1 ? WK : 1][WK > 1 ? WN * ROWS * COLS : 1];
     __shared__ __attribute__((aligned(16))) int c_row[ROWS];
     Tile t;
-    if (!place_tile(a, ROWS, COLS * WN, t)) return;
+    if (!place_tile(a, ROWS, COLS * WN, block, t)) return;
     const int g = t.g, p0 = t.p0, p1 = t.p1;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6) / WN, wn = __builtin_amdgcn_readfirstlane(tid >> 6) % WN;
@@ -569,6 +569,28 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
             store4(q, left, out);
         }
     }
+}
+
+template <int MB, int VW, int WK, int WN, int WPE, bool TRANS_B>
+__global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_eu(WPE))) thin(GroupedArgs a) {
+    thin_tile<MB, VW, WK, WN, WPE, TRANS_B>(a, (int)blockIdx.x);
+}
+
+// A product and, in workgroups of its own ahead of it, few rows times their
+// adapters' U: neither needs the other, and together they are one launch (with
+// expand_rows behind it, one row, 4096 x 4096: 18.4 us, 21.4 one after the other;
+// 29 rows, 4095 x 2048: 22.7 against 25.2).
+struct PairArgs {
+    GroupedArgs product;
+    ShrinkArgs shrink;
+    int ahead;  // workgroups, a multiple of 8: the tiles keep their XCDs
+};
+template <int MB, int VW, int WK, int WN, int WPE>
+__global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_eu(WPE))) thin_and_shrink(PairArgs a) {
+    static_assert(WK * WN == 4, "shrink_row's workgroup");
+    const int block = (int)blockIdx.x;
+    if (block < a.ahead) shrink_row(a.shrink, block);
+    else thin_tile<MB, VW, WK, WN, WPE, false>(a.product, block - a.ahead);
 }
 
 }  // namespace rowk

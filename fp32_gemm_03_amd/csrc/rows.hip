@@ -59,6 +59,7 @@ long long row_tiles(const GroupedArgs &a, int bm) {
 }
 
 typedef void (*GroupedFn)(GroupedArgs);
+typedef void (*PairFn)(rowk::PairArgs);
 
 // The fast kernels' byte offsets are 32-bit: a gathered operand is addressed
 // from its first row, one in order from the tile's (tn: the group's) first.
@@ -71,18 +72,22 @@ bool within_reach(long long rows, int div, int ld, long long tile_rows) {
 struct Block {
     int bm, bn, threads;
     GroupedFn fn;
+    PairFn pair;  // with few rows' adapters ahead of it
 };
 #define THIN_NN(MB, VW, WK, WN, WPE) \
-    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>}
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, nullptr}
+#define THIN_FEW(MB, VW, WK, WN, WPE)                                              \
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, \
+     rowk::thin_and_shrink<MB, VW, WK, WN, WPE>}
 #define THIN_NT(MB, VW, WK, WN, WPE) \
-    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, true>}
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, true>, nullptr}
 // rows x columns of a tile; waves over K x waves over columns.  B as K x N:
 const Block kTall = THIN_NN(4, 4, 2, 2, 2);      // 64 x 128, 2 x 2
-const Block kLow = THIN_NN(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
+const Block kLow = THIN_FEW(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
 const Block kLowFlat = THIN_NN(2, 4, 1, 1, 4);   // 32 x 64, one wave
-const Block kNarrow = THIN_NN(2, 2, 4, 1, 4);    // 32 x 32, 4 x 1
-const Block kLeast = THIN_NN(1, 2, 4, 1, 4);     // 16 x 32, 4 x 1
-const Block kSquare = THIN_NN(1, 1, 4, 1, 4);    // 16 x 16, 4 x 1
+const Block kNarrow = THIN_FEW(2, 2, 4, 1, 4);    // 32 x 32, 4 x 1
+const Block kLeast = THIN_FEW(1, 2, 4, 1, 4);     // 16 x 32, 4 x 1
+const Block kSquare = THIN_FEW(1, 1, 4, 1, 4);    // 16 x 16, 4 x 1
 // and as N x K:
 const Block kTallT = THIN_NT(4, 4, 4, 1, 2);     // 64 x 64, 4 x 1
 const Block kLowT = THIN_NT(2, 4, 4, 1, 4);      // 32 x 64, 4 x 1
@@ -137,11 +142,22 @@ int xcd_shift(long long columns) {
     return columns < xcds ? 0 : shift;
 }
 
-int launch_block(const Block &b, bool dealt, GroupedArgs a, hipStream_t stream) {
+// How many workgroups, and the XCDs they are dealt to.
+long long grid_of(const Block &b, bool dealt, GroupedArgs &a) {
     a.xcd_shift = dealt ? xcd_shift(ceil_div(a.N, b.bn)) : 0;
     // every XCD's share of the tile columns, rounded up in every row of tiles
     const long long columns = ceil_div(ceil_div(a.N, b.bn), 1LL << a.xcd_shift) << a.xcd_shift;
-    return enqueue(b.fn, row_tiles(a, b.bm) * columns, b.threads, a, stream);
+    return row_tiles(a, b.bm) * columns;
+}
+
+int launch_block(const Block &b, bool dealt, GroupedArgs a, hipStream_t stream) {
+    const long long grid = grid_of(b, dealt, a);
+    return enqueue(b.fn, grid, b.threads, a, stream);
+}
+
+// 32-bit offsets reach all of both operands
+bool reachable(const GroupedArgs &a, bool trans_b) {
+    return within_reach(a.R, a.a_div, a.lda, 256) && (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
 }
 
 int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
@@ -150,10 +166,8 @@ int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     if (a.R >= 1 << 29) return SGEMM_ERR_TOO_LARGE;
     if (a.alpha == 0.0f) a.K = 0;
     if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
-    const bool reach = within_reach(a.R, a.a_div, a.lda, 256) &&
-                       (trans_b ? a.N : a.K) + 256LL <= kReach / 4 / a.ldb;
-    if (reach) return launch_block(choose_block(a, trans_b), true, a, stream);
-    const Block simple = {32, 32, 256, trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>};
+    if (reachable(a, trans_b)) return launch_block(choose_block(a, trans_b), true, a, stream);
+    const Block simple = {32, 32, 256, trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>, nullptr};
     return launch_block(simple, false, a, stream);
 }
 
@@ -244,9 +258,9 @@ bool workspace_ok(const void *p, size_t have, size_t need) {
 }
 
 // ---- adapters ----------------------------------------------------------------
-// Up to 64 rows, which a batch of sequences has, each with an adapter of its own:
-// h = A[m] U_g in pieces of K, C = alpha h V_g + beta C, both a workgroup per row
-// and piece, and C += alpha A B.  More: rows sorted by adapter, H = A U_g, the
+// Up to 64 rows, which a batch of sequences has, each with an adapter of its own: in
+// one launch alpha A B + beta C and h = A[m] U_g in pieces of K, then C += alpha s h
+// V_g, a wave per row and 256 columns.  More: rows sorted by adapter, H = A U_g, the
 // projection, and C += H V_g.  (Summing A B and H V_g over sorted rows in one
 // grouped product was slower, 4096 x 4096 x 2048 with 11 adapters 613 us against
 // 559: sgemm's blocks gain more than C's extra traffic costs.)
@@ -287,12 +301,8 @@ GroupedArgs blank(int G, int R) {
     return a;
 }
 
-// C = alpha A B + beta C: up to 512 rows on the grouped kernels, as one group (100 x
-// 4096 x 4096 36 us against sgemm_ws's 42, 300 rows 94 against 98), beyond on
-// sgemm's blocks (4096 x 4096 x 2048 473 against 482, 2000 x 2048 x 1024 66 against 68).
-int project(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta, float *C,
-            int ldc, void *workspace, size_t bytes, hipStream_t stream) {
-    if (M > 512) return sgemm_ws(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, workspace, bytes, stream);
+GroupedArgs projection(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta,
+                       float *C, int ldc) {
     GroupedArgs a = blank(1, M);
     a.N = N;
     a.K = K;
@@ -304,7 +314,16 @@ int project(int M, int N, int K, float alpha, const float *A, int lda, const flo
     a.ldb = ldb;
     a.C = C;
     a.ldc = ldc;
-    return grouped(a, false, stream);
+    return a;
+}
+
+// C = alpha A B + beta C: up to 512 rows on the grouped kernels, as one group (100 x
+// 4096 x 4096 36 us against sgemm_ws's 42, 300 rows 94 against 98), beyond on
+// sgemm's blocks (4096 x 4096 x 2048 473 against 482, 2000 x 2048 x 1024 66 against 68).
+int project(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb, float beta, float *C,
+            int ldc, void *workspace, size_t bytes, hipStream_t stream) {
+    if (M > 512) return sgemm_ws(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, workspace, bytes, stream);
+    return grouped(projection(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc), false, stream);
 }
 
 // H[m] = scales[g] A[m] U_g for the placed rows (trans_u: U_g rank x K)
@@ -626,9 +645,11 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h);
     int rc;
+    rowk::PairArgs p;
+    p.product = projection(M, N, K, alpha, A, lda, B, ldb, beta, C, ldc);
     // (a piece of U within 32-bit offsets, with the steps that overrun its end)
-    if (M <= kFewRows && ceil_div(K, shrink_parts(K)) + 8 * 256 <= kReach / 4 / ldu) {
-        rowk::ShrinkArgs h;
+    if (M <= kFewRows && ceil_div(K, shrink_parts(K)) + 8 * 256 <= kReach / 4 / ldu && reachable(p.product, false)) {
+        rowk::ShrinkArgs &h = p.shrink;
         h.M = M;
         h.K = K;
         h.G = G;
@@ -642,7 +663,10 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
         h.ids = ids;
         h.ranks = ranks;
         h.H = H;
-        rc = enqueue(rowk::shrink_rows, (long long)M * h.parts, 256, h, stream);
+        p.ahead = (int)(ceil_div(M * h.parts, 8) * 8);
+        const Block &b = K <= 64 ? kNarrow : choose_block(p.product, false);
+        const long long grid = p.ahead + grid_of(b, true, p.product);
+        rc = enqueue(b.pair, grid, b.threads, p, stream);
         if (rc != SGEMM_OK) return rc;
         rowk::ExpandArgs e;
         e.M = M;
@@ -652,7 +676,6 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
         e.parts = h.parts;
         e.chunks = (int)ceil_div(N, 256);
         e.alpha = alpha;
-        e.beta = beta;
         e.H = H;
         e.V = V;
         e.scales = scales;
@@ -662,9 +685,7 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
         e.ids = ids;
         e.ranks = ranks;
         e.C = C;
-        rc = enqueue(rowk::expand_rows, (long long)M * e.chunks, 64, e, stream);
-        if (rc != SGEMM_OK) return rc;
-        return project(M, N, K, alpha, A, lda, B, ldb, 1.0f, C, ldc, nullptr, 0, stream);
+        return enqueue(rowk::expand_rows, (long long)M * e.chunks, 64, e, stream);
     }
     rc = group(M, G, ids, offsets, rows, w + at.counts, stream);
     if (rc == SGEMM_OK)

@@ -640,10 +640,10 @@ __global__ void __launch_bounds__(64) group_few(GroupArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// A row times its own adapter's U (K x rank), for few rows: a workgroup per row
-// and piece of K, four columns per lane, the lanes of a column group taking k in
-// turn; H holds the pieces' sums, [piece][row][rank].  And back: a wave per row and
-// 256 columns adds alpha h V_g to beta C.  Memory bounds both (29 rows with an
+// A row times its own adapter's U (K x rank), for few rows: a workgroup of 256 per
+// row and piece of K, four columns per lane, the lanes of a column group taking k
+// in turn; H holds the pieces' sums, [piece][row][rank].  And back: a wave per row
+// and 256 columns adds alpha s h V_g to C.  Memory bounds both (29 rows with an
 // adapter each, rank 64: 15 MB of U in 5.1 us, 30 MB of V in 8.0, launches in it);
 // loads go through descriptors that end where the data does, because a branch
 // around each kept them from overlapping (V took 28 us).
@@ -656,9 +656,10 @@ struct ShrinkArgs {
     float *H;
 };
 
-__global__ void __launch_bounds__(256) shrink_rows(ShrinkArgs a) {
+__device__ __forceinline__ void shrink_row(const ShrinkArgs &a, int block) {
     __shared__ __attribute__((aligned(16))) float part[256 * 4];
-    const int m = blockIdx.x % a.M, piece = blockIdx.x / a.M;
+    const int m = block % a.M, piece = block / a.M;
+    if (piece >= a.parts) return;
     const int id = a.ids[m];
     if ((unsigned)id >= (unsigned)a.G) return;
     int rank = a.rank;
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(256) shrink_rows(ShrinkArgs a) {
 
 struct ExpandArgs {
     int M, N, G, rank, parts, chunks;  // chunks of 256 columns
-    float alpha, beta;
+    float alpha;
     const float *H, *V, *scales;
     int64_t ldv, stride_v, ldc;
     const int *ids, *ranks;
@@ -721,30 +722,28 @@ __global__ void __launch_bounds__(64) expand_rows(ExpandArgs a) {
     const int m = blockIdx.x / a.chunks, lane = threadIdx.x;
     const int c0 = (int)(blockIdx.x % a.chunks) * 256;  // first column
     const int id = a.ids[m];
-    int rank = 0;
-    if ((unsigned)id < (unsigned)a.G) {
-        rank = a.rank;
-        if (a.ranks != nullptr) {
-            rank = a.ranks[id];
-            rank = rank < 0 ? 0 : (rank > a.rank ? a.rank : rank);
-        }
-        const float s = a.scales != nullptr ? a.alpha * a.scales[id] : a.alpha;
-        for (int k = lane; k < (rank + DEEP - 1) / DEEP * DEEP; k += 64) {
-            float v = 0.0f;
-            if (k < rank) {
+    if ((unsigned)id >= (unsigned)a.G) return;
+    int rank = a.rank;
+    if (a.ranks != nullptr) {
+        rank = a.ranks[id];
+        rank = rank < 0 ? 0 : (rank > a.rank ? a.rank : rank);
+    }
+    if (rank == 0) return;
+    const float s = a.scales != nullptr ? a.alpha * a.scales[id] : a.alpha;
+    for (int k = lane; k < (rank + DEEP - 1) / DEEP * DEEP; k += 64) {
+        float v = 0.0f;
+        if (k < rank) {
 #pragma unroll 16
-                for (int i = 0; i < a.parts; ++i) v += a.H[((int64_t)i * a.M + m) * a.rank + k];
-            }
-            h[k] = k < rank ? s * v : 0.0f;
+            for (int i = 0; i < a.parts; ++i) v += a.H[((int64_t)i * a.M + m) * a.rank + k];
         }
+        h[k] = k < rank ? s * v : 0.0f;
     }
     __syncthreads();
     const int64_t bytes = (int64_t)(a.N - c0) * 4;
     const uint32_t off = 16u * (uint32_t)lane;
     const rsrc_t rc = whole_rsrc(a.C + (int64_t)m * a.ldc + c0, bytes);
-    const float *V = a.V + (int64_t)(rank > 0 ? id : 0) * a.stride_v + c0;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.beta != 0.0f) acc = fma4(a.beta, sgk::raw_load_v4f32(rc, off, 0, 0), acc);
+    const float *V = a.V + (int64_t)id * a.stride_v + c0;
+    f32x4 acc = sgk::raw_load_v4f32(rc, off, 0, 0);
     for (int k = 0; k < rank; k += DEEP) {  // rows past the rank read 0.0, as h does
         f32x4 v[DEEP];
 #pragma unroll
