@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(64) group_few(GroupArgs a) {
 // and 256 columns adds alpha s h V_g to C.  Memory bounds both (29 rows with an
 // adapter each, rank 64: 15 MB of U in 5.1 us, 30 MB of V in 8.0, launches in it);
 // loads go through descriptors that end where the data does, because a branch
-// around each kept them from overlapping (V took 28 us).
+// around each kept them from overlapping (V took 28 us), and V's first rows are on
+// their way while h is summed (29 rows 22.0 us in all, 22.7 with h first).
 // ---------------------------------------------------------------------------
 struct ShrinkArgs {
     int M, K, G, rank, parts;
@@ -729,28 +730,34 @@ __global__ void __launch_bounds__(64) expand_rows(ExpandArgs a) {
         rank = rank < 0 ? 0 : (rank > a.rank ? a.rank : rank);
     }
     if (rank == 0) return;
-    const float s = a.scales != nullptr ? a.alpha * a.scales[id] : a.alpha;
-    for (int k = lane; k < (rank + DEEP - 1) / DEEP * DEEP; k += 64) {
-        float v = 0.0f;
-        if (k < rank) {
-#pragma unroll 16
-            for (int i = 0; i < a.parts; ++i) v += a.H[((int64_t)i * a.M + m) * a.rank + k];
-        }
-        h[k] = k < rank ? s * v : 0.0f;
-    }
-    __syncthreads();
     const int64_t bytes = (int64_t)(a.N - c0) * 4;
     const uint32_t off = 16u * (uint32_t)lane;
     const rsrc_t rc = whole_rsrc(a.C + (int64_t)m * a.ldc + c0, bytes);
     const float *V = a.V + (int64_t)id * a.stride_v + c0;
-    f32x4 acc = sgk::raw_load_v4f32(rc, off, 0, 0);
-    for (int k = 0; k < rank; k += DEEP) {  // rows past the rank read 0.0, as h does
-        f32x4 v[DEEP];
+    f32x4 v[DEEP];
+    auto fetch = [&](int k) {  // rows past the rank read 0.0, as h does
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
             v[i] = sgk::raw_load_v4f32(whole_rsrc(V + (int64_t)(k + i) * a.ldv, k + i < rank ? bytes : 0), off, 0, 0);
+    };
+    f32x4 acc = sgk::raw_load_v4f32(rc, off, 0, 0);
+    fetch(0);  // on its way while h is summed
+    const float s = a.scales != nullptr ? a.alpha * a.scales[id] : a.alpha;
+    for (int k = lane; k < (rank + DEEP - 1) / DEEP * DEEP; k += 64) {
+        float x = 0.0f;
+        if (k < rank) {
+#pragma unroll 16
+            for (int i = 0; i < a.parts; ++i) x += a.H[((int64_t)i * a.M + m) * a.rank + k];
+        }
+        h[k] = k < rank ? s * x : 0.0f;
+    }
+    __syncthreads();
+    for (int k = 0;;) {
 #pragma unroll
         for (int i = 0; i < DEEP; ++i) acc = fma4(h[k + i], v[i], acc);
+        k += DEEP;
+        if (k >= rank) break;
+        fetch(k);
     }
     sgk::raw_store_v4f32(acc, rc, off, 0, 0);
 }
