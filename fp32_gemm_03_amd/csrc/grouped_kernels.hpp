@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 // and are summed through LDS in order, with no barrier inside the K loop; each
 // wave has a few steps in flight.
 // Measured: 64 groups of 2 or 3 rows, 1280 x 2048, N x K: 109 us, 5.2 TB/s from HBM;
-// 16 groups of 512 rows, 4096 x 2048: 1035 us, 133 TFLOP/s, matrix cores busy 92%.
+// 16 groups of 512 rows, 4096 x 2048: 1030 us, 133 TFLOP/s, matrix cores busy 92%.
 // ---------------------------------------------------------------------------
 template <int MB, int VW, int WK, int WN, int WPE, bool TRANS_B>
 __device__ __forceinline__ void thin_tile(const GroupedArgs &a, int block) {
@@ -350,11 +350,13 @@ __device__ __forceinline__ void thin_tile(const GroupedArgs &a, int block) {
         // A step is H halves of 16 k.  With 16 rows or fewer and B as N x K it is two,
         // so that what runs along K is read in whole 128-byte lines (1280 x 2048,
         // 64 groups of two rows: 113 us against 126); elsewhere one half at a time
-        // leaves more steps in the registers (16 groups of 512 rows, 4096 x 2048:
-        // 1048 us against 1121).  Lane group lk takes k H 4 lk + 4 h + e of a step.
+        // is faster (16 groups of 512 rows, 4096 x 2048: 1019 us against 1121).  Lane
+        // group lk takes k H 4 lk + 4 h + e of a step.
         constexpr int H = TRANS_B && L == 1 ? 2 : 1;
-        // steps in flight: as many as the operands' share of the registers holds
-        constexpr int SHARE = WPE >= 4 ? (H == 2 ? 80 : 64) : (H == 2 ? 120 : 96), STEP = 4 * H * (VW + L);
+        // steps in flight: what 64 registers hold (80 for two halves).  More were
+        // slower, for tall tiles too, which have the registers (8 groups of 503 rows,
+        // 2048 x 1024, N x K: 172 us with two steps, 178 with three, 189 with four).
+        constexpr int SHARE = H == 2 ? 80 : 64, STEP = 4 * H * (VW + L);
         constexpr int D = SHARE / STEP < 8 ? SHARE / STEP : 8;
         static_assert(D >= 2, "steps in flight");
         const int last = (K + 16 * H - 1) / (16 * H);
@@ -374,9 +376,10 @@ __device__ __forceinline__ void thin_tile(const GroupedArgs &a, int block) {
         // of MFMAs (with 0.7 of them per MFMA the matrix cores were busy 84% of
         // the time).  Past the wave's last step the descriptors are empty and nothing
         // is read, in a round of its own behind the loop (37 x 4 rows, 64 groups:
-        // 112 us, 115 with the last step read again); the tall tiles' loops, whose
-        // code is large, read it again (16 x 512 rows: 1080 us, 1103 with the round).
-        constexpr bool AGAIN = MB > 2;
+        // 112 us, 115 with the last step read again; 8192 rows, 2048 x 2048, N x K: 512
+        // against 538).  Only the 64 x 128 tile reads it again (16 x 512 rows, 4096 x
+        // 2048: 1034 us, 1084 with the round).
+        constexpr bool AGAIN = MB > 2 && !TRANS_B;
         auto fetch = [&](int d, int u, bool there) __attribute__((always_inline)) {
             if constexpr (AGAIN) {
                 u = u < u1 ? u : u1 - 1;
