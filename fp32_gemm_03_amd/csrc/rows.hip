@@ -407,7 +407,7 @@ int sgemm_route(int T, int E, int k, int scoring, const float *logits, int ldl, 
     a.ids = ids;
     a.weights = weights;
     const RouteKernel &r = route_kernel(E, k);
-    const bool wide = bias != nullptr || (groups > 1 && group_best == 2);
+    const bool wide = bias != nullptr || group_best == 2;  // (with one group too)
     return enqueue(wide ? r.wide : r.narrow, ceil_div(T, rowk::kRouteThreads / r.lanes), rowk::kRouteThreads, a,
                    stream);
 }
