@@ -117,8 +117,8 @@ template <class V> __device__ __forceinline__ V fma4(float s, V a, V c) {
 // group), where 32 bits would swap neighbours that differ by less than their
 // rounding: WIDE computes scores and keys in 64 bits.  Otherwise the scores
 // rise with the logits, and those are compared as they are.  The chosen
-// weights are computed in 64 bits either way (one lane per choice) and rounded
-// once.
+// weights (one lane per choice), and a softmax row's sum, are computed in 64 bits
+// either way and rounded once.
 //
 // The instructions issued bound it where there is a bias: 8191 x 256 with 8 groups
 // takes 11.4 us (8.4 MB of logits: 2), of which the 64-bit exponentials and the 8
@@ -235,13 +235,12 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
         }
     } else {
         if (!a.sigmoid && !a.renorm) {
-            float sum = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float p = exp_below(x[v], top);
-                sum += x[v] > -INFINITY ? p : 0.0f;
+                const double p = exp_below((double)x[v], (double)top);
+                total += x[v] > -INFINITY ? p : 0.0;
             }
-            total = (double)reduce<L>(sum, Add());
+            total = reduce<L>(total, Add());
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? x[v] : NONE;

@@ -50,3 +50,16 @@ def test_route_order_with_one_group(score, best):
     ids, w = call_route(x, 4, dict(sigmoid=score == "sigmoid", best=best))
     assert np.array_equal(ids, want)
     within(w, np.take_along_axis(s, want, 1), np.take_along_axis(s, want, 1), 64 * U24, "weights")
+
+
+@pytest.mark.parametrize("E", [5, 16, 64, 250, 1024])
+def test_route_softmax_weights_are_rounded_once(E):
+    """Softmax weights that are not renormalised: the row's sum is held in 64 bits too."""
+    T, k = 300, min(E, 8)
+    gu.say("route softmax weights", E)
+    x = (np.random.default_rng(E).standard_normal((T, E)) * 2).astype(np.float32)
+    for scale in (1.0, 2.5):
+        ids, w = call_route(x, k, dict(scale=scale))
+        want_ids, want = ro.route(x, k, scale=scale)
+        assert np.array_equal(ids, want_ids)
+        within(w, want, np.abs(want), ONCE, "weights")
