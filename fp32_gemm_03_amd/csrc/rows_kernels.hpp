@@ -122,7 +122,8 @@ template <class V> __device__ __forceinline__ V fma4(float s, V a, V c) {
 //
 // The instructions issued bound it where there is a bias: 8191 x 256 with 8 groups
 // takes 11.4 us (8.4 MB of logits: 2), of which the 64-bit exponentials and the 8
-// rounds are a third each.  16384 x 64 without: 4.4 us, of which 2.2 are the launch.
+// rounds are a third each.  16384 x 64, k 6, without: 4.8 us renormalised and 5.5
+// with the row's sum (5.1 in 32 bits), of which 2.2 are the launch.
 // ---------------------------------------------------------------------------
 struct RouteArgs {
     int T, E, k, sigmoid, groups, top_groups, group_best, renorm;
@@ -136,7 +137,6 @@ struct RouteArgs {
 // exp(x - m) with m the row's maximum; equal values (infinities too) give 1.
 // (No branches here or below: around each element they kept the elements' loads
 // and exponentials from overlapping.)
-__device__ __forceinline__ float exp_below(float x, float m) { return expf(x == m ? 0.0f : x - m); }
 __device__ __forceinline__ double exp_below(double x, double m) { return exp(x == m ? 0.0 : x - m); }
 
 constexpr int kRouteThreads = 256;
@@ -364,13 +364,21 @@ __global__ void __launch_bounds__(kRouteThreads) route(RouteArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The router's gradient, from the logits, the ids and the weights' gradient c:
-// with p the weights before `scale` and c scaled,
+// The router's gradient, from the logits, the ids and the weights' gradient c
+// (scaled): with p the weights before `scale`,
 //   renorm:  dl_i = p_i (c_i - sum c p) for the chosen (times 1 - s_i for the
 //            sigmoid), 0 elsewhere; the rest of the row need not be read;
 //   else softmax: dl_e = s_e (c_e - sum c s), sigmoid: dl_e = c_e s_e (1 - s_e).
-// The chosen parts are computed in 64 bits, one lane per choice, and spread
-// over the row through LDS.  16384 x 64 takes 4.4 us: the launch, 2.2, and 8.4 MB.
+// A confident router has a weight next to 1, and c_i - sum c p cancels there (to 0
+// in 32 bits from a gap of 17 between the logits).  So b, the c of the highest
+// logit (0 where that is not chosen), is taken off first: of the sum's terms
+// p_i (c_i - b) the large one is then 0 exactly, and
+//   c_e - sum c p = (c_e - b) - sum p_i (c_i - b),
+// the last sum over the chosen with renorm, else over the row, where what was not
+// chosen gives -b times the sum of the scores beside the highest.  All in 64 bits,
+// rounded once, one lane per choice, spread over the row through LDS.
+// 16384 x 64, k 6, takes 5.0 us, of which 2.2 are the launch and 1.7 the 8.4 MB (4.1
+// with the row in 32 bits); 4096 x 1024 12.5 (9.2).  Chosen alone (renorm): 3.9.
 // ---------------------------------------------------------------------------
 struct RouteGradArgs {
     int T, E, k, sigmoid, renorm;
@@ -386,7 +394,7 @@ struct RouteGradArgs {
 template <int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) route_grad(RouteGradArgs a) {
     constexpr int ROWS = kRouteThreads / L;
-    __shared__ float spread[ROWS][L * V + 1];
+    __shared__ double spread[ROWS][L * V + 1];
     const int l = threadIdx.x % L, r = threadIdx.x / L;
     const int t = (int)blockIdx.x * ROWS + r;
     const bool in = t < a.T;
@@ -394,71 +402,84 @@ __global__ void __launch_bounds__(kRouteThreads) route_grad(RouteGradArgs a) {
     const bool whole = !a.sigmoid && !a.renorm;  // every element has a gradient
 
     int id = -1;
-    float c = 0.0f;
+    double c = 0.0;
     if (in && l < a.k) {
         id = a.ids[(int64_t)t * a.k + l];
         if ((unsigned)id >= (unsigned)a.E) id = -1;
-        if (id >= 0) c = a.dweights[(int64_t)t * a.k + l] * a.scale;
+        if (id >= 0) c = (double)a.dweights[(int64_t)t * a.k + l] * (double)a.scale;
     }
     const float xi = id >= 0 ? row[id] : -INFINITY;
+    const bool has = xi > -INFINITY || xi != xi;
 
-    float x[V], top = -INFINITY, sum = 0.0f;
+    // whole: the row's exponentials, their sum `rest` where the logit is not the
+    // highest, and how many are the highest
+    double e[V], rest = 0.0, ties = 0.0;
+    float top = -INFINITY;
     if (whole) {
+        float x[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = l + L * v;
-            x[v] = in && e < a.E ? row[e] : -INFINITY;
+            x[v] = in && l + L * v < a.E ? row[l + L * v] : -INFINITY;
             top = fmaxf(top, x[v]);
         }
         top = reduce<L>(top, Max());
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x[v] = x[v] == -INFINITY ? 0.0f : exp_below(x[v], top);
-            sum += x[v];
+            e[v] = exp_below((double)x[v], (double)top);
+            e[v] = x[v] == -INFINITY ? 0.0 : e[v];
+            rest += x[v] == top ? 0.0 : e[v];
+            ties += x[v] == top && x[v] > -INFINITY ? 1.0 : 0.0;
         }
-        sum = reduce<L>(sum, Add());
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-
-    double d = 0.0;  // the chosen expert's own part
-    float q = 0.0f;  // what every element of the row subtracts
-    const bool has = xi > -INFINITY || xi != xi;
-    if (a.sigmoid) {
-        const double s = has ? 1.0 / (1.0 + exp(-(double)xi)) : 0.0;
-        const double other = 1.0 / (1.0 + exp((double)xi));  // 1 - s without cancellation
-        if (a.renorm) {
-            const double S = reduce<L>(id >= 0 ? s : 0.0, Add());
-            const double p = id >= 0 && S != 0.0 ? s / S : 0.0;
-            const double mean = reduce<L>(p * (double)c, Add());
-            d = p * ((double)c - mean) * other;
-        } else {
-            d = (double)c * s * other;
-        }
-    } else if (a.renorm) {
-        const float m = reduce<L>(xi, Max());
-        const double e = has ? exp_below((double)xi, (double)m) : 0.0;
-        const double S = reduce<L>(e, Add());
-        const double p = S != 0.0 ? e / S : 0.0;
-        d = p * ((double)c - reduce<L>(p * (double)c, Add()));
+        rest = reduce<L>(rest, Add());
+        ties = reduce<L>(ties, Add());
     } else {
-        const double s = has ? exp_below((double)xi, (double)top) * (double)inv : 0.0;
-        q = (float)reduce<L>(s * (double)c, Add());
-        d = (double)c;
+        top = reduce<L>(xi, Max());
+    }
+    const int first = reduce<L>(has && xi == top ? l : INT_MAX, Min());  // a choice of the highest logit
+    const double b = reduce<L>(l == first ? c : 0.0, Add());
+
+    double d;          // the chosen expert's gradient; whole: what its score multiplies
+    double off = 0.0;  // whole: what the other experts' scores multiply
+    if (whole) {
+        const double sum = rest + ties, inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+        const double s = has ? exp_below((double)xi, (double)top) : 0.0;
+        double q = reduce<L>(l == first ? 0.0 : s * c, Add());
+        if (first != INT_MAX) q -= b * (rest + (ties - 1.0));
+        q *= inv;
+        d = (c - b) - q;
+        off = -b - q;
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v] *= inv;
+    } else {
+        double s = 0.0, other = 1.0;
+        if (a.sigmoid) {
+            if (has) s = 1.0 / (1.0 + exp(-(double)xi));
+            other = 1.0 / (1.0 + exp((double)xi));  // 1 - s without cancellation
+        } else if (has) {
+            s = exp_below((double)xi, (double)top);
+        }
+        if (a.renorm) {
+            const double S = reduce<L>(s, Add());
+            const double p = S != 0.0 ? s / S : 0.0;
+            d = p * ((c - b) - reduce<L>(id >= 0 ? p * (c - b) : 0.0, Add())) * other;
+        } else {
+            d = c * s * other;
+        }
     }
 
 #pragma unroll
-    for (int v = 0; v < V; ++v) spread[r][l + L * v] = 0.0f;
+    for (int v = 0; v < V; ++v) spread[r][l + L * v] = off;
     __syncthreads();
-    if (id >= 0) spread[r][id] = (float)d;
+    if (id >= 0) spread[r][id] = d;
     __syncthreads();
     if (!in) return;
     float *out = a.dlogits + (int64_t)t * a.lddl;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = l + L * v;
-        if (e >= a.E) continue;
-        const float w = spread[r][e];
-        out[e] = whole ? x[v] * inv * (w - q) : w;
+        const int at = l + L * v;
+        if (at >= a.E) continue;
+        const double w = spread[r][at];
+        out[at] = (float)(whole ? e[v] * w : w);
     }
 }
 

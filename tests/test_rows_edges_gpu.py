@@ -63,3 +63,69 @@ def test_route_softmax_weights_are_rounded_once(E):
         want_ids, want = ro.route(x, k, scale=scale)
         assert np.array_equal(ids, want_ids)
         within(w, want, np.abs(want), ONCE, "weights")
+
+
+def confident_rows(E, seed):
+    """Rows whose highest logit is 0 to 60 above the next, the rest spread below it; one of two
+    equal highest logits, one with a masked half, one of -infinity."""
+    r = np.random.default_rng(seed)
+    gaps = [0.0, 0.5, 3.0, 8.0, 10.0, 14.0, 16.0, 17.0, 18.0, 20.0, 25.0, 30.0, 36.0, 40.0, 60.0]
+    x = (-np.abs(r.standard_normal((len(gaps) + 3, E))) * 2).astype(np.float32)
+    for t, gap in enumerate(gaps):
+        x[t, r.integers(E)] = gap
+    x[-3, :2] = 20.0
+    x[-2, E // 2:] = -np.inf
+    x[-2, 0] = 18.0
+    x[-1] = -np.inf
+    return x
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("E,k", [(2, 1), (9, 1), (9, 2), (64, 1), (64, 6), (200, 8), (40, 33)])
+def test_route_grad_of_confident_rows(E, k, score, renorm):
+    """dl_j = p_j sum_i p_i (c_j - c_i), over the row (c_i = 0 where not chosen) or with renorm
+    over the chosen: no term of it cancels.  64 bits are off by at most 2^-40 of the terms (sums of
+    200 terms, each with a difference that has up to 400 times their size), then one rounding."""
+    gu.say("route_grad confident", E, k, score, renorm)
+    x = confident_rows(E, E + k)
+    T = len(x)
+    r = np.random.default_rng([E, k])
+    ids, _ = ro.route(x, k, sigmoid=score == "sigmoid")
+    if E > 9:
+        ids[3, 0] = ids[8, k - 1] = -1  # the highest is not among the chosen; one choice less
+    dw = r.standard_normal((T, k)).astype(np.float32)
+    if k > 1:
+        dw[5] = dw[5, 0]  # one gradient for all: with renorm nothing is left
+    scale = np.float32(2.5)
+    out = Buffer(np.full((T, E), 7.0, np.float32))
+    X, I, D = Buffer(x), Buffer(ids.reshape(-1)), Buffer(dw.reshape(-1))
+    g.sgemm_route_grad(T, E, k, 1 if score == "sigmoid" else 0, X.ptr, X.ld, renorm, float(scale), I.ptr, D.ptr,
+                       out.ptr, out.ld)
+    torch.cuda.synchronize()
+    want, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        c, chosen = np.zeros(E), np.zeros(E, bool)
+        for i, v in zip(ids[t], dw[t]):
+            if i >= 0:
+                c[i], chosen[i] = float(v) * float(scale), True
+        row = x[t].astype(np.float64)
+        over = chosen if renorm else np.ones(E, bool)
+        over = over & (row > -np.inf)
+        if not over.any():
+            continue
+        if score == "sigmoid":
+            s, rest = 1.0 / (1.0 + np.exp(-row)), 1.0 / (1.0 + np.exp(row))
+            if not renorm:
+                want[t] = c * s * rest
+                continue
+        else:
+            s, rest = np.exp(row - row[over].max()), 1.0
+        p = np.where(over, s, 0.0)
+        p = p / p.sum()
+        terms = p[:, None] * (c[:, None] - c[None, :]) * p[None, :]
+        want[t], size[t] = terms.sum(1) * rest, np.abs(terms).sum(1) * rest
+    got = out.read().astype(np.float64)
+    assert (np.abs(got - want) <= ONCE * np.abs(want) + 2.0 ** -40 * size + 1e-37).all(), \
+        np.max(np.abs(got - want) / (ONCE * np.abs(want) + 2.0 ** -40 * size + 1e-37))
+    if score == "softmax":  # a row's gradient sums to 0, but for the roundings of its elements
+        assert (np.abs(got.sum(1)) <= ONCE * np.abs(got).sum(1) + 1e-36).all()
