@@ -122,8 +122,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lk = lane >> 4;
-    const int a_rows = a.a_div > 1 ? (a.R + a.a_div - 1) / a.a_div : a.R;
-    const int b_rows = a.b_div > 1 ? (a.R + a.b_div - 1) / a.b_div : a.R;
+    const int64_t a_rows = rows_behind(a.R, a.a_div), b_rows = rows_behind(a.R, a.b_div);
     // rows in order are taken from the group's first: their offsets stay small
     const int64_t a0 = a.a_div == 0 ? p0 : 0, b0 = a.b_div == 0 ? p0 : 0;
     const rsrc_t ra = whole_rsrc(a.A + a0 * a.lda + m0, ((a_rows - a0 - 1) * a.lda + (a.M - m0)) * 4);
@@ -320,7 +319,7 @@ __device__ __forceinline__ void thin_tile(const GroupedArgs &a, int block) {
     const int K = a.rank_k ? __builtin_amdgcn_readfirstlane(group_rank(a, g, a.K)) : a.K;
     const int steps = (K + 31) / 32;
     const int s0 = (int)((int64_t)steps * w / WK), s1 = (int)((int64_t)steps * (w + 1) / WK);
-    const int64_t a_rows = a.a_div > 1 ? (a.R + a.a_div - 1) / a.a_div : a.R;
+    const int64_t a_rows = rows_behind(a.R, a.a_div);
     const int64_t a_base = a.a_div == 0 ? p0 : 0;
     const float *a_from = a.A + a_base * a.lda;
     const int64_t a_bytes = ((a_rows - a_base - 1) * a.lda + a.K) * 4;

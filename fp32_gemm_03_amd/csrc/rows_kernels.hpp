@@ -952,6 +952,11 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs &a, int bm, int t, i
     return false;
 }
 
+// the rows of an operand that R slots reach (unsigned: R + div - 1 passes 31 bits)
+__device__ __forceinline__ int64_t rows_behind(int R, int div) {
+    return div > 1 ? ((unsigned)R + (unsigned)div - 1u) / (unsigned)div : (unsigned)R;
+}
+
 // place p's row of an operand: p itself, or rows[p] / div; -1: no such slot
 __device__ __forceinline__ int64_t row_of(const GroupedArgs &a, int p, int div) {
     if (div == 0) return p;

@@ -129,3 +129,35 @@ def test_route_grad_of_confident_rows(E, k, score, renorm):
         np.max(np.abs(got - want) / (ONCE * np.abs(want) + 2.0 ** -40 * size + 1e-37))
     if score == "softmax":  # a row's gradient sums to 0, but for the roundings of its elements
         assert (np.abs(got.sum(1)) <= ONCE * np.abs(got).sum(1) + 1e-36).all()
+
+
+# ---------------------------------------------------------------------------
+# products over groups of rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("div", [10, 2 ** 31 - 10, 2 ** 31 - 1])
+@pytest.mark.parametrize("trans", [False, True], ids=["nn", "nt"])
+def test_grouped_one_row_for_all_slots(trans, div):
+    """a_div (b_div) at and beyond R, up to the largest int: every slot takes row 0."""
+    gu.say("grouped one row", trans, div)
+    G, R, N, K = 2, 10, 40, 24
+    r = np.random.default_rng(3)
+    a, b = (r.uniform(-1, 1, s).astype(np.float32) for s in ((1, K), (G, N, K) if trans else (G, K, N)))
+    offsets, rows = np.array([0, 4, 10], np.int32), r.permutation(R).astype(np.int32)
+    A, B, C, off, rw = Buffer(a), Buffer(b), Buffer(np.full((R, N), np.nan, np.float32)), Buffer(offsets), Buffer(rows)
+    g.sgemm_grouped(G, R, N, K, 1.0, A.ptr, K, div, B.ptr, B.ld, N * K, trans, 0.0, C.ptr, N, True, off.ptr, rw.ptr)
+    torch.cuda.synchronize()
+    want, size = ro.grouped(offsets, rows, N, K, 1.0, a, div, b, trans, 0.0, np.full((R, N), np.nan), True)
+    within(C.read(), want, size, 1e-5, "C")
+    y = r.uniform(-1, 1, (R, N)).astype(np.float32)
+    Y = Buffer(y)
+    for swap in (False, True):
+        if swap:
+            D = Buffer(np.full((G, N, K), np.nan, np.float32))
+            g.sgemm_grouped_tn(G, R, N, K, 1.0, Y.ptr, N, 1, A.ptr, K, div, 0.0, D.ptr, K, N * K, off.ptr, rw.ptr)
+            want, size = ro.grouped_tn(offsets, rows, 1.0, y, 1, a, div, 0.0, np.zeros((G, N, K)))
+        else:
+            D = Buffer(np.full((G, K, N), np.nan, np.float32))
+            g.sgemm_grouped_tn(G, R, K, N, 1.0, A.ptr, K, div, Y.ptr, N, 1, 0.0, D.ptr, N, N * K, off.ptr, rw.ptr)
+            want, size = ro.grouped_tn(offsets, rows, 1.0, a, div, y, 1, 0.0, np.zeros((G, K, N)))
+        torch.cuda.synchronize()
+        within(D.read(), want, size, 1e-5, "C")
