@@ -26,6 +26,11 @@ int enqueue(void (*kernel)(A), long long grid, int threads, const A &args, hipSt
     return (int)hipGetLastError();
 }
 
+// What a kernel's loop steps through in 31 bits is at most this long: no step
+// beyond the end passes INT_MAX (it would go on from below 0).
+constexpr int kLongest = INT_MAX - 1024;
+constexpr int kMostSlots = 1 << 29;  // of sgemm_grouped, and rows of the adapters
+
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
@@ -162,8 +167,9 @@ bool reachable(const GroupedArgs &a, bool trans_b) {
 
 int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     if (a.R == 0 || a.N == 0 || a.G == 0) return SGEMM_OK;
-    // the kernels count a wave's 64 groups' tiles (16 rows at least) in 31 bits
-    if (a.R >= 1 << 29) return SGEMM_ERR_TOO_LARGE;
+    // the kernels count a wave's 64 groups' tiles (16 rows at least) in 31 bits, and
+    // step through groups and K by up to 64 beyond their end
+    if (a.R >= kMostSlots || a.G > kLongest || a.K > kLongest) return SGEMM_ERR_TOO_LARGE;
     if (a.alpha == 0.0f) a.K = 0;
     if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
     if (reachable(a, trans_b)) return launch_block(choose_block(a, trans_b), true, a, stream);
@@ -210,6 +216,7 @@ int grouped_tn(GroupedArgs a, hipStream_t stream) {
     if (a.G == 0 || a.M == 0 || a.N == 0) return SGEMM_OK;
     if (a.alpha == 0.0f) a.R = 0;  // every group's range is then empty
     if (a.R == 0 && a.beta == 1.0f) return SGEMM_OK;
+    if (a.R > kLongest) return SGEMM_ERR_TOO_LARGE;  // the slots are stepped through likewise
     const bool reach = within_reach(a.R, a.a_div, a.lda, a.R) && within_reach(a.R, a.b_div, a.ldb, a.R);
     const BlockTN simple = {32, 32, 256, rowk::grouped_tn_simple};
     const BlockTN &b = reach ? choose_tn(a) : simple;
@@ -583,6 +590,7 @@ int sgemm_combine_grad(int T, int k, int N, int E, const int *ids, const float *
     NEED(12, lddy >= (N > 1 ? N : 1));
     NEED(13, aligned4(dweights));
     if (T == 0 || (dweights == nullptr && (dY == nullptr || N == 0))) return SGEMM_OK;
+    if (N > kLongest) return SGEMM_ERR_TOO_LARGE;
     rowk::CombineGradArgs a;
     a.T = T;
     a.k = k;
@@ -641,6 +649,7 @@ int sgemm_adapters(int M, int N, int K, float alpha, const float *A, int lda, co
     const AdapterSpace at(M, N, K, G, rank, false);
     if (!workspace_ok(workspace, workspace_bytes, at.end)) return SGEMM_ERR_WORKSPACE;
     if (!product) return sgemm(M, N, K, 0.0f, A, lda, B, ldb, beta, C, ldc, stream);
+    if (M >= kMostSlots || K > kLongest) return SGEMM_ERR_TOO_LARGE;  // before anything is written
     char *w = static_cast<char *>(workspace);
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h);
@@ -736,6 +745,7 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
     const AdapterSpace at(M, N, K, G, rank, true);
     if (!workspace_ok(workspace, workspace_bytes, sgemm_adapters_grad_workspace_size(M, N, K, G, rank)))
         return SGEMM_ERR_WORKSPACE;
+    if (product && (M >= kMostSlots || N > kLongest || K > kLongest)) return SGEMM_ERR_TOO_LARGE;
     char *w = static_cast<char *>(workspace);
     int *offsets = reinterpret_cast<int *>(w + at.offsets), *rows = reinterpret_cast<int *>(w + at.rows);
     float *H = reinterpret_cast<float *>(w + at.h), *dH = reinterpret_cast<float *>(w + at.dh);

@@ -400,8 +400,11 @@ int sgemm_device_fp32_peak(int device, int *compute_units, int *clock_khz, doubl
  * pair, number t * k + j.
  *
  * Return value.  0; SGEMM_ERR_WORKSPACE; SGEMM_ERR_TOO_LARGE (a grid beyond
- * one launch); a positive hipError_t; or -(100 + position) for an invalid
- * argument, numbered by its position in that call from 1 (-101 the first).
+ * one launch; R of sgemm_grouped or M of the adapters 2^29 or more; G or K of
+ * sgemm_grouped, R of sgemm_grouped_tn, N of sgemm_combine_grad, K of the
+ * adapters or N of their gradient within 1024 of 2^31); a positive hipError_t;
+ * or -(100 + position) for an invalid argument, numbered by its position in
+ * that call from 1 (-101 the first).
  * Checks run before any HIP call and the first bad argument wins; every pointer
  * has to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed
  * where nothing is said: such a call launches nothing that would read or write

@@ -1,0 +1,31 @@
+"""Corners of the calls around products whose B is picked row by row that show without a GPU:
+sizes that are refused before any HIP call, and calls from several threads."""
+import pytest
+
+import fp32_gemm_03_amd as g
+from tests.test_rows_abi import ADAPT, AGRAD, CGRAD, GROUPED, TN
+
+INT_MAX = 2 ** 31 - 1
+TOO_LARGE = -22
+
+
+@pytest.mark.parametrize("fn,base,sizes", [
+    (g.sgemm_grouped, GROUPED, dict(G=INT_MAX)), (g.sgemm_grouped, GROUPED, dict(G=INT_MAX - 63)),
+    (g.sgemm_grouped, GROUPED, dict(K=INT_MAX, lda=INT_MAX)), (g.sgemm_grouped, GROUPED, dict(R=2 ** 29)),
+    (g.sgemm_grouped, GROUPED, dict(K=INT_MAX - 31, lda=INT_MAX, ldb=INT_MAX, trans_b=1)),
+    (g.sgemm_grouped_tn, TN, dict(R=INT_MAX)), (g.sgemm_grouped_tn, TN, dict(R=INT_MAX - 31, a_div=0, b_div=0)),
+    (g.sgemm_grouped_tn, TN, dict(R=INT_MAX - 15, a_div=1 << 20, b_div=1 << 20)),
+    (g.sgemm_combine_grad, CGRAD, dict(N=INT_MAX, ldd=INT_MAX, ldy=INT_MAX, lddy=INT_MAX)),
+    (g.sgemm_combine_grad, CGRAD, dict(N=INT_MAX - 1023, ldd=INT_MAX, ldy=INT_MAX, lddy=INT_MAX)),
+    (g.sgemm_adapters, ADAPT, dict(M=2 ** 29, workspace_bytes=1 << 50)),
+    (g.sgemm_adapters, ADAPT, dict(K=INT_MAX, lda=INT_MAX, workspace_bytes=1 << 50)),
+    (g.sgemm_adapters_grad, AGRAD, dict(M=2 ** 29, workspace_bytes=1 << 50)),
+    (g.sgemm_adapters_grad, AGRAD, dict(K=INT_MAX, lda=INT_MAX, ldda=INT_MAX, stride_du=1 << 40, workspace_bytes=1 << 50)),
+    (g.sgemm_adapters_grad, AGRAD, dict(N=INT_MAX, ldb=INT_MAX, lddc=INT_MAX, ldv=INT_MAX, lddv=INT_MAX,
+                                        stride_dv=1 << 40, workspace_bytes=1 << 50)),
+], ids=lambda v: getattr(v, "__name__", None) or (",".join(v) if len(v) < 9 else "_"))
+def test_sizes_next_to_2_31_are_refused(fn, base, sizes):
+    """A kernel's loop that steps past INT_MAX would not end: such a size is turned away."""
+    assert fn(*{**base, **sizes}.values(), stream=0, check=False) == TOO_LARGE
+    with pytest.raises(g.SgemmError):
+        fn(*{**base, **sizes}.values(), stream=0)
