@@ -466,8 +466,8 @@ def _start():
     import torch
     _I32, _F32 = torch.int32, torch.float32
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _torch = torch
     _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _torch = torch  # last: another thread that finds it finds all of them
 
 
 def _begin(stream):

@@ -29,3 +29,46 @@ def test_sizes_next_to_2_31_are_refused(fn, base, sizes):
     assert fn(*{**base, **sizes}.values(), stream=0, check=False) == TOO_LARGE
     with pytest.raises(g.SgemmError):
         fn(*{**base, **sizes}.values(), stream=0)
+
+
+def test_first_calls_of_two_threads(monkeypatch):
+    """A call that begins while another thread's first one is looking up what it asks torch for
+    looks it up itself: it does not run with half of it."""
+    import threading
+
+    import torch
+    seen, errors = [], []
+
+    def other():
+        try:
+            seen.append(g._begin(7))
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    real = torch._C
+
+    class Slow:
+        """torch, where each of the first look-ups lets another thread's call through."""
+
+        def __init__(self):
+            self.asked = set()
+
+        def __getattr__(self, name):
+            if name.startswith("_cuda") and name not in self.asked:
+                self.asked.add(name)
+                t = threading.Thread(target=other)
+                t.start()
+                t.join(60)
+            return getattr(real, name)
+
+    device = torch.cuda.current_device if torch.cuda.is_available() else lambda: 0
+    slow = Slow()
+    monkeypatch.setattr(torch, "_C", slow)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(real, "_cuda_getDevice", device, raising=False)
+    for name in ("_torch", "_F32", "_I32", "_raw_stream", "_get_device"):
+        monkeypatch.setattr(g, name, None)
+    monkeypatch.setattr(g, "_on_gpu", False)
+    mine = g._begin(7)
+    monkeypatch.undo()
+    assert not errors and len(seen) == len(slow.asked) >= 2 and set(seen) == {mine}
