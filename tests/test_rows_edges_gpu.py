@@ -11,7 +11,7 @@ import torch
 import fp32_gemm_03_amd as g
 from tests import gpu_util as gu
 from tests import rows_oracle as ro
-from tests.test_rows_gpu import U24, Buffer, call_route, within
+from tests.test_rows_gpu import U24, Buffer, call_route, router_logits, within
 
 pytestmark = pytest.mark.gpu
 ONCE = 1.01 * U24  # one rounding
@@ -129,6 +129,56 @@ def test_route_grad_of_confident_rows(E, k, score, renorm):
         np.max(np.abs(got - want) / (ONCE * np.abs(want) + 2.0 ** -40 * size + 1e-37))
     if score == "softmax":  # a row's gradient sums to 0, but for the roundings of its elements
         assert (np.abs(got.sum(1)) <= ONCE * np.abs(got).sum(1) + 1e-36).all()
+
+
+# groups of more than four experts per lane of a row, on 16 lanes and on 64
+LONG_GROUPS = [
+    (9, 256, 8, dict(groups=2)), (9, 130, 5, dict(groups=2, best=2, bias=True)), (8, 255, 8, dict(groups=3, top_groups=2, best=2)),
+    (9, 200, 6, dict(groups=2, bias=True, sigmoid=True, renorm=True)), (7, 1024, 8, dict(groups=2, best=2, bias=True)),
+    (9, 520, 20, dict(groups=2)), (8, 1023, 64, dict(groups=3, top_groups=2, best=2, sigmoid=True)),
+    (9, 600, 9, dict(groups=2, top_groups=2, bias=True)),
+]
+
+
+@pytest.mark.parametrize("case", LONG_GROUPS, ids=lambda c: f"{c[1]}in{c[3]['groups']}k{c[2]}")
+@pytest.mark.parametrize("special", [False, True])
+def test_route_long_groups(case, special):
+    T, E, k, o = case
+    gu.say("route long groups", case, special)
+    x = router_logits(T, E, 20 + k, special)
+    o = dict(o)
+    bias = (np.random.default_rng(E).standard_normal(E) * 0.2).astype(np.float32) if o.pop("bias", False) else None
+    ids, w = call_route(x, k, o, ldl=E + 1, bias_values=bias)
+    want_ids, want = ro.route(x, k, bias=bias, **o)
+    assert np.array_equal(ids, want_ids)
+    within(w, want, np.abs(np.nan_to_num(want)), 2 * U24, "weights")
+
+
+# ---------------------------------------------------------------------------
+# slots sorted by group
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("R,G", [((1 << 20) + 4097, 16), ((1 << 20) + 1, 1500), ((1 << 21) + 12345, 256), (3 << 20, 5)])
+def test_group_rows_of_several_turns(R, G):
+    """So many slots that a workgroup takes several runs of 4096 one after the other."""
+    gu.say("group_rows several turns", R, G)
+    r = np.random.default_rng([R, G])
+    ids = (r.integers(0, G, R) * r.random(R) ** 2).astype(np.int32)  # low ones often
+    ids[r.random(R) < 0.05] = -1
+    ids[9000:30000] = G - 1
+    I, off = Buffer(ids), Buffer(np.full(G + 1, -9, np.int32))
+    rows = Buffer(np.full(R, -9, np.int32))
+    need = g.sgemm_group_rows_workspace_size(R, G)
+    ws = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    placed = np.nonzero(ids >= 0)[0]
+    want = placed[np.argsort(ids[placed], kind="stable")]
+    begins = np.concatenate([[0], np.cumsum(np.bincount(ids[placed], minlength=G))])
+    for _ in range(2):
+        g.sgemm_group_rows(R, G, I.ptr, off.ptr, rows.ptr, ws, need)
+        torch.cuda.synchronize()
+        assert np.array_equal(off.read(), begins)
+        got = rows.read()
+        assert np.array_equal(got[:len(want)], want) and (got[len(want):] == -9).all()
+    assert (ws[need:] == 0xAB).all()
 
 
 # ---------------------------------------------------------------------------
