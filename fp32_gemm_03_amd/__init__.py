@@ -538,6 +538,8 @@ def _ints(what, x, n, device):
 
 
 def _space(x, nbytes, device):
+    if nbytes is not None and nbytes < 0:
+        raise ValueError(f"workspace_bytes is {nbytes}")
     if x is None or isinstance(x, int):
         return x, int(nbytes or 0)
     if nbytes is None and x.__class__ is _torch.Tensor and x.get_device() == device >= 0 and x.is_contiguous():

@@ -72,3 +72,31 @@ def test_first_calls_of_two_threads(monkeypatch):
     mine = g._begin(7)
     monkeypatch.undo()
     assert not errors and len(seen) == len(slow.asked) >= 2 and set(seen) == {mine}
+
+
+@pytest.mark.parametrize("workspace", ["address", "tensor", "none"])
+def test_a_negative_workspace_size_is_refused(monkeypatch, workspace):
+    """In C it would be the largest size there is."""
+    class Space:  # as much of a GPU tensor as the binding looks at
+        is_cuda, device, nbytes = True, "cuda:0", 512
+
+        def data_ptr(self):
+            return 0x10000
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return -1  # the current device, where none is in use
+
+        def numel(self):
+            return 512
+
+        def element_size(self):
+            return 1
+    x = {"address": 0x10000, "tensor": Space(), "none": None}[workspace]
+    with pytest.raises(ValueError):
+        g._space(x, -1, -1)
+    with pytest.raises(ValueError):
+        g.sgemm_group_rows(100000, 8, 0x10000, 0x10000, 0x10000, x, -256, stream=0)
+    assert g._space(x, 256, -1) == (None if x is None else 0x10000, 256)
