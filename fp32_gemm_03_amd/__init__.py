@@ -590,8 +590,15 @@ def sgemm_group_rows(R, G, ids, offsets, rows, workspace=None, workspace_bytes=N
         "sgemm_group_rows", check)
 
 
+def _int(what, v):
+    """An integer that no size check sees, and that ctypes would cut to its low 32 bits."""
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{what} is {v}, beyond 32 bits")
+    return v
+
+
 def _rows(R, div):
-    return -(-R // div) if div > 1 else R
+    return -(-R // div) if _int("the slots' division", div) > 1 else R
 
 
 def sgemm_grouped(G, R, N, K, alpha, A, lda, a_div, B, ldb, stride_b, trans_b, beta, C, ldc, c_scatter, offsets,
@@ -620,7 +627,7 @@ def sgemm_combine(T, k, N, E, ids, weights, Y, ldy, beta, out, ldo, stream=None,
     """``out[t]`` = the weighted sum of token t's k rows of ``Y``, plus ``beta * out[t]``."""
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_combine(
-        T, k, N, E, _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
+        T, k, N, _int("E", E), _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
         _matrix("Y", Y, T * k, N, ldy, d), ldy, beta, _matrix("out", out, T, N, ldo, d), ldo, s),
         "sgemm_combine", check)
 
@@ -629,7 +636,7 @@ def sgemm_combine_grad(T, k, N, E, ids, weights, dout, ldd, Y, ldy, dY, lddy, dw
     """``dY`` (T * k x N) and ``dweights`` (T x k) from ``dout``; either may be None."""
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_combine_grad(
-        T, k, N, E, _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
+        T, k, N, _int("E", E), _ints("ids", ids, T * k, d), _floats("weights", weights, T * k, d),
         _matrix("dout", dout, T, N, ldd, d), ldd, _matrix("Y", Y, T * k, N, ldy, d), ldy,
         _matrix("dY", dY, T * k, N, lddy, d), lddy, _floats("dweights", dweights, T * k, d), s),
         "sgemm_combine_grad", check)

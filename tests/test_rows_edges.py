@@ -3,7 +3,7 @@ sizes that are refused before any HIP call, and calls from several threads."""
 import pytest
 
 import fp32_gemm_03_amd as g
-from tests.test_rows_abi import ADAPT, AGRAD, CGRAD, GROUPED, TN
+from tests.test_rows_abi import ADAPT, AGRAD, CGRAD, COMBINE, GROUPED, TN
 
 INT_MAX = 2 ** 31 - 1
 TOO_LARGE = -22
@@ -100,3 +100,15 @@ def test_a_negative_workspace_size_is_refused(monkeypatch, workspace):
     with pytest.raises(ValueError):
         g.sgemm_group_rows(100000, 8, 0x10000, 0x10000, 0x10000, x, -256, stream=0)
     assert g._space(x, 256, -1) == (None if x is None else 0x10000, 256)
+
+
+@pytest.mark.parametrize("fn,base,name", [
+    (g.sgemm_grouped, GROUPED, "a_div"), (g.sgemm_grouped_tn, TN, "a_div"), (g.sgemm_grouped_tn, TN, "b_div"),
+    (g.sgemm_combine, COMBINE, "E"), (g.sgemm_combine_grad, CGRAD, "E")],
+    ids=lambda v: getattr(v, "__name__", None) or (v if isinstance(v, str) else "_"))
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 32, -2 ** 31 - 1])
+def test_integers_beyond_32_bits_are_refused(fn, base, name, value):
+    """Their low 32 bits would be another division of the slots (2^32: none, so that rows of A beyond
+    the one asked for are read), or another number of experts."""
+    with pytest.raises(ValueError):
+        fn(*{**base, name: value}.values(), stream=0, check=False)
