@@ -271,6 +271,16 @@ bool workspace_ok(const void *p, size_t have, size_t need) {
 // projection, and C += H V_g.  (Summing A B and H V_g over sorted rows in one
 // grouped product was slower, 4096 x 4096 x 2048 with 11 adapters 613 us against
 // 559: sgemm's blocks gain more than C's extra traffic costs.)
+//   Measured on both (us, few rows against sorted; K x N):
+//     4096 x 4096, rank 16: 1 row 17.6 / 30.9, 29 of as many adapters 22.3 / 39.2,
+//       64 of one 32.5 / 51.9, of four 43.9 / 50.9, of 64 55.6 / 52.8;
+//     the same, rank 64: 64 rows of one 40.2 / 58.7, of 16 63.3 / 55.0; rank 256: 1 row
+//       33.0 / 34.4, 64 rows of one 58.4 / 79.1, of four 86.0 / 63.8;
+//     1024 x 2048, rank 16: 64 rows of any 12.6 / 25; rank 256: 1 row 30.0 / 17.5, 64 of
+//       one 35.5 / 33.8.
+//   So rows that share an adapter read it from the L2s at little cost; the few-row form
+//   loses at rank 256 (a small shared product, or rows of several adapters), and at 64
+//   rows of many adapters by up to 8% (rank 16) or 15% (rank 64).
 constexpr int kFewRows = 64;
 
 // Pieces of K that the few rows' h are summed in: a workgroup's loads of 128 k's

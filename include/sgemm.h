@@ -384,8 +384,8 @@ int sgemm_device_fp32_peak(int device, int *compute_units, int *clock_khz, doubl
 /* ==== products whose B is picked row by row ==================================
  * A layer of experts, or a projection with low-rank adapters, is a product
  * whose rows do not share one B.  The calls below are its parts, all FP32
- * like sgemm() (operands, products and sums; the router's scores in 64 bits
- * where their order is decided by sums of them), all asynchronous on `stream`,
+ * like sgemm() (operands, products and sums; the router's scores, weights and
+ * gradient are computed in 64 bits and rounded once), all asynchronous on `stream`,
  * with caller-owned device pointers, no allocation and results that are the
  * same run to run.  A layer of experts is
  *
@@ -426,7 +426,9 @@ int sgemm_device_fp32_peak(int device, int *compute_units, int *clock_khz, doubl
  * top_groups runs worth most are chosen from.  The k highest keys are taken in
  * falling order, ties (of runs too) to the lowest index.  weights[t * k + j] is
  * the chosen score, divided by the sum of the token's k when renorm != 0 (0
- * when that sum is 0), times `scale`.
+ * when that sum is 0), times `scale`.  A softmax that is renormalised is the
+ * softmax over the chosen logits: scores too small for 64 bits beside the row's
+ * highest keep their ratio, and a +infinity not chosen has no part in them.
  *   Without a bias and with group_best 1 the order is that of the logits
  * themselves, else keys are computed and compared in 64 bits.
  *   A logit of -infinity masks its expert and a NaN logit or key is never
@@ -446,7 +448,9 @@ int sgemm_route(int T, int E, int k, int scoring, const float *logits, int ldl, 
  * d_j <- (d_j - sum_i d_i s_i / S) / S over the chosen, S their sum of scores
  * (d = 0 when S is 0); then softmax: dl_e = s_e (d_e - sum_i d_i s_i), sigmoid:
  * dl_e = d_e s_e (1 - s_e), d_e = 0 for experts not chosen.  The choice itself
- * and the bias have no gradient.  The ids of a row are distinct. */
+ * and the bias have no gradient.  The ids of a row are distinct.  A NaN logit
+ * makes the gradients NaN that it enters: its row's (softmax, not renormalised),
+ * the chosen ones' (renorm, when it is one of them), its own (sigmoid). */
 int sgemm_route_grad(int T, int E, int k, int scoring, const float *logits, int ldl, int renorm, float scale,
                      const int *ids, const float *dweights, float *dlogits, int lddl, hipStream_t stream);
 
@@ -482,8 +486,8 @@ int sgemm_grouped(int G, int R, int N, int K, float alpha, const float *A, int l
  *   C_g = alpha * sum_p A[a]^T B[b] + beta * C_g,  offsets[g] <= p < offsets[g + 1],
  * C_g (M x N) at C + g * stride_c with leading dimension ldc; A's rows hold M
  * columns and B's N; a and b are p (div 0) or rows[p] / div as above.  Every
- * C_g is written: an empty group's becomes beta * C_g.  The C_g must not
- * overlap. */
+ * C_g is written: an empty group's becomes beta * C_g.  The C_g lie one after
+ * the other: with more than one, stride_c >= (M - 1) * ldc + N. */
 int sgemm_grouped_tn(int G, int R, int M, int N, float alpha, const float *A, int lda, int a_div, const float *B,
                      int ldb, int b_div, float beta, float *C, int ldc, long long stride_c, const int *offsets,
                      const int *rows, hipStream_t stream);
@@ -525,8 +529,9 @@ size_t sgemm_adapters_workspace_size(int M, int N, int K, int G, int rank);
  *   dV_g  = alpha * scales[g] * sum_m (A[m] U_g)^T dC[m] + beta * dV_g
  * over the rows m of group g.  dA (M x K) is written; dU_g (K x rank) and dV_g
  * (rank x N) are written whole for every g, with no contribution beyond
- * ranks[g] and for adapters no row uses.  dA, or dU and dV together, may be
- * NULL (not wanted).  Workspace as above, at least
+ * ranks[g] and for adapters no row uses; with more than one, stride_du >=
+ * (K - 1) * lddu + rank and stride_dv >= (rank - 1) * lddv + N.  dA, or dU and
+ * dV together, may be NULL (not wanted).  Workspace as above, at least
  * sgemm_adapters_grad_workspace_size() bytes, which are at least
  * sgemm_adapters_workspace_size()'s: a training step needs one of them. */
 int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,
