@@ -1,5 +1,6 @@
-"""MI355X (gfx950) FP32 SGEMM: C = alpha*A*B + beta*C on row-major matrices, and
-products whose B is picked row by row (experts, low-rank adapters).
+"""MI355X (gfx950) FP32 SGEMM: C = alpha*A*B + beta*C on row-major matrices,
+products whose B is picked row by row (experts, low-rank adapters), and the parts of a
+gated feed-forward block (norm, gated projections, 8-bit rows and their product).
 
 A thin Python binding of the C ABI in ``include/sgemm.h``: every function has
 the name and argument order of its C counterpart and only marshals arguments.
@@ -38,6 +39,9 @@ __all__ = [
     "sgemm_group_rows_workspace_size", "sgemm_grouped", "sgemm_grouped_tn", "sgemm_combine",
     "sgemm_combine_grad", "sgemm_adapters", "sgemm_adapters_workspace_size", "sgemm_adapters_grad",
     "sgemm_adapters_grad_workspace_size",
+    "SGEMM_ACT_SILU", "SGEMM_ACT_GELU", "SGEMM_ACT_GELU_TANH", "SGEMM_I8_MAX_K", "sgemm_norm", "sgemm_norm_grad",
+    "sgemm_norm_grad_workspace_size", "sgemm_quantize", "sgemm_i8", "sgemm_gated", "sgemm_gated_grad",
+    "sgemm_gated_grad_workspace_size",
 ]
 
 SGEMM_PATH_AUTO = 0
@@ -46,6 +50,11 @@ SGEMM_PATH_MFMA = 2
 
 SGEMM_SCORE_SOFTMAX = 0
 SGEMM_SCORE_SIGMOID = 1
+
+SGEMM_ACT_SILU = 0
+SGEMM_ACT_GELU = 1
+SGEMM_ACT_GELU_TANH = 2
+SGEMM_I8_MAX_K = 131071
 
 SGEMM_ACCESS_AUTO = 0
 SGEMM_ACCESS_BUFFER_128 = 1
@@ -163,11 +172,19 @@ def load_library():
                                sz, vp],
             "sgemm_adapters_grad": [i, i, i, f, vp, i, vp, i, vp, i, i, i, vp, vp, vp, vp, i, ll, vp, i, ll, f,
                                     vp, i, vp, i, ll, vp, i, ll, vp, sz, vp],
+            "sgemm_norm": [i, i, vp, i, vp, i, vp, f, vp, i, vp, i, vp, i, vp, vp],
+            "sgemm_norm_grad": [i, i, vp, i, vp, f, vp, i, vp, i, vp, i, f, vp, vp, sz, vp],
+            "sgemm_quantize": [i, i, vp, i, i, vp, i, vp, i, vp, vp],
+            "sgemm_i8": [i, i, i, f, vp, i, vp, vp, i, vp, f, vp, i, vp],
+            "sgemm_gated": [i, i, i, i, vp, i, vp, i, vp, i, vp, i, vp, i, vp, i, vp],
+            "sgemm_gated_grad": [i, i, i, i, vp, i, vp, i, vp, i, vp, i, vp, i, vp, i, vp, i, f, vp, i, vp, i, vp, sz,
+                                 vp],
         }.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = i
         for name, n in (("sgemm_group_rows_workspace_size", 2), ("sgemm_adapters_workspace_size", 5),
-                        ("sgemm_adapters_grad_workspace_size", 5)):
+                        ("sgemm_adapters_grad_workspace_size", 5), ("sgemm_norm_grad_workspace_size", 2),
+                        ("sgemm_gated_grad_workspace_size", 3)):
             getattr(lib, name).argtypes = [i] * n
             getattr(lib, name).restype = sz
         _lib = lib
@@ -456,15 +473,15 @@ def variants():
 # where it serves single tokens, so the usual case (a contiguous tensor, torch's
 # current stream) takes the shortest way here: four queries per tensor, and the
 # stream's handle without a Stream object around it.
-_torch = _F32 = _I32 = _raw_stream = _get_device = None  # (_start)
+_torch = _F32 = _I32 = _I8 = _raw_stream = _get_device = None  # (_start)
 _on_gpu = False  # torch has begun to use a GPU, and so goes on
 
 
 def _start():
     """What the calls below ask torch for, looked up once."""
-    global _F32, _I32, _raw_stream, _get_device, _torch
+    global _F32, _I32, _I8, _raw_stream, _get_device, _torch
     import torch
-    _I32, _F32 = torch.int32, torch.float32
+    _I32, _F32, _I8 = torch.int32, torch.float32, torch.int8
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch  # last: another thread that finds it finds all of them
@@ -676,3 +693,97 @@ def sgemm_adapters_grad(M, N, K, alpha, A, lda, B, ldb, dC, lddc, G, rank, ids, 
         _matrix("dA", dA, M, K, ldda, d), ldda, _matrix("dU", dU, K, rank, lddu, d, G, stride_du), lddu, stride_du,
         _matrix("dV", dV, rank, N, lddv, d, G, stride_dv), lddv, stride_dv, ws, nbytes, s),
         "sgemm_adapters_grad", check)
+
+
+# ---- a gated feed-forward block ---------------------------------------------
+# The same checks; 8-bit rows are int8 tensors.
+def _matrix8(what, x, rows, cols, ld, device):
+    need = (rows - 1) * ld + cols if rows > 0 and cols > 0 else 0
+    if (x.__class__ is _torch.Tensor and x.dtype is _I8 and x.get_device() == device >= 0 and x.is_contiguous()
+            and x.numel() >= need):
+        return x.data_ptr()
+    return _address(what, x, _I8, need, device, True)
+
+
+def _sizes(*values):
+    """Integers that ctypes would cut to their low 32 bits are refused."""
+    if max(values) > 0x7fffffff or min(values) < -0x80000000:
+        raise ValueError(f"a size, leading dimension or choice among {values} is beyond 32 bits")
+
+
+def sgemm_norm(T, N, x, ldx, residual, ldr, weight, eps, sum, lds, y, ldy, q, ldq, scales, stream=None, check=True):
+    """``sum`` = ``x`` + ``residual``; ``y`` = its root-mean-square norm times ``weight``; ``q`` (int8)
+    and ``scales`` = y in 8 bits.  residual, weight, sum, y and q (with scales) may be None."""
+    _sizes(T, N, ldx, ldr, lds, ldy, ldq)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_norm(
+        T, N, _matrix("x", x, T, N, ldx, d), ldx, _matrix("residual", residual, T, N, ldr, d), ldr,
+        _floats("weight", weight, N, d), eps, _matrix("sum", sum, T, N, lds, d), lds,
+        _matrix("y", y, T, N, ldy, d), ldy, _matrix8("q", q, T, N, ldq, d), ldq, _floats("scales", scales, T, d), s),
+        "sgemm_norm", check)
+
+
+def sgemm_norm_grad_workspace_size(T, N) -> int:
+    return int(load_library().sgemm_norm_grad_workspace_size(int(T), int(N)))
+
+
+def sgemm_norm_grad(T, N, h, ldh, weight, eps, dy, lddy, dsum, ldds, dh, lddh, beta, dweight, workspace=None,
+                    workspace_bytes=None, stream=None, check=True):
+    """``dh`` (of x and of residual) and ``dweight`` from ``dy`` and ``dsum``; either may be None."""
+    _sizes(T, N, ldh, lddy, ldds, lddh)
+    d, s = _begin(stream)
+    ws, nbytes = _space(workspace, workspace_bytes, d)
+    return _ret((_lib or load_library()).sgemm_norm_grad(
+        T, N, _matrix("h", h, T, N, ldh, d), ldh, _floats("weight", weight, N, d), eps,
+        _matrix("dy", dy, T, N, lddy, d), lddy, _matrix("dsum", dsum, T, N, ldds, d), ldds,
+        _matrix("dh", dh, T, N, lddh, d), lddh, beta, _floats("dweight", dweight, N, d), ws, nbytes, s),
+        "sgemm_norm_grad", check)
+
+
+def sgemm_quantize(T, N, x, ldx, activation, gate, ldg, q, ldq, scales, stream=None, check=True):
+    """``q`` (int8) and ``scales`` = ``x``, or act(``gate``) * x, in 8 bits with a scale per row."""
+    _sizes(T, N, ldx, activation, ldg, ldq)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_quantize(
+        T, N, _matrix("x", x, T, N, ldx, d), ldx, activation, _matrix("gate", gate, T, N, ldg, d), ldg,
+        _matrix8("q", q, T, N, ldq, d), ldq, _floats("scales", scales, T, d), s), "sgemm_quantize", check)
+
+
+def sgemm_i8(M, N, K, alpha, A, lda, a_scales, B, ldb, b_scales, beta, C, ldc, stream=None, check=True):
+    """``C = alpha * a_scales[m] * b_scales[n] * <A[m], B[n]> + beta * C``, A (M x K) and B (N x K) int8."""
+    _sizes(M, N, K, lda, ldb, ldc)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_i8(
+        M, N, K, alpha, _matrix8("A", A, M, K, lda, d), lda, _floats("a_scales", a_scales, M, d),
+        _matrix8("B", B, N, K, ldb, d), ldb, _floats("b_scales", b_scales, N, d), beta,
+        _matrix("C", C, M, N, ldc, d), ldc, s), "sgemm_i8", check)
+
+
+def sgemm_gated(T, N, K, activation, x, ldx, G, ldg, U, ldu, y, ldy, gate, ldgate, up, ldup, stream=None, check=True):
+    """``y`` = act(x G) * (x U); ``gate`` = x G and ``up`` = x U too, unless both are None."""
+    _sizes(T, N, K, activation, ldx, ldg, ldu, ldy, ldgate, ldup)
+    d, s = _begin(stream)
+    return _ret((_lib or load_library()).sgemm_gated(
+        T, N, K, activation, _matrix("x", x, T, K, ldx, d), ldx, _matrix("G", G, K, N, ldg, d), ldg,
+        _matrix("U", U, K, N, ldu, d), ldu, _matrix("y", y, T, N, ldy, d), ldy,
+        _matrix("gate", gate, T, N, ldgate, d), ldgate, _matrix("up", up, T, N, ldup, d), ldup, s),
+        "sgemm_gated", check)
+
+
+def sgemm_gated_grad_workspace_size(T, N, K) -> int:
+    return int(load_library().sgemm_gated_grad_workspace_size(int(T), int(N), int(K)))
+
+
+def sgemm_gated_grad(T, N, K, activation, x, ldx, G, ldg, U, ldu, gate, ldgate, up, ldup, dy, lddy, dx, lddx, beta, dG,
+                     lddg, dU, lddu, workspace, workspace_bytes=None, stream=None, check=True):
+    """``dx``, and ``dG`` and ``dU``, from ``dy`` and the gate and up that sgemm_gated() wrote; dx, or dG and
+    dU together, may be None."""
+    _sizes(T, N, K, activation, ldx, ldg, ldu, ldgate, ldup, lddy, lddx, lddg, lddu)
+    d, s = _begin(stream)
+    ws, nbytes = _space(workspace, workspace_bytes, d)
+    return _ret((_lib or load_library()).sgemm_gated_grad(
+        T, N, K, activation, _matrix("x", x, T, K, ldx, d), ldx, _matrix("G", G, K, N, ldg, d), ldg,
+        _matrix("U", U, K, N, ldu, d), ldu, _matrix("gate", gate, T, N, ldgate, d), ldgate,
+        _matrix("up", up, T, N, ldup, d), ldup, _matrix("dy", dy, T, N, lddy, d), lddy,
+        _matrix("dx", dx, T, K, lddx, d), lddx, beta, _matrix("dG", dG, K, N, lddg, d), lddg,
+        _matrix("dU", dU, K, N, lddu, d), lddu, ws, nbytes, s), "sgemm_gated_grad", check)

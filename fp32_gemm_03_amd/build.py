@@ -18,9 +18,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
-SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "rows.hip")]
-DEPENDS = SOURCES + [os.path.join(CSRC, "sgemm_kernels.hpp"), os.path.join(CSRC, "rows_kernels.hpp"),
-                     os.path.join(CSRC, "grouped_kernels.hpp"), os.path.join(INCLUDE, "sgemm.h")]
+SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "rows.hip"), os.path.join(CSRC, "block.hip")]
+DEPENDS = SOURCES + [os.path.join(CSRC, name) for name in (
+    "sgemm_kernels.hpp", "lanes.hpp", "rows_kernels.hpp", "grouped_kernels.hpp", "activations.hpp",
+    "norm_kernels.hpp", "i8_kernels.hpp", "gated_kernels.hpp")] + [os.path.join(INCLUDE, "sgemm.h")]
 LIBRARY = os.path.join(PKG, "libsgemm_mi355x.so")
 ARCH = "gfx950"
 

@@ -1,0 +1,458 @@
+// block.hip -- C ABI of a feed-forward block's operators (see include/sgemm.h):
+// norm, 8-bit rows and their product, gated projections, and back.  Argument checks,
+// the choice of kernel and launches on the caller's stream.  No state, no
+// allocation.
+#include "sgemm.h"
+
+#include <limits.h>
+#include <stdint.h>
+
+#include "gated_kernels.hpp"
+#include "i8_kernels.hpp"
+#include "norm_kernels.hpp"
+
+namespace {
+
+#define NEED(position, condition) \
+    if (!(condition)) return SGEMM_ERR_ARGUMENT - (position)
+
+template <class A>
+int enqueue(void (*kernel)(A), long long grid, int threads, const A &args, hipStream_t stream) {
+    if (grid <= 0) return SGEMM_OK;
+    // a launch holds fewer than 2^32 threads
+    if (grid > INT_MAX || grid * threads >= (1LL << 32)) return SGEMM_ERR_TOO_LARGE;
+    (void)hipGetLastError();  // drop any stale error so the code below is this launch's
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, args);
+    return (int)hipGetLastError();
+}
+
+// What a kernel's loop steps through in 31 bits is at most this long: no step
+// beyond the end passes INT_MAX (it would go on from below 0).
+constexpr int kLongest = INT_MAX - 4 * 4096;
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+int at_least_1(int n) { return n > 1 ? n : 1; }
+bool is_act(int a) { return a == SGEMM_ACT_SILU || a == SGEMM_ACT_GELU || a == SGEMM_ACT_GELU_TANH; }
+
+int xcd_shift() {
+    int xcds = 1, shift = 0;
+    (void)sgemm_device_shape(nullptr, &xcds);
+    while ((2 << shift) <= xcds) ++shift;
+    return shift;
+}
+
+// ---- rows in registers -------------------------------------------------------
+
+template <class A> struct RowKernel {
+    int threads, columns;
+    void (*fn)(A);
+};
+template <class A, int N> const RowKernel<A> *row_kernel(const RowKernel<A> (&table)[N], int columns) {
+    for (const RowKernel<A> &k : table)
+        if (columns <= k.columns) return &k;
+    return nullptr;
+}
+template <class A> int launch_rows(const RowKernel<A> &k, int T, const A &a, hipStream_t stream) {
+    const int rows = k.threads < 256 ? 256 / k.threads : 1;
+    return enqueue(k.fn, ceil_div(T, rows), k.threads * rows, a, stream);
+}
+
+#define ROW(fn, NT, V, ...) {NT, 4 * NT * V, fn<NT, V, ##__VA_ARGS__>}
+const RowKernel<normk::NormArgs> kNorms[] = {
+    ROW(normk::norm, 64, 1), ROW(normk::norm, 64, 2), ROW(normk::norm, 64, 4), ROW(normk::norm, 256, 2),
+    ROW(normk::norm, 256, 4), ROW(normk::norm, 512, 4), ROW(normk::norm, 1024, 4)};
+#define QUANTIZE(ACT)                                                                                          \
+    {ROW(normk::quantize, 64, 1, ACT), ROW(normk::quantize, 64, 2, ACT), ROW(normk::quantize, 64, 4, ACT),    \
+     ROW(normk::quantize, 256, 2, ACT), ROW(normk::quantize, 256, 4, ACT), ROW(normk::quantize, 512, 4, ACT), \
+     ROW(normk::quantize, 1024, 4, ACT)}
+const RowKernel<normk::QuantArgs> kQuants[4][7] = {QUANTIZE(0), QUANTIZE(1), QUANTIZE(2), QUANTIZE(-1)};
+void (*const kLongQuants[4])(normk::QuantArgs) = {normk::quantize_long<0>, normk::quantize_long<1>,
+                                                  normk::quantize_long<2>, normk::quantize_long<-1>};
+const RowKernel<normk::NormGradArgs> kNormGrads[] = {
+    ROW(normk::norm_grad, 64, 1), ROW(normk::norm_grad, 64, 2), ROW(normk::norm_grad, 256, 1),
+    ROW(normk::norm_grad, 256, 2), ROW(normk::norm_grad, 256, 4), ROW(normk::norm_grad, 512, 4)};
+
+// Shares that dweight is summed in: a workgroup each.
+int weight_shares(int T) { return T < 512 ? T : 512; }
+
+bool workspace_ok(const void *p, size_t have, size_t need) {
+    return need == 0 || (p != nullptr && have >= need && ((uintptr_t)p & 255u) == 0);
+}
+
+size_t norm_grad_bytes(int T, int N) { return round_up((size_t)weight_shares(T) * N * 4); }
+
+// ---- 8-bit products ------------------------------------------------------------
+struct I8Kernel {
+    int bm, bn, threads;
+    void (*fn)(i8k::Args);
+};
+#define I8_TILE(BM, BN, WM, WN, WPE) {BM, BN, (BM / WM) * (BN / WN) * 64, i8k::i8_tile<BM, BN, WM, WN, WPE>}
+#define I8_THIN(MB, NB, WK, WPE) {16 * MB, 16 * NB, WK * 64, i8k::i8_thin<MB, NB, WK, WPE>}
+const I8Kernel kI8Large = I8_TILE(256, 256, 128, 64, 2);
+const I8Kernel kI8Mid = I8_TILE(128, 128, 64, 64, 1);
+const I8Kernel kI8Small = I8_TILE(64, 64, 32, 32, 2);
+const I8Kernel kI8Thin1 = I8_THIN(1, 1, 8, 4);
+const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 4);
+const I8Kernel kI8Thin4 = I8_THIN(4, 1, 8, 2);
+const I8Kernel kI8Simple = {32, 32, 256, i8k::i8_simple};
+
+long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ceil_div(N, k.bn); }
+
+const I8Kernel &choose_i8(const i8k::Args &a) {
+    // the fast kernels load 16 bytes at 4-byte alignment, at 32-bit offsets from a tile's
+    // first row
+    const bool words = ((uintptr_t)a.A & 3) == 0 && ((uintptr_t)a.B & 3) == 0 && a.lda % 4 == 0 && a.ldb % 4 == 0;
+    constexpr int64_t reach = (1LL << 31) / 256 - 1024;
+    if (!words || a.lda > reach || a.ldb > reach) return kI8Simple;
+    if (a.M <= 16) return kI8Thin1;
+    if (a.M <= 32) return kI8Thin2;
+    if (a.M <= 64) return kI8Thin4;
+    if (tiles(kI8Large, a.M, a.N) >= 256) return kI8Large;
+    if (tiles(kI8Mid, a.M, a.N) >= 200) return kI8Mid;
+    return kI8Small;
+}
+
+// ---- gated projections -----------------------------------------------------------
+struct GatedKernel {
+    int bm, bn, threads;  // columns of the result
+    void (*fn)(gatedk::TileArgs);
+};
+#define FORWARD_TILE(BM, BN, BK, WM, WN, WPE) \
+    {BM, BN / 2, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::FORWARD, BM, BN, BK, WM, WN, WPE>}
+#define BACK_TILE(KIND, BM, BN, BK, WM, WN, WPE) \
+    {BM, BN, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::KIND, BM, BN, BK, WM, WN, WPE>}
+#define GATED_THIN(MB, VW, WK, WPE) {16 * MB, 16 * VW, WK * 64, gatedk::gated_thin<MB, VW, WK, WPE>}
+const GatedKernel kForward[] = {FORWARD_TILE(256, 256, 32, 64, 64, 4), FORWARD_TILE(128, 128, 32, 32, 64, 4),
+                                FORWARD_TILE(64, 64, 32, 32, 64, 2)};
+const GatedKernel kBackX[] = {BACK_TILE(BACK_X, 256, 256, 32, 64, 64, 4), BACK_TILE(BACK_X, 128, 128, 32, 32, 64, 4),
+                              BACK_TILE(BACK_X, 64, 64, 32, 32, 32, 2)};
+const GatedKernel kBackW[] = {BACK_TILE(BACK_W, 256, 256, 32, 64, 64, 4), BACK_TILE(BACK_W, 128, 128, 32, 32, 64, 4),
+                              BACK_TILE(BACK_W, 64, 64, 32, 32, 32, 2)};
+const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(2, 1, 8, 4), GATED_THIN(4, 2, 4, 2)};
+const GatedKernel kSimple[] = {{32, 32, 256, gatedk::gated_simple<gatedk::FORWARD>},
+                               {32, 32, 256, gatedk::gated_simple<gatedk::BACK_X>},
+                               {32, 32, 256, gatedk::gated_simple<gatedk::BACK_W>}};
+
+long long tiles(const GatedKernel &k, const gatedk::TileArgs &a, int kind) {
+    return ceil_div(a.M, k.bm) * ceil_div(a.N, k.bn) * (kind == gatedk::BACK_W ? 2 : 1);
+}
+
+// 32-bit offsets from a tile's first row reach all of a tile's operands
+bool reachable(const gatedk::TileArgs &a) {
+    constexpr int64_t reach = (1LL << 29) / 256 - 1024;
+    return a.lda <= reach && a.ldb[0] <= reach && a.ldb[1] <= reach;
+}
+
+int gated_product(int kind, gatedk::TileArgs a, hipStream_t stream) {
+    a.xcd_shift = xcd_shift();
+    const GatedKernel *k = &kSimple[kind];
+    if (reachable(a)) {
+        const GatedKernel *sizes = kind == gatedk::FORWARD ? kForward : kind == gatedk::BACK_X ? kBackX : kBackW;
+        if (kind == gatedk::FORWARD && a.M <= 64)
+            k = &kThin[a.M <= 16 ? 0 : a.M <= 32 ? 1 : 2];
+        else
+            k = &sizes[tiles(sizes[0], a, kind) >= 256 ? 0 : tiles(sizes[1], a, kind) >= 256 ? 1 : 2];
+    }
+    return enqueue(k->fn, tiles(*k, a, kind), k->threads, a, stream);
+}
+
+// Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors
+int64_t slope_ld(int N) { return ((int64_t)N + 3) / 4 * 4; }
+size_t gated_grad_bytes(int T, int N) { return 2 * round_up((size_t)T * slope_ld(N) * 4); }
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_norm(int T, int N, const float *x, int ldx, const float *residual, int ldr, const float *weight, float eps,
+               float *sum, int lds, float *y, int ldy, signed char *q, int ldq, float *scales, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, N >= 0);
+    const bool empty = T == 0 || N == 0;
+    NEED(3, (empty || x != nullptr) && aligned4(x));
+    NEED(4, ldx >= at_least_1(N));
+    NEED(5, aligned4(residual));
+    NEED(6, ldr >= at_least_1(N));
+    NEED(7, aligned4(weight));
+    NEED(8, eps >= 0.0f && eps <= 3.402823466e38f);
+    NEED(9, aligned4(sum));
+    NEED(10, lds >= at_least_1(N));
+    NEED(11, aligned4(y));
+    NEED(12, ldy >= at_least_1(N));
+    NEED(14, ldq >= at_least_1(N));
+    NEED(15, (T == 0 || q == nullptr || scales != nullptr) && aligned4(scales));
+    if (T == 0 || (N == 0 && q == nullptr) || (sum == nullptr && y == nullptr && q == nullptr)) return SGEMM_OK;
+    if (T > kLongest || N > kLongest) return SGEMM_ERR_TOO_LARGE;
+    normk::NormArgs a;
+    a.T = T;
+    a.N = N;
+    a.eps = (double)eps;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.sum = sum;
+    a.y = y;
+    a.scales = scales;
+    a.lds = lds;
+    a.ldy = ldy;
+    a.ldq = ldq;
+    a.q = q;
+    const RowKernel<normk::NormArgs> *k = row_kernel(kNorms, N);
+    if (k == nullptr) return enqueue(normk::norm_long, T, normk::kLongThreads, a, stream);
+    return launch_rows(*k, T, a, stream);
+}
+
+size_t sgemm_norm_grad_workspace_size(int T, int N) { return T < 0 || N < 0 ? 0 : norm_grad_bytes(T, N); }
+
+int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, float eps, const float *dy, int lddy,
+                    const float *dsum, int ldds, float *dh, int lddh, float beta, float *dweight, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, N >= 0);
+    const bool empty = T == 0 || N == 0;
+    NEED(3, (empty || h != nullptr) && aligned4(h));
+    NEED(4, ldh >= at_least_1(N));
+    NEED(5, aligned4(weight));
+    NEED(6, eps >= 0.0f && eps <= 3.402823466e38f);
+    NEED(7, (empty || dy != nullptr) && aligned4(dy));
+    NEED(8, lddy >= at_least_1(N));
+    NEED(9, aligned4(dsum));
+    NEED(10, ldds >= at_least_1(N));
+    NEED(11, aligned4(dh));
+    NEED(12, lddh >= at_least_1(N));
+    NEED(14, aligned4(dweight));
+    if (N == 0 || (dh == nullptr && dweight == nullptr)) return SGEMM_OK;
+    if (dweight != nullptr && !workspace_ok(workspace, workspace_bytes, norm_grad_bytes(T, N))) return SGEMM_ERR_WORKSPACE;
+    if (T > kLongest || N > kLongest) return SGEMM_ERR_TOO_LARGE;
+    normk::NormGradArgs a;
+    a.T = T;
+    a.N = N;
+    a.eps = (double)eps;
+    a.h = h;
+    a.weight = weight;
+    a.dy = dy;
+    a.dsum = dsum;
+    a.ldh = ldh;
+    a.lddy = lddy;
+    a.ldds = ldds;
+    a.lddh = lddh;
+    a.dh = dh;
+    a.part = dweight == nullptr ? nullptr : static_cast<float *>(workspace);
+    a.dweight = dweight;
+    a.beta = beta;
+    a.P = weight_shares(T);
+    const RowKernel<normk::NormGradArgs> *k = row_kernel(kNormGrads, N);
+    const int rc = k == nullptr ? enqueue(normk::norm_grad_long, a.P, normk::kLongThreads, a, stream)
+                                : enqueue(k->fn, a.P, k->threads, a, stream);
+    if (rc != SGEMM_OK || dweight == nullptr) return rc;
+    return enqueue(normk::norm_weight_grad, ceil_div(N, 64), 64 * normk::kShareWaves, a, stream);
+}
+
+int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const float *gate, int ldg, signed char *q,
+                   int ldq, float *scales, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, N >= 0);
+    const bool empty = T == 0 || N == 0;
+    NEED(3, (empty || x != nullptr) && aligned4(x));
+    NEED(4, ldx >= at_least_1(N));
+    NEED(5, is_act(activation));
+    NEED(6, aligned4(gate));
+    NEED(7, ldg >= at_least_1(N));
+    NEED(8, empty || q != nullptr);
+    NEED(9, ldq >= at_least_1(N));
+    NEED(10, (T == 0 || scales != nullptr) && aligned4(scales));
+    if (T == 0) return SGEMM_OK;
+    if (T > kLongest || N > kLongest) return SGEMM_ERR_TOO_LARGE;
+    normk::QuantArgs a;
+    a.T = T;
+    a.N = N;
+    a.x = x;
+    a.gate = gate;
+    a.ldx = ldx;
+    a.ldg = ldg;
+    a.ldq = ldq;
+    a.q = q;
+    a.scales = scales;
+    const int kind = gate == nullptr ? 3 : activation;
+    const RowKernel<normk::QuantArgs> *k = row_kernel(kQuants[kind], N);
+    if (k == nullptr) return enqueue(kLongQuants[kind], T, normk::kLongThreads, a, stream);
+    return launch_rows(*k, T, a, stream);
+}
+
+int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, const float *a_scales,
+             const signed char *B, int ldb, const float *b_scales, float beta, float *C, int ldc, hipStream_t stream) {
+    NEED(1, M >= 0);
+    NEED(2, N >= 0);
+    NEED(3, K >= 0);
+    const bool empty = M == 0 || N == 0;
+    const bool product = !empty && K > 0 && alpha != 0.0f;
+    NEED(5, !product || A != nullptr);
+    NEED(6, lda >= at_least_1(K));
+    NEED(7, aligned4(a_scales));
+    NEED(8, !product || B != nullptr);
+    NEED(9, ldb >= at_least_1(K));
+    NEED(10, aligned4(b_scales));
+    NEED(12, (empty || C != nullptr) && aligned4(C));
+    NEED(13, ldc >= at_least_1(N));
+    if (empty || (!product && beta == 1.0f)) return SGEMM_OK;
+    if (K > SGEMM_I8_MAX_K || M > kLongest || N > kLongest) return SGEMM_ERR_TOO_LARGE;
+    i8k::Args a;
+    a.M = M;
+    a.N = N;
+    a.K = product ? K : 0;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.A = A;
+    a.B = B;
+    a.sa = a_scales;
+    a.sb = b_scales;
+    a.C = C;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.xcd_shift = xcd_shift();
+    const I8Kernel &k = choose_i8(a);
+    return enqueue(k.fn, tiles(k, M, N), k.threads, a, stream);
+}
+
+int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg, const float *U,
+                int ldu, float *y, int ldy, float *gate, int ldgate, float *up, int ldup, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, N >= 0);
+    NEED(3, K >= 0);
+    NEED(4, is_act(activation));
+    const bool empty = T == 0 || N == 0, product = !empty && K > 0;
+    NEED(5, (!product || x != nullptr) && aligned4(x));
+    NEED(6, ldx >= at_least_1(K));
+    NEED(7, (!product || G != nullptr) && aligned4(G));
+    NEED(8, ldg >= at_least_1(N));
+    NEED(9, (!product || U != nullptr) && aligned4(U));
+    NEED(10, ldu >= at_least_1(N));
+    NEED(11, (empty || y != nullptr) && aligned4(y));
+    NEED(12, ldy >= at_least_1(N));
+    NEED(13, aligned4(gate));
+    NEED(14, ldgate >= at_least_1(N));
+    NEED(15, (gate == nullptr) == (up == nullptr) && aligned4(up));
+    NEED(16, ldup >= at_least_1(N));
+    if (empty) return SGEMM_OK;
+    if (T > kLongest || N > kLongest || K > kLongest) return SGEMM_ERR_TOO_LARGE;
+    gatedk::TileArgs a = {};
+    a.M = T;
+    a.N = N;
+    a.K = K;
+    a.act = activation;
+    a.A[0] = a.A[1] = x;
+    a.B[0] = G;
+    a.B[1] = U;
+    a.lda = ldx;
+    a.ldb[0] = ldg;
+    a.ldb[1] = ldu;
+    a.C[0] = a.C[1] = y;
+    a.ldc[0] = a.ldc[1] = ldy;
+    a.gate = gate;
+    a.up = up;
+    a.ldgate = ldgate;
+    a.ldup = ldup;
+    return gated_product(gatedk::FORWARD, a, stream);
+}
+
+size_t sgemm_gated_grad_workspace_size(int T, int N, int K) {
+    return T < 0 || N < 0 || K < 0 ? 0 : gated_grad_bytes(T, N);
+}
+
+int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg,
+                     const float *U, int ldu, const float *gate, int ldgate, const float *up, int ldup,
+                     const float *dy, int lddy, float *dx, int lddx, float beta, float *dG, int lddg, float *dU,
+                     int lddu, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    NEED(1, T >= 0);
+    NEED(2, N >= 0);
+    NEED(3, K >= 0);
+    NEED(4, is_act(activation));
+    const bool to_x = dx != nullptr && T > 0 && K > 0, to_w = dG != nullptr && N > 0 && K > 0;
+    const bool slopes = T > 0 && N > 0 && (to_x || to_w);  // else the sums are empty
+    NEED(5, (!(slopes && to_w) || x != nullptr) && aligned4(x));
+    NEED(6, ldx >= at_least_1(K));
+    NEED(7, (!(slopes && to_x) || G != nullptr) && aligned4(G));
+    NEED(8, ldg >= at_least_1(N));
+    NEED(9, (!(slopes && to_x) || U != nullptr) && aligned4(U));
+    NEED(10, ldu >= at_least_1(N));
+    NEED(11, (!slopes || gate != nullptr) && aligned4(gate));
+    NEED(12, ldgate >= at_least_1(N));
+    NEED(13, (!slopes || up != nullptr) && aligned4(up));
+    NEED(14, ldup >= at_least_1(N));
+    NEED(15, (!slopes || dy != nullptr) && aligned4(dy));
+    NEED(16, lddy >= at_least_1(N));
+    NEED(17, aligned4(dx));
+    NEED(18, lddx >= at_least_1(K));
+    NEED(20, aligned4(dG));
+    NEED(21, lddg >= at_least_1(N));
+    NEED(22, (dG == nullptr) == (dU == nullptr) && aligned4(dU));
+    NEED(23, lddu >= at_least_1(N));
+    if (slopes && !workspace_ok(workspace, workspace_bytes, gated_grad_bytes(T, N))) return SGEMM_ERR_WORKSPACE;
+    if (T > kLongest || N > kLongest || K > kLongest) return SGEMM_ERR_TOO_LARGE;
+    const int64_t ldz = slope_ld(N);
+    float *dgate = static_cast<float *>(workspace);
+    float *dup = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up((size_t)T * ldz * 4));
+    if (slopes) {
+        gatedk::SlopeArgs s;
+        s.T = T;
+        s.N = N;
+        s.gate = gate;
+        s.up = up;
+        s.dy = dy;
+        s.ldgate = ldgate;
+        s.ldup = ldup;
+        s.lddy = lddy;
+        s.ldz = ldz;
+        s.dgate = dgate;
+        s.dup = dup;
+        s.chunks = (int)ceil_div(ldz, 256);
+        s.units = (int64_t)T * s.chunks;
+        const int rc = enqueue(activation == SGEMM_ACT_SILU   ? gatedk::gated_slopes<normk::kSilu>
+                               : activation == SGEMM_ACT_GELU ? gatedk::gated_slopes<normk::kGelu>
+                                                              : gatedk::gated_slopes<normk::kGeluTanh>,
+                               ceil_div(s.units, 4), 256, s, stream);
+        if (rc != SGEMM_OK) return rc;
+    }
+    gatedk::TileArgs a = {};
+    if (to_x) {
+        a.M = T;
+        a.N = K;
+        a.K = N;
+        a.A[0] = dgate;
+        a.A[1] = dup;
+        a.lda = ldz;
+        a.B[0] = G;
+        a.B[1] = U;
+        a.ldb[0] = ldg;
+        a.ldb[1] = ldu;
+        a.C[0] = a.C[1] = dx;
+        a.ldc[0] = a.ldc[1] = lddx;
+        const int rc = gated_product(gatedk::BACK_X, a, stream);
+        if (rc != SGEMM_OK) return rc;
+    }
+    if (to_w && !(T == 0 && beta == 1.0f)) {
+        a = {};
+        a.M = K;
+        a.N = N;
+        a.K = T;
+        a.A[0] = a.A[1] = x;
+        a.lda = ldx;
+        a.B[0] = dgate;
+        a.B[1] = dup;
+        a.ldb[0] = a.ldb[1] = ldz;
+        a.C[0] = dG;
+        a.C[1] = dU;
+        a.ldc[0] = lddg;
+        a.ldc[1] = lddu;
+        a.beta = beta;
+        return gated_product(gatedk::BACK_W, a, stream);
+    }
+    return SGEMM_OK;
+}
+
+}  // extern "C"

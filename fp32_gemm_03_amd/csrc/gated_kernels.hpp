@@ -1,0 +1,523 @@
+// gated_kernels.hpp -- a gated feed-forward block's products on the matrix cores:
+// gate = x G, up = x U, y = act(gate) up, and back.
+//
+//   * gated_tile: LDS tiles; one product of x with [G | U] (the activation in the
+//     epilogue), dgate G^T + dup U^T as one sum, or x^T [dgate | dup].
+//   * gated_thin: few rows; operands from memory straight to the matrix cores.
+//   * gated_slopes: dgate and dup from dy and what the forward kept.
+//   * gated_simple: any strides.
+#pragma once
+
+#include "activations.hpp"
+#include "lanes.hpp"
+
+namespace gatedk {
+
+using rowk::f32x4u;
+using rowk::rsrc_t;
+using rowk::whole_rsrc;
+using sgk::f32x2;
+using sgk::f32x4;
+using sgk::floatx16;
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+template <int ACT> __device__ __forceinline__ float act32(float g) { return normk::act<ACT>(g); }
+__device__ __forceinline__ float act32(int kind, float g) {
+    return kind == normk::kSilu ? act32<normk::kSilu>(g) : kind == normk::kGelu ? act32<normk::kGelu>(g)
+                                                                                 : act32<normk::kGeluTanh>(g);
+}
+__device__ __forceinline__ float gated(int kind, float g, float u) { return act32(kind, g) * u; }
+
+enum Kind { FORWARD, BACK_X, BACK_W };
+
+// What is summed, by kind (M x N the result):
+//   FORWARD  A x (M x K), B G and U (K x N)         K of both the same
+//   BACK_X   A dgate and dup (M x K), B G and U (N x K)   one sum over both
+//   BACK_W   A x (K x M), B dgate and dup (K x N)   a result each
+struct TileArgs {
+    int M, N, K, act;
+    const float *A[2], *B[2];
+    int64_t lda, ldb[2];
+    float beta;
+    float *C[2], *gate, *up;  // FORWARD: C[0] is y, gate and up may be NULL
+    int64_t ldc[2], ldgate, ldup;
+    int xcd_shift;
+};
+
+// ---------------------------------------------------------------------------
+// One operand's part of an LDS stage, filled by loads that write LDS directly
+// (instruction p of wave w fills floats (p WAVES + w) 256 ..).
+//   Along K (`Long`): rows of BK floats, the 16-byte chunks of a row permuted so
+//     that loads and fragment reads both touch every bank (AKLayout).
+//   Across (`Wide`): BK rows of COLS floats as they are.
+// ---------------------------------------------------------------------------
+template <int ROWS, int BK, int NT> struct Long {
+    static constexpr int WAVES = NT / 64, P = ROWS * BK / (NT * 4), SIZE = ROWS * BK;
+    static_assert(P * NT * 4 == ROWS * BK, "whole instructions");
+    uint32_t off[P];
+    int col[P];
+    __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int f = (p * WAVES + wave) * 256 + 4 * lane, row = f / BK;
+            col[p] = 4 * sgk::AKLayout<BK>::chunk_pos(row, f % BK / 4);
+            off[p] = (uint32_t)((row * ld + col[p]) * 4);
+        }
+    }
+    // r begins at the tile's first row and column; `left` columns of K are there
+    __device__ __forceinline__ void load(rsrc_t r, float *lds, int wave, int p, int left) const {
+        sgk::load_to_lds<4>(r, lds + (p * WAVES + wave) * 256, col[p] < left ? off[p] : rowk::kOut);
+    }
+    // the chunk that holds K's last column also brought what follows it in the row
+    __device__ __forceinline__ void clear(float *lds, int wave, int lane, int left) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int n = left - col[p];
+            float *q = lds + (p * WAVES + wave) * 256 + 4 * lane;
+            if (n > 0 && n < 4)
+#pragma unroll
+                for (int j = 1; j < 4; ++j)
+                    if (j >= n) q[j] = 0.0f;
+        }
+    }
+};
+template <int COLS, int BK, int NT> struct Wide {
+    static constexpr int WAVES = NT / 64, P = COLS * BK / (NT * 4), SIZE = COLS * BK;
+    static_assert(P * NT * 4 == COLS * BK, "whole instructions");
+    uint32_t off[P];
+    __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int f = (p * WAVES + wave) * 256 + 4 * lane;
+            off[p] = (uint32_t)((f / COLS * ld + f % COLS) * 4);
+        }
+    }
+    __device__ __forceinline__ void load(rsrc_t r, float *lds, int wave, int p, int) const {
+        sgk::load_to_lds<4>(r, lds + (p * WAVES + wave) * 256, off[p]);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Tiles of BM x BN (FORWARD: BN / 2 columns of gate and the same of up), K in tiles
+// of BK, two LDS stages, WM x WN per wave with v_mfma_f32_32x32x2_f32.  Within a K
+// tile lane half lh takes k = lh BK / 2 + j in k-step j, of both operands.
+// FORWARD's wave holds gate and up of the same columns (block columns 2 j and 2 j +
+// 1), so the activation's product is taken in registers.
+// ---------------------------------------------------------------------------
+template <int KIND, int BM, int BN, int BK, int WM, int WN, int WPE>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+gated_tile(TileArgs a) {
+    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
+    constexpr bool DUAL = KIND == FORWARD, A_WIDE = KIND == BACK_W, B_LONG = KIND == BACK_X;
+    constexpr int CN = DUAL ? BN / 2 : BN;  // columns of the result
+    static_assert(!DUAL || NI % 2 == 0, "gate and up in pairs of block columns");
+    typedef typename std::conditional<A_WIDE, Wide<BM, BK, NT>, Long<BM, BK, NT>>::type SA;
+    typedef typename std::conditional<B_LONG, Long<BN, BK, NT>, Wide<CN, BK, NT>>::type SB;
+    constexpr int STAGE = (BM + BN) * BK;
+    __shared__ __attribute__((aligned(16))) float smem[2 * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 31, lh = lane >> 5;
+    const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + CN - 1) / CN;
+    int tm, tn;
+    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, KIND == BACK_W ? 2 * nbn : nbn, a.xcd_shift, tm, tn);
+    const int which = KIND == BACK_W && tn >= nbn ? 1 : 0;  // BACK_W: dG's columns, then dU's
+    const int bm = tm * BM, bn = (tn - which * nbn) * CN;
+
+    SA sa;
+    SB sb;
+    sa.init(a.lda, wave, lane);
+    sb.init(a.ldb[which], wave, lane);  // (FORWARD and BACK_X: of both)
+    SB sb2;
+    if constexpr (KIND != BACK_W) sb2.init(a.ldb[1], wave, lane);
+
+    const int KT1 = (a.K + BK - 1) / BK, KT = KIND == BACK_X ? 2 * KT1 : KT1;
+    // loads of K tile t, piece p: A's, then B's (DUAL: G's, then U's)
+    constexpr int DP = SA::P + (DUAL ? 2 : 1) * SB::P;
+    auto fetch = [&](float *st, int t, int p) {
+        const int seg = KIND == BACK_X && t >= KT1 ? 1 : 0;
+        const int64_t k0 = (int64_t)(t - seg * KT1) * BK;
+        const int64_t left = t < KT ? a.K - k0 : 0;  // (past the last tile nothing is read)
+        if (p < SA::P) {
+            const float *A = a.A[seg];
+            const rsrc_t r = A_WIDE ? whole_rsrc(A + k0 * a.lda + bm, left > 0 ? ((left - 1) * a.lda + (a.M - bm)) * 4 : 0)
+                                    : whole_rsrc(A + (int64_t)bm * a.lda + k0,
+                                                 left > 0 ? ((int64_t)(a.M - bm - 1) * a.lda + left) * 4 : 0);
+            sa.load(r, st, wave, p, (int)left);
+            return;
+        }
+        p -= SA::P;
+        const int src = DUAL ? (p >= SB::P ? 1 : 0) : KIND == BACK_X ? seg : which;
+        const float *B = a.B[src];
+        const int64_t ldb = a.ldb[src];
+        const rsrc_t r = B_LONG ? whole_rsrc(B + (int64_t)bn * ldb + k0, left > 0 ? ((int64_t)(a.N - bn - 1) * ldb + left) * 4 : 0)
+                                : whole_rsrc(B + k0 * ldb + bn, left > 0 ? ((left - 1) * ldb + (a.N - bn)) * 4 : 0);
+        float *lds = st + SA::SIZE;
+        if constexpr (DUAL) {
+            if (src == 1) sb2.load(r, lds + SB::SIZE, wave, p - SB::P, (int)left);
+            else sb.load(r, lds, wave, p, (int)left);
+        } else if constexpr (KIND == BACK_X) {
+            if (src == 1) sb2.load(r, lds, wave, p, (int)left);
+            else sb.load(r, lds, wave, p, (int)left);
+        } else {
+            sb.load(r, lds, wave, p, (int)left);
+        }
+    };
+    auto landed = [&](float *st, int t) {
+        __builtin_amdgcn_s_waitcnt(0);
+        if constexpr (KIND != BACK_W) {
+            const int left = a.K - (KIND == BACK_X && t >= KT1 ? t - KT1 : t) * BK;
+            if ((a.K & 3) != 0 && t < KT && left > 0 && left < BK) {
+                sa.clear(st, wave, lane, left);
+                if constexpr (B_LONG) sb.clear(st + SA::SIZE, wave, lane, left);
+            }
+        }
+        __syncthreads();
+    };
+
+    floatx16 acc[MI][NI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    // A chunk is four k-steps: q of BK / 8, lane half lh its own
+    constexpr int QN = BK / 8;
+    int at[QN];  // of a row's chunk (rows wm + 32 i and wn + 32 j + li: one permutation)
+    if constexpr (!A_WIDE) {
+#pragma unroll
+        for (int q = 0; q < QN; ++q) at[q] = 4 * sgk::AKLayout<BK>::chunk_pos(li, lh * QN + q);
+    }
+    const int a_at = A_WIDE ? lh * (BK / 2) * BM + wm + MI * li : (wm + li) * BK;
+    const int b_at = SA::SIZE + (B_LONG ? (wn + li) * BK
+                                        : lh * (BK / 2) * CN + (DUAL ? wn / 2 + NI / 2 * li : wn + NI * li));
+
+    auto tile = [&](const float *__restrict__ st, float *__restrict__ nx, int tnext) {
+        float av[2][MI][4], bv[2][NI][4];
+        auto read_a = [&](int d, int q) {
+            if constexpr (A_WIDE) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    typedef typename sgk::vec_t<MI>::type V;
+                    const V v = *reinterpret_cast<const V *>(st + a_at + (4 * q + e) * BM);
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) av[d][i][e] = sgk::vget(v, i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const float4 v = *reinterpret_cast<const float4 *>(st + a_at + i * 32 * BK + at[q]);
+                    av[d][i][0] = v.x;
+                    av[d][i][1] = v.y;
+                    av[d][i][2] = v.z;
+                    av[d][i][3] = v.w;
+                }
+            }
+        };
+        auto read_b = [&](int d, int q) {
+            if constexpr (B_LONG) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    const float4 v = *reinterpret_cast<const float4 *>(st + b_at + j * 32 * BK + at[q]);
+                    bv[d][j][0] = v.x;
+                    bv[d][j][1] = v.y;
+                    bv[d][j][2] = v.z;
+                    bv[d][j][3] = v.w;
+                }
+            } else {
+                constexpr int W = DUAL ? NI / 2 : NI;
+                typedef typename sgk::vec_t<W>::type V;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int s = 0; s < (DUAL ? 2 : 1); ++s) {
+                        const V v = *reinterpret_cast<const V *>(st + b_at + s * SB::SIZE + (4 * q + e) * CN);
+#pragma unroll
+                        for (int j = 0; j < W; ++j) bv[d][DUAL ? 2 * j + s : j][e] = sgk::vget(v, j);
+                    }
+            }
+        };
+        read_b(0, 0);
+        read_a(0, 0);
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+            if (q + 1 < QN) {
+                read_b((q + 1) & 1, q + 1);
+                read_a((q + 1) & 1, q + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(av[q & 1][i][e], bv[q & 1][j][e], acc[i][j], 0, 0, 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                        // the next tile's loads, in pieces behind the first chunk's MFMAs
+                        constexpr int U = 4 * MI * NI;
+                        const int u = (e * MI + i) * NI + j;
+                        if (q == 0) {
+#pragma unroll
+                            for (int p = 0; p < DP; ++p)
+                                if (p * U / DP == u) fetch(nx, tnext, p);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+        }
+    };
+    if (KT > 0) {
+#pragma unroll
+        for (int p = 0; p < DP; ++p) fetch(smem, 0, p);
+        landed(smem, 0);
+        for (int t = 0; t < KT; ++t) {
+            tile(smem + (t & 1) * STAGE, smem + ((t + 1) & 1) * STAGE, t + 1);
+            landed(smem + ((t + 1) & 1) * STAGE, t + 1);
+        }
+    }
+
+    // Register r of block (i, j) on lane (li, lh): block row 8 (r / 4) + 4 lh + r % 4 = b
+    // of the wave's row 32 i + b (A along K) or MI b + i (across); column 32 j + li (B
+    // along K), NI li + j (across), NI / 2 li + j / 2 of gate (even j) and up (odd).
+    const int W = DUAL ? NI / 2 : NI;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int b = 8 * (r >> 2) + 4 * lh + (r & 3);
+            const int m = bm + wm + (A_WIDE ? MI * b + i : 32 * i + b);
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int n = bn + (B_LONG ? wn + 32 * j + li : DUAL ? wn / 2 + W * li + j : wn + W * li + j);
+                if (n >= a.N) continue;
+                float *c = a.C[which] + (int64_t)m * a.ldc[which] + n;
+                if constexpr (DUAL) {
+                    const float g = acc[i][2 * j][r], u = acc[i][2 * j + 1][r];
+                    *c = gated(a.act, g, u);
+                    if (a.gate != nullptr) {
+                        a.gate[(int64_t)m * a.ldgate + n] = g;
+                        a.up[(int64_t)m * a.ldup + n] = u;
+                    }
+                } else {
+                    *c = a.beta != 0.0f ? fmaf(a.beta, *c, acc[i][j][r]) : acc[i][j][r];
+                }
+            }
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: reading G and U once is the work.  16 MB rows and 16 VW columns of both a
+// workgroup, its WK waves each a share of K, operands from memory straight to
+// v_mfma_f32_16x16x4_f32: lane (li, lk) loads VW consecutive columns of k = 4 lk + e
+// of 16 k's, and the four k's of a row of x.  Partial sums meet in LDS in order.
+// ---------------------------------------------------------------------------
+template <int MB, int VW, int WK, int WPE>
+__global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) gated_thin(TileArgs a) {
+    constexpr int BM = 16 * MB, BN = 16 * VW;
+    __shared__ __attribute__((aligned(16))) float part[WK][2][BM * BN];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lk = lane >> 4;
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
+    int tm, tn;
+    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const float *A = a.A[0] + (int64_t)m0 * a.lda;
+    const int64_t a_bytes = ((int64_t)(a.M - m0 - 1) * a.lda + a.K) * 4;
+    uint32_t ao[MB], bo[2][4];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) ao[i] = (uint32_t)(((16 * i + li) * a.lda + 4 * lk) * 4);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bo[s][e] = (uint32_t)(((4 * lk + e) * a.ldb[s] + VW * li) * 4);
+
+    floatx4 acc[2][MB][VW];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) acc[s][i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int steps = (a.K + 15) / 16;
+    const int u0 = (int)((int64_t)steps * w / WK), u1 = (int)((int64_t)steps * (w + 1) / WK);
+    constexpr int STEP = 8 * VW + 4 * MB, D = 96 / STEP < 8 ? (96 / STEP < 2 ? 2 : 96 / STEP) : 8;
+    f32x4 av[D][MB];
+    float bv[D][2][4][VW];
+    auto fetch = [&](int d, int u) {  // (past the wave's last step the descriptors are empty)
+        const int64_t k0 = 16 * (int64_t)u;
+        const bool there = u < u1;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const rsrc_t rb = whole_rsrc(a.B[s] + k0 * a.ldb[s] + n0, there ? ((a.K - k0 - 1) * a.ldb[s] + (a.N - n0)) * 4 : 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (VW == 4) {
+                    const f32x4 v = sgk::raw_load_v4f32(rb, bo[s][e], 0, 0);
+                    bv[d][s][e][0] = v.x;
+                    bv[d][s][e][1] = v.y;
+                    bv[d][s][e][2] = v.z;
+                    bv[d][s][e][3] = v.w;
+                } else if constexpr (VW == 2) {
+                    const f32x2 v = sgk::raw_load_v2f32(rb, bo[s][e], 0, 0);
+                    bv[d][s][e][0] = v.x;
+                    bv[d][s][e][1] = v.y;
+                } else {
+                    bv[d][s][e][0] = sgk::raw_load_f32(rb, bo[s][e], 0, 0);
+                }
+            }
+        }
+        const rsrc_t ra = whole_rsrc(A + k0, there ? a_bytes - 4 * k0 : 0);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) av[d][i] = sgk::raw_load_v4f32(ra, ao[i], 0, 0);
+    };
+    auto multiply = [&](int d) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < VW; ++j)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+                        acc[s][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[d][i][e], bv[d][s][e][j], acc[s][i][j], 0, 0, 0);
+    };
+    const int whole = (int64_t)u1 * 16 > a.K ? u1 - 1 : u1;
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, u0 + d);
+    for (int u = u0; u < u1; u += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (u + d == whole) {  // K's end: x's row goes on into what follows it
+                const int left = a.K - 16 * whole - 4 * lk;
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) av[d][i][e] = e < left ? av[d][i][e] : 0.0f;
+            }
+            if (u + d < u1) multiply(d);
+            if (u + D < u1) fetch(d, u + d + D);
+        }
+    }
+    // acc[s][i][j] register r on lane (li, lk): row 16 i + 4 lk + r, column VW li + j
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < VW; ++j) part[w][s][(16 * i + 4 * lk + r) * BN + VW * li + j] = acc[s][i][j][r];
+    __syncthreads();
+    for (int f = tid; f < BM * BN; f += WK * 64) {
+        const int m = m0 + f / BN, n = n0 + f % BN;
+        if (m >= a.M || n >= a.N) continue;
+        float g = part[0][0][f], u = part[0][1][f];
+#pragma unroll
+        for (int i = 1; i < WK; ++i) {
+            g += part[i][0][f];
+            u += part[i][1][f];
+        }
+        a.C[0][(int64_t)m * a.ldc[0] + n] = gated(a.act, g, u);
+        if (a.gate != nullptr) {
+            a.gate[(int64_t)m * a.ldgate + n] = g;
+            a.up[(int64_t)m * a.ldup + n] = u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dgate = dy up act'(gate), dup = dy act(gate), rows ldz apart, the columns up to
+// ldz 0 (so that what reads them along N needs no end).
+// ---------------------------------------------------------------------------
+struct SlopeArgs {
+    int T, N;
+    const float *gate, *up, *dy;
+    int64_t ldgate, ldup, lddy, ldz;
+    float *dgate, *dup;
+    int chunks;  // of 256 columns a wave each
+    int64_t units;
+};
+
+template <int ACT> __global__ void __launch_bounds__(256) gated_slopes(SlopeArgs a) {
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (unit >= a.units) return;
+    const int64_t t = unit / a.chunks;
+    const int n = (int)(unit - t * a.chunks) * 256 + 4 * (threadIdx.x & 63);
+    if (n >= a.ldz) return;
+    const int left = a.N - n;
+    const f32x4u g = rowk::load4(a.gate + t * a.ldgate + n, left), u = rowk::load4(a.up + t * a.ldup + n, left);
+    const f32x4u d = rowk::load4(a.dy + t * a.lddy + n, left);
+    f32x4u dg, du;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        dg[e] = d[e] * u[e] * normk::act_slope<ACT>(g[e]);
+        du[e] = d[e] * act32<ACT>(g[e]);
+    }
+    *reinterpret_cast<f32x4u *>(a.dgate + t * a.ldz + n) = dg;
+    *reinterpret_cast<f32x4u *>(a.dup + t * a.ldz + n) = du;
+}
+
+// ---------------------------------------------------------------------------
+// Any strides: 32 x 32 tiles, every element checked.
+// ---------------------------------------------------------------------------
+template <int KIND> __global__ void __launch_bounds__(256) gated_simple(TileArgs a) {
+    constexpr int T = 32;
+    __shared__ float As[T][T + 1], Bs[2][T][T + 1];
+    const int nbn = (a.N + T - 1) / T;
+    const int cols = KIND == BACK_W ? 2 * nbn : nbn;
+    const int tn = (int)(blockIdx.x % cols), which = KIND == BACK_W && tn >= nbn ? 1 : 0;
+    const int64_t m0 = (int64_t)(blockIdx.x / cols) * T, n0 = (int64_t)(tn - which * nbn) * T;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int seg = 0; seg < (KIND == BACK_X ? 2 : 1); ++seg)
+        for (int64_t k0 = 0; k0 < a.K; k0 += T) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = ty + 8 * i;
+                // As[m][k], Bs[k][n]; lanes walk what is contiguous
+                if (KIND == BACK_W)
+                    As[tx][r] = k0 + r < a.K && m0 + tx < a.M ? a.A[0][(k0 + r) * a.lda + m0 + tx] : 0.0f;
+                else
+                    As[r][tx] = k0 + tx < a.K && m0 + r < a.M ? a.A[seg][(m0 + r) * a.lda + k0 + tx] : 0.0f;
+#pragma unroll
+                for (int s = 0; s < (KIND == FORWARD ? 2 : 1); ++s) {
+                    const int src = KIND == FORWARD ? s : KIND == BACK_X ? seg : which;
+                    const float *B = a.B[src];
+                    const int64_t ldb = a.ldb[src];
+                    if (KIND == BACK_X)
+                        Bs[s][tx][r] = k0 + tx < a.K && n0 + r < a.N ? B[(n0 + r) * ldb + k0 + tx] : 0.0f;
+                    else
+                        Bs[s][r][tx] = k0 + r < a.K && n0 + tx < a.N ? B[(k0 + r) * ldb + n0 + tx] : 0.0f;
+                }
+            }
+            __syncthreads();
+            for (int k = 0; k < T; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[0][i] = fmaf(As[ty + 8 * i][k], Bs[0][k][tx], acc[0][i]);
+                    if (KIND == FORWARD) acc[1][i] = fmaf(As[ty + 8 * i][k], Bs[1][k][tx], acc[1][i]);
+                }
+            __syncthreads();
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + ty + 8 * i, n = n0 + tx;
+        if (m >= a.M || n >= a.N) continue;
+        float *c = a.C[which] + m * a.ldc[which] + n;
+        if (KIND == FORWARD) {
+            *c = gated(a.act, acc[0][i], acc[1][i]);
+            if (a.gate != nullptr) {
+                a.gate[m * a.ldgate + n] = acc[0][i];
+                a.up[m * a.ldup + n] = acc[1][i];
+            }
+        } else {
+            *c = a.beta != 0.0f ? fmaf(a.beta, *c, acc[0][i]) : acc[0][i];
+        }
+    }
+}
+
+}  // namespace gatedk

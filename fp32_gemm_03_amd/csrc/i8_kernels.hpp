@@ -1,0 +1,349 @@
+// i8_kernels.hpp -- the product of 8-bit rows with 8-bit channels, scaled by row and
+// channel:  C[m][n] = alpha sa[m] sb[n] sum_k A[m][k] B[n][k] + beta C[m][n].
+//
+// Both operands run along K, so a lane's 16 bytes of a row are what the matrix
+// instructions take, of A and of B alike; the order of k inside an instruction is
+// the same for both and does not matter.  The sum is exact: 32-bit integers hold
+// 131071 products of -128 by -128.  The rest is computed in 64 bits and rounded
+// once.
+//
+//   * i8_tile: LDS tiles filled by loads that write LDS directly.
+//   * i8_thin: few rows; operands from memory straight to the matrix cores.
+//   * i8_simple: rows of any alignment.
+#pragma once
+
+#include "lanes.hpp"
+
+namespace i8k {
+
+using rowk::rsrc_t;
+using rowk::whole_rsrc;
+
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef int intx16 __attribute__((ext_vector_type(16)));
+
+struct Args {
+    int M, N, K;  // K == 0 also when alpha == 0 (A, B and the scales not read)
+    float alpha, beta;
+    const signed char *A, *B;
+    const float *sa, *sb;  // NULL: all 1
+    float *C;
+    int64_t lda, ldb, ldc;
+    int xcd_shift;
+};
+
+__device__ __forceinline__ double scale_at(const float *s, int64_t i) { return s == nullptr ? 1.0 : (double)s[i]; }
+// (without the product, nothing of the scales: they may be NaN)
+__device__ __forceinline__ float scaled(const Args &a, int sum, double s, float old) {
+    const double v = a.K == 0 ? 0.0 : (double)sum * s;
+    return (float)(a.beta != 0.0f ? fma((double)a.beta, (double)old, v) : v);
+}
+
+__device__ __forceinline__ intx4 load16(rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(intx4, sgk::raw_load_v4f32(r, off, 0, 0));
+}
+// Descriptors are checked by whole 4-byte words: a last word that K fills in part
+// counts as inside (it is aligned, so no page begins in it).
+__device__ __forceinline__ int words(int bytes) { return (bytes + 3) & ~3; }
+// the first `left` of 16 bytes
+__device__ __forceinline__ intx4 first_bytes(intx4 v, int left) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = left - 4 * i;
+        v[i] = n >= 4 ? v[i] : n <= 0 ? 0 : v[i] & (int)((1u << (8 * n)) - 1u);
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of BM x BN, K in tiles of 128 bytes, two LDS stages.  A row of a stage is
+// eight 16-byte chunks, chunk c of row m at c ^ (m / 2) % 8: a load instruction
+// fills eight whole rows, and a fragment read takes one chunk of each of 16
+// consecutive rows; both then touch 16 different 16-byte bank groups.  A wave sums a
+// WM x WN tile with v_mfma_i32_32x32x32_i8.
+// ---------------------------------------------------------------------------
+constexpr int BK = 128;
+
+template <int ROWS, int NT> struct Stage {
+    static constexpr int WAVES = NT / 64;
+    static constexpr int P = ROWS * BK / (NT * 16);
+    static_assert(P * NT * 16 == ROWS * BK, "whole instructions");
+    uint32_t off[P];
+    int col[P];
+
+    __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int row = (p * WAVES + wave) * 8 + lane / 8;
+            col[p] = 16 * (lane % 8 ^ (row / 2) % 8);
+            off[p] = (uint32_t)(row * ld + col[p]);
+        }
+    }
+    __device__ __forceinline__ void load(rsrc_t r, char *lds, int wave, int p, int left) const {
+        typedef __attribute__((address_space(3))) void lds_t;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t *)(lds + (p * WAVES + wave) * 1024), 16,
+                                                 col[p] < left ? off[p] : rowk::kOut, 0, 0, 0);
+    }
+    // the chunk that holds K's last byte also brought what follows it in the row
+    __device__ __forceinline__ void clear(char *lds, int wave, int lane, int left) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int n = left - col[p];
+            if (n > 0 && n < 16) {
+                intx4 *q = reinterpret_cast<intx4 *>(lds + (p * WAVES + wave) * 1024 + 16 * lane);
+                *q = first_bytes(*q, n);
+            }
+        }
+    }
+};
+
+template <int BM, int BN, int WM, int WN, int WPE>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+i8_tile(Args a) {
+    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
+    constexpr int STAGE = (BM + BN) * BK;
+    __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 31, lh = lane >> 5;
+    const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
+    int tm, tn;
+    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
+    const int bm = tm * BM, bn = tn * BN;
+
+    typedef Stage<BM, NT> SA;
+    typedef Stage<BN, NT> SB;
+    SA sa;
+    SB sb;
+    sa.init(a.lda, wave, lane);
+    sb.init(a.ldb, wave, lane);
+    const signed char *A = a.A + (int64_t)bm * a.lda, *B = a.B + (int64_t)bn * a.ldb;
+    const int64_t a_bytes = (int64_t)(a.M - bm - 1) * a.lda + words(a.K);
+    const int64_t b_bytes = (int64_t)(a.N - bn - 1) * a.ldb + words(a.K);
+    const int KT = (a.K + BK - 1) / BK;
+
+    intx16 acc[MI][NI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+    // byte offsets of the lane's rows and of its chunk of k-step s
+    const int a_row = (wm + li) * BK, b_row = BM * BK + (wn + li) * BK;
+    int at[4];  // (wm, wn and 32 i are multiples of 16 rows: one permutation)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) at[s] = 16 * ((2 * s + lh) ^ (li / 2) % 8);
+
+    auto fetch = [&](char *st, int k0, int p) {
+        const int left = a.K - k0;
+        if (p < SA::P)
+            sa.load(whole_rsrc(A + k0, left > 0 ? a_bytes - k0 : 0), st, wave, p, left);
+        else
+            sb.load(whole_rsrc(B + k0, left > 0 ? b_bytes - k0 : 0), st + BM * BK, wave, p - SA::P, left);
+    };
+    constexpr int DP = SA::P + SB::P;
+    auto landed = [&](char *st, int k0) {
+        __builtin_amdgcn_s_waitcnt(0);
+        const int left = a.K - k0;
+        if ((a.K & 15) != 0 && left > 0 && left < BK) sa.clear(st, wave, lane, left);
+        __syncthreads();
+    };
+    auto tile = [&](const char *__restrict__ st, char *__restrict__ nx, int kn) {
+        intx4 av[2][MI], bv[2][NI];
+        auto read = [&](int d, int s) {
+#pragma unroll
+            for (int j = 0; j < NI; ++j) bv[d][j] = *reinterpret_cast<const intx4 *>(st + b_row + j * 32 * BK + at[s]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) av[d][i] = *reinterpret_cast<const intx4 *>(st + a_row + i * 32 * BK + at[s]);
+        };
+        read(0, 0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s < 3) read((s + 1) & 1, s + 1);
+            // the next tile's loads, in pieces behind the MFMAs of the first k-steps
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[s & 1][i], bv[s & 1][j], acc[i][j], 0, 0, 0);
+                    constexpr int U = MI * NI, SPREAD = 2 * U;
+                    const int u = s * U + i * NI + j;
+#pragma unroll
+                    for (int p = 0; p < DP; ++p)
+                        if (u < SPREAD && p * SPREAD / DP == u) fetch(nx, kn, p);
+                }
+        }
+    };
+    if (KT > 0) {
+#pragma unroll
+        for (int p = 0; p < DP; ++p) fetch(smem, 0, p);
+        landed(smem, 0);
+        for (int t = 0; t < KT; ++t) {
+            char *st = smem + (t & 1) * STAGE, *nx = smem + ((t + 1) & 1) * STAGE;
+            tile(st, nx, (t + 1) * BK);
+            landed(nx, (t + 1) * BK);
+        }
+    }
+
+    // acc[i][j] register r on lane (li, lh): row 32 i + 8 (r / 4) + 4 lh + r % 4, column 32 j + li
+    double sb_of[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+        const int n = bn + wn + 32 * j + li;
+        sb_of[j] = a.K > 0 && n < a.N ? (double)a.alpha * scale_at(a.sb, n) : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int m = bm + wm + 32 * i + 8 * (r >> 2) + 4 * lh + (r & 3);
+            if (m >= a.M) continue;
+            const double s = a.K > 0 ? scale_at(a.sa, m) : 0.0;
+            float *c = a.C + (int64_t)m * a.ldc + bn + wn + li;
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                if (bn + wn + 32 * j + li < a.N)
+                    c[32 * j] = scaled(a, acc[i][j][r], s * sb_of[j], a.beta != 0.0f ? c[32 * j] : 0.0f);
+        }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: reading B once is the work, so 16 MB rows and 16 NB channels a
+// workgroup, its WK waves each a share of K, both operands straight from memory to
+// v_mfma_i32_16x16x64_i8, the partial sums added through LDS.  A step is 128 bytes
+// of K: a lane takes 32 of them of its row, so that whole lines are read.
+// ---------------------------------------------------------------------------
+template <int MB, int NB, int WK, int WPE>
+__global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) i8_thin(Args a) {
+    constexpr int BM = 16 * MB, BN = 16 * NB;
+    __shared__ __attribute__((aligned(16))) int part[WK][BM * BN];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lk = lane >> 4;
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
+    int tm, tn;
+    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const signed char *A = a.A + (int64_t)m0 * a.lda, *B = a.B + (int64_t)n0 * a.ldb;
+    const int64_t a_bytes = (int64_t)(a.M - m0 - 1) * a.lda + words(a.K);
+    const int64_t b_bytes = (int64_t)(a.N - n0 - 1) * a.ldb + words(a.K);
+    uint32_t ao[MB], bo[NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) ao[i] = (uint32_t)((16 * i + li) * a.lda + 32 * lk);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) bo[j] = (uint32_t)((16 * j + li) * a.ldb + 32 * lk);
+
+    intx4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = intx4{0, 0, 0, 0};
+
+    const int steps = (a.K + 127) / 128;
+    const int u0 = (int)((int64_t)steps * w / WK), u1 = (int)((int64_t)steps * (w + 1) / WK);
+    constexpr int STEP = 8 * (MB + NB), D = 96 / STEP < 4 ? (96 / STEP < 2 ? 2 : 96 / STEP) : 4;
+    intx4 av[D][2][MB], bv[D][2][NB];
+    auto fetch = [&](int d, int u) {  // (past the wave's last step the descriptors are empty)
+        const int64_t k0 = 128 * (int64_t)u;
+        const rsrc_t ra = whole_rsrc(A + k0, u < u1 ? a_bytes - k0 : 0), rb = whole_rsrc(B + k0, u < u1 ? b_bytes - k0 : 0);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) bv[d][h][j] = load16(rb, bo[j] + 16 * h);
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) av[d][h][i] = load16(ra, ao[i] + 16 * h);
+    };
+    auto multiply = [&](int d) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[d][h][i], bv[d][h][j], acc[i][j], 0, 0, 0);
+    };
+    const int whole = (int64_t)u1 * 128 > a.K ? u1 - 1 : u1;
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, u0 + d);
+    for (int u = u0; u < u1; u += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (u + d == whole) {  // K's end: A's row goes on into what follows it
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+                        av[d][h][i] = first_bytes(av[d][h][i], a.K - 128 * whole - 32 * lk - 16 * h);
+            }
+            if (u + d < u1) multiply(d);
+            if (u + D < u1) fetch(d, u + d + D);
+        }
+    }
+    // acc[i][j] register r on lane (li, lk): row 16 i + 4 lk + r, column 16 j + li
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) part[w][(16 * i + 4 * lk + r) * BN + 16 * j + li] = acc[i][j][r];
+    __syncthreads();
+    for (int f = tid; f < BM * BN; f += WK * 64) {
+        const int m = m0 + f / BN, n = n0 + f % BN;
+        if (m >= a.M || n >= a.N) continue;
+        int sum = part[0][f];
+#pragma unroll
+        for (int i = 1; i < WK; ++i) sum += part[i][f];
+        float *c = a.C + (int64_t)m * a.ldc + n;
+        const double s = a.K > 0 ? (double)a.alpha * scale_at(a.sa, m) * scale_at(a.sb, n) : 0.0;
+        *c = scaled(a, sum, s, a.beta != 0.0f ? *c : 0.0f);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows of any alignment and any leading dimensions: 32 x 32 tiles, bytes one by one.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) i8_simple(Args a) {
+    __shared__ int At[32][17], Bt[32][17];  // 64 bytes of K of each row
+    const int tid = threadIdx.x;
+    const int nbn = (a.N + 31) / 32;
+    const int64_t m0 = (int64_t)(blockIdx.x / nbn) * 32, n0 = (int64_t)(blockIdx.x % nbn) * 32;
+    const int tx = tid & 31, ty = tid >> 5;
+    int acc[4] = {0, 0, 0, 0};
+    for (int64_t k0 = 0; k0 < a.K; k0 += 64) {
+        for (int f = tid; f < 512; f += 256) {
+            const int row = f >> 4, word = f & 15;
+            int av = 0, bv = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int64_t k = k0 + 4 * word + b;
+                if (k >= a.K) continue;
+                if (m0 + row < a.M) av |= (a.A[(m0 + row) * a.lda + k] & 0xff) << (8 * b);
+                if (n0 + row < a.N) bv |= (a.B[(n0 + row) * a.ldb + k] & 0xff) << (8 * b);
+            }
+            At[row][word] = av;
+            Bt[row][word] = bv;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int word = 0; word < 16; ++word) {
+            const int b = Bt[tx][word];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_sdot4(At[ty + 8 * i][word], b, acc[i], false);
+        }
+        __syncthreads();
+    }
+    if (n0 + tx >= a.N) return;
+    const double sb = a.K > 0 ? (double)a.alpha * scale_at(a.sb, n0 + tx) : 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + ty + 8 * i;
+        if (m >= a.M) continue;
+        float *c = a.C + m * a.ldc + n0 + tx;
+        *c = scaled(a, acc[i], a.K > 0 ? sb * scale_at(a.sa, m) : 0.0, a.beta != 0.0f ? *c : 0.0f);
+    }
+}
+
+}  // namespace i8k

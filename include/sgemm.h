@@ -542,6 +542,103 @@ int sgemm_adapters_grad(int M, int N, int K, float alpha, const float *A, int ld
                         size_t workspace_bytes, hipStream_t stream);
 size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank);
 
+/* ==== a gated feed-forward block ==============================================
+ * What stands around a block's products: the norm with the residual's addition,
+ * the gated projections, and the same block in 8 bits.  In FP32, for training,
+ *
+ *   sgemm_norm         h = x + residual, y = its norm
+ *   sgemm_gated        act(y G) (y U), both projections in one kernel
+ *   sgemm              the projection back down
+ *
+ * and back sgemm_gated_grad and sgemm_norm_grad.  In 8 bits, for serving,
+ *
+ *   sgemm_norm         to 8 bits with a scale per row
+ *   sgemm_i8           gate and up: one product of 2 F channels
+ *   sgemm_quantize     act(gate) up to 8 bits
+ *   sgemm_i8           back down, beta = 1 onto the residual stream
+ *
+ * with the weights' channels quantized once by sgemm_quantize.  All asynchronous
+ * on `stream`, with caller-owned device pointers, no allocation and results that
+ * are the same run to run.
+ *
+ * 8-bit rows.  A row v has the scale s = max |v| / 127 and the whole numbers
+ * q = v (127 / max |v|), to the nearest, halves to the even one: q s stands for
+ * v.  Both are computed in 64 bits from v, which is rounded to 32 (s is rounded
+ * once more).  A row of zeros has s = 0; one that holds a NaN or an infinity has
+ * s = NaN and q = 0, so that products of it are NaN.  Pointers to 8-bit numbers
+ * need no alignment.
+ *
+ * Return value.  0; SGEMM_ERR_WORKSPACE; SGEMM_ERR_TOO_LARGE (a grid beyond one
+ * launch; a size within 16384 of 2^31; K of sgemm_i8 above SGEMM_I8_MAX_K); a
+ * positive hipError_t; or -(100 + position) for an invalid argument, as above.
+ * Checks run before any HIP call, the first bad argument wins, and a leading
+ * dimension is checked whether or not its matrix is given; pointers to floats
+ * have to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed. */
+#define SGEMM_ACT_SILU 0      /* g / (1 + exp(-g)) */
+#define SGEMM_ACT_GELU 1      /* g (1 + erf(g / sqrt(2))) / 2 */
+#define SGEMM_ACT_GELU_TANH 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+#define SGEMM_I8_MAX_K 131071 /* products of -128 by -128 that 32 bits hold */
+
+/* Root-mean-square norm of T rows of N columns:
+ *   h = x + residual (NULL: x), rounded to 32 bits,
+ *   y = h (mean(h^2) + eps)^-1/2 weight (NULL: 1), in 64 bits, rounded once,
+ *   q, scales = y in 8 bits (q: T rows of N, scales: T floats).
+ * sum takes h; sum, y and q may each be NULL (not wanted), scales may where q is.
+ * sum may be x or residual itself (same pointer and leading dimension), y may be
+ * x, residual or sum.  eps >= 0; with eps 0 a row of zeros is NaN. */
+int sgemm_norm(int T, int N, const float *x, int ldx, const float *residual, int ldr, const float *weight, float eps,
+               float *sum, int lds, float *y, int ldy, signed char *q, int ldq, float *scales, hipStream_t stream);
+
+/* Back through sgemm_norm() from dy, the gradient of y, and dsum, what reaches h
+ * by another way (NULL: nothing).  With r = (mean(h^2) + eps)^-1/2:
+ *   dh = r (weight dy - h r^2 mean(weight dy h)) + dsum,
+ *   dweight = sum over the rows of dy h r, + beta * dweight,
+ * h as sgemm_norm() summed it.  dh (the gradient of x and of residual alike) or
+ * dweight may be NULL (not wanted); dh may be dy or dsum itself.  beta == 0 does
+ * not read dweight.  Workspace, where dweight is wanted: at least
+ * sgemm_norm_grad_workspace_size() bytes, 256-byte aligned, any contents; calls
+ * that share one must not overlap in time. */
+int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, float eps, const float *dy, int lddy,
+                    const float *dsum, int ldds, float *dh, int lddh, float beta, float *dweight, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+size_t sgemm_norm_grad_workspace_size(int T, int N);
+
+/* T rows of N columns to 8 bits: x, or with a gate act(gate) * x (`activation`,
+ * SGEMM_ACT_*, in 64 bits, rounded once to 32).  gate NULL: none. */
+int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const float *gate, int ldg, signed char *q,
+                   int ldq, float *scales, hipStream_t stream);
+
+/* The product of 8-bit rows A (M x K) with 8-bit channels B (N x K, a channel's K
+ * numbers side by side):
+ *   C[m][n] = alpha * a_scales[m] * b_scales[n] * sum_k A[m][k] B[n][k] + beta * C[m][n],
+ * the sum exact, the rest in 64 bits and rounded once.  Scales NULL: all 1.
+ * beta == 0 does not read C; alpha == 0 or K == 0 read neither A, B nor the scales
+ * (C = beta * C).  A and B 4-byte aligned with leading dimensions that are
+ * multiples of 4 below 2^23 take the fast kernels; others are slow. */
+int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, const float *a_scales,
+             const signed char *B, int ldb, const float *b_scales, float beta, float *C, int ldc, hipStream_t stream);
+
+/* Both projections of a gated block, the activation and the product:
+ *   gate = x G,  up = x U,  y = act(gate) * up,
+ * x (T x K), G and U (K x N), y (T x N).  gate and up (T x N) are written where
+ * they are wanted, for the gradient (both NULL: neither).  No output overlaps an
+ * input or another output. */
+int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg, const float *U,
+                int ldu, float *y, int ldy, float *gate, int ldgate, float *up, int ldup, hipStream_t stream);
+
+/* Back through sgemm_gated() from dy (T x N), with the gate and up it wrote.  With
+ * dgate = dy * up * act'(gate) and dup = dy * act(gate):
+ *   dx = dgate G^T + dup U^T,
+ *   dG = x^T dgate + beta * dG,  dU = x^T dup + beta * dU.
+ * dx, or dG and dU together, may be NULL (not wanted).  beta == 0 reads neither dG
+ * nor dU.  Workspace: at least sgemm_gated_grad_workspace_size() bytes, 256-byte
+ * aligned, any contents; calls that share one must not overlap in time. */
+int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg,
+                     const float *U, int ldu, const float *gate, int ldgate, const float *up, int ldup,
+                     const float *dy, int lddy, float *dx, int lddx, float beta, float *dG, int lddg, float *dU,
+                     int lddu, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t sgemm_gated_grad_workspace_size(int T, int N, int K);
+
 #ifdef __cplusplus
 }
 #endif
