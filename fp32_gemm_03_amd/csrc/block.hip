@@ -88,11 +88,13 @@ struct I8Kernel {
     int bm, bn, threads;
     void (*fn)(i8k::Args);
 };
-#define I8_TILE(BM, BN, WM, WN, WPE) {BM, BN, (BM / WM) * (BN / WN) * 64, i8k::i8_tile<BM, BN, WM, WN, WPE>}
+#define I8_TILE(BM, BN, BK, WM, WN, STG, AHEAD, WPE) \
+    {BM, BN, (BM / WM) * (BN / WN) * 64, i8k::i8_tile<BM, BN, BK, WM, WN, STG, AHEAD, WPE>}
 #define I8_THIN(MB, NB, WK, WPE) {16 * MB, 16 * NB, WK * 64, i8k::i8_thin<MB, NB, WK, WPE>}
-const I8Kernel kI8Large = I8_TILE(256, 256, 128, 64, 2);
-const I8Kernel kI8Mid = I8_TILE(128, 128, 64, 64, 1);
-const I8Kernel kI8Small = I8_TILE(64, 64, 32, 32, 2);
+const I8Kernel kI8Large = I8_TILE(256, 256, 128, 64, 64, 2, 1, 4);  // 16 waves, one workgroup per CU
+const I8Kernel kI8Mid = I8_TILE(128, 128, 128, 32, 64, 2, 1, 4);    // 8 waves, two per CU
+const I8Kernel kI8Lone = I8_TILE(128, 128, 256, 32, 64, 2, 1, 2);   // 8 waves, one per CU
+const I8Kernel kI8Small = I8_TILE(64, 64, 256, 32, 32, 2, 3, 2);    // 4 waves, two per CU
 const I8Kernel kI8Thin1 = I8_THIN(1, 1, 8, 4);
 const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 4);
 const I8Kernel kI8Thin4 = I8_THIN(4, 1, 8, 2);
@@ -100,18 +102,32 @@ const I8Kernel kI8Simple = {32, 32, 256, i8k::i8_simple};
 
 long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ceil_div(N, k.bn); }
 
+// Measured (us, N = K = 4096, A from memory; thin: 16, 32 and 64 rows):
+//   rows           1    8   37*  64  100  200  1024  2048  4096      (* 4096 x 2048)
+//   thin          5.2  5.7  6.1 12.0 18.4 33.4   145
+//   64 x 64      12.5 12.5  8.0 12.6 12.7 16.3  33.3  64.5   127
+//   128 x 128    21.5 21.4 13.2 21.6 21.6 28.9  31.8  40.9    80
+//     256 of K   18.4 18.2 11.6 18.3 18.2 22.4  25.9  53.1   104
+//   256 x 256    46.3 46.2 28.6 46.3 46.6 50.6  51.7  54.0    73
+// So up to 64 rows thin; then by rounds of tiles (256 CUs; 64 x 64: two on each), each
+// priced by what a full one took: 64 x 64 10, 128 x 128 16 alone on its CU and 12.4
+// among others, 256 x 256 41.
 const I8Kernel &choose_i8(const i8k::Args &a) {
     // the fast kernels load 16 bytes at 4-byte alignment, at 32-bit offsets from a tile's
     // first row
     const bool words = ((uintptr_t)a.A & 3) == 0 && ((uintptr_t)a.B & 3) == 0 && a.lda % 4 == 0 && a.ldb % 4 == 0;
     constexpr int64_t reach = (1LL << 31) / 256 - 1024;
-    if (!words || a.lda > reach || a.ldb > reach) return kI8Simple;
+    if (!words || a.lda > reach || a.ldb > reach || a.ldc > reach / 4) return kI8Simple;
     if (a.M <= 16) return kI8Thin1;
     if (a.M <= 32) return kI8Thin2;
     if (a.M <= 64) return kI8Thin4;
-    if (tiles(kI8Large, a.M, a.N) >= 256) return kI8Large;
-    if (tiles(kI8Mid, a.M, a.N) >= 200) return kI8Mid;
-    return kI8Small;
+    const long long mid = tiles(kI8Mid, a.M, a.N);
+    const double small = 10.0 * ceil_div(tiles(kI8Small, a.M, a.N), 512);
+    const double middle = mid <= 256 ? 16.0 : 12.4 * ceil_div(mid, 256);
+    const double large = 41.0 * ceil_div(tiles(kI8Large, a.M, a.N), 256);
+    if (small <= middle && small <= large) return kI8Small;
+    if (middle <= large) return mid <= 256 ? kI8Lone : kI8Mid;
+    return kI8Large;
 }
 
 // ---- gated projections -----------------------------------------------------------

@@ -56,16 +56,14 @@ __device__ __forceinline__ intx4 first_bytes(intx4 v, int left) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles of BM x BN, K in tiles of 128 bytes, two LDS stages.  A row of a stage is
-// eight 16-byte chunks, chunk c of row m at c ^ (m / 2) % 8: a load instruction
-// fills eight whole rows, and a fragment read takes one chunk of each of 16
-// consecutive rows; both then touch 16 different 16-byte bank groups.  A wave sums a
-// WM x WN tile with v_mfma_i32_32x32x32_i8.
+// Tiles of BM x BN, K in tiles of BK bytes, a ring of STG LDS stages; the barrier that
+// ends a K tile waits for the next one only.  A row of a stage is BK / 16 chunks of 16 bytes, permuted
+// (AKLayout) so that a load instruction (whole rows) and a fragment read (one chunk
+// of each of 16 consecutive rows) both touch every bank.  A wave sums a WM x WN tile
+// with v_mfma_i32_32x32x32_i8; lane half lh takes chunks lh BK / 32 + s.
 // ---------------------------------------------------------------------------
-constexpr int BK = 128;
-
-template <int ROWS, int NT> struct Stage {
-    static constexpr int WAVES = NT / 64;
+template <int ROWS, int BK, int NT> struct Stage {
+    static constexpr int WAVES = NT / 64, CPR = BK / 16;
     static constexpr int P = ROWS * BK / (NT * 16);
     static_assert(P * NT * 16 == ROWS * BK, "whole instructions");
     uint32_t off[P];
@@ -74,8 +72,8 @@ template <int ROWS, int NT> struct Stage {
     __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int row = (p * WAVES + wave) * 8 + lane / 8;
-            col[p] = 16 * (lane % 8 ^ (row / 2) % 8);
+            const int chunk = (p * WAVES + wave) * 64 + lane, row = chunk / CPR;
+            col[p] = 16 * sgk::AKLayout<BK / 4>::chunk_pos(row, chunk % CPR);
             off[p] = (uint32_t)(row * ld + col[p]);
         }
     }
@@ -97,12 +95,28 @@ template <int ROWS, int NT> struct Stage {
     }
 };
 
-template <int BM, int BN, int WM, int WN, int WPE>
+// Waits until this wave's loads but the newest N have landed and its LDS accesses have
+// completed (gfx9 encoding: vmcnt in bits 3:0 and 15:14, lgkmcnt 0, expcnt any).
+template <int N> __device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N <= 63, "vmcnt is 6 bits");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int BM, int BN, int BK, int WM, int WN, int STG, int AHEAD, int WPE>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
 i8_tile(Args a) {
     constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
-    constexpr int STAGE = (BM + BN) * BK;
-    __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+    constexpr int STAGE = (BM + BN) * BK, STEPS = BK / 32;
+    __shared__ __attribute__((aligned(16))) char smem[STG * STAGE];
+    __shared__ __attribute__((aligned(16))) float scale[BM + BN];  // alpha's product comes later
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 31, lh = lane >> 5;
     const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
@@ -111,8 +125,8 @@ i8_tile(Args a) {
     sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
     const int bm = tm * BM, bn = tn * BN;
 
-    typedef Stage<BM, NT> SA;
-    typedef Stage<BN, NT> SB;
+    typedef Stage<BM, BK, NT> SA;
+    typedef Stage<BN, BK, NT> SB;
     SA sa;
     SB sb;
     sa.init(a.lda, wave, lane);
@@ -132,80 +146,119 @@ i8_tile(Args a) {
 
     // byte offsets of the lane's rows and of its chunk of k-step s
     const int a_row = (wm + li) * BK, b_row = BM * BK + (wn + li) * BK;
-    int at[4];  // (wm, wn and 32 i are multiples of 16 rows: one permutation)
+    int at[STEPS];  // (wm, wn and 32 i are multiples of 16 rows: one permutation)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) at[s] = 16 * ((2 * s + lh) ^ (li / 2) % 8);
+    for (int s = 0; s < STEPS; ++s) at[s] = 16 * sgk::AKLayout<BK / 4>::chunk_pos(li, lh * STEPS + s);
 
-    auto fetch = [&](char *st, int k0, int p) {
-        const int left = a.K - k0;
-        if (p < SA::P)
-            sa.load(whole_rsrc(A + k0, left > 0 ? a_bytes - k0 : 0), st, wave, p, left);
-        else
-            sb.load(whole_rsrc(B + k0, left > 0 ? b_bytes - k0 : 0), st + BM * BK, wave, p - SA::P, left);
-    };
     constexpr int DP = SA::P + SB::P;
-    auto landed = [&](char *st, int k0) {
-        __builtin_amdgcn_s_waitcnt(0);
+    auto fetch = [&](char *st, int k0) {  // (past K nothing is read)
         const int left = a.K - k0;
-        if ((a.K & 15) != 0 && left > 0 && left < BK) sa.clear(st, wave, lane, left);
-        __syncthreads();
+        const rsrc_t ra = whole_rsrc(A + k0, left > 0 ? a_bytes - k0 : 0);
+        const rsrc_t rb = whole_rsrc(B + k0, left > 0 ? b_bytes - k0 : 0);
+#pragma unroll
+        for (int p = 0; p < SA::P; ++p) sa.load(ra, st, wave, p, left);
+#pragma unroll
+        for (int p = 0; p < SB::P; ++p) sb.load(rb, st + BM * BK, wave, p, left);
     };
-    auto tile = [&](const char *__restrict__ st, char *__restrict__ nx, int kn) {
-        intx4 av[2][MI], bv[2][NI];
-        auto read = [&](int d, int s) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j) bv[d][j] = *reinterpret_cast<const intx4 *>(st + b_row + j * 32 * BK + at[s]);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) av[d][i] = *reinterpret_cast<const intx4 *>(st + a_row + i * 32 * BK + at[s]);
-        };
-        read(0, 0);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s < 3) read((s + 1) & 1, s + 1);
-            // the next tile's loads, in pieces behind the MFMAs of the first k-steps
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[s & 1][i], bv[s & 1][j], acc[i][j], 0, 0, 0);
-                    constexpr int U = MI * NI, SPREAD = 2 * U;
-                    const int u = s * U + i * NI + j;
-#pragma unroll
-                    for (int p = 0; p < DP; ++p)
-                        if (u < SPREAD && p * SPREAD / DP == u) fetch(nx, kn, p);
-                }
+    auto landed = [&](char *st, int k0) {
+        const int left = a.K - k0;
+        if ((a.K & 15) != 0 && left > 0 && left < BK) {
+            sa.clear(st, wave, lane, left);
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0
         }
+        meet();
+    };
+    constexpr int SETS = AHEAD + 1;  // of fragments: one multiplied, AHEAD being read
+    static_assert(STEPS % SETS == 0, "a tile begins with the first set");
+    intx4 av[SETS][MI], bv[SETS][NI];
+    auto read = [&](const char *__restrict__ st, int s) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            bv[s % SETS][j] = *reinterpret_cast<const intx4 *>(st + b_row + j * 32 * BK + at[s]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            av[s % SETS][i] = *reinterpret_cast<const intx4 *>(st + a_row + i * 32 * BK + at[s]);
+    };
+    auto multiply = [&](int s) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[s % SETS][i], bv[s % SETS][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     };
     if (KT > 0) {
-#pragma unroll
-        for (int p = 0; p < DP; ++p) fetch(smem, 0, p);
-        landed(smem, 0);
-        for (int t = 0; t < KT; ++t) {
-            char *st = smem + (t & 1) * STAGE, *nx = smem + ((t + 1) & 1) * STAGE;
-            tile(st, nx, (t + 1) * BK);
-            landed(nx, (t + 1) * BK);
+        for (int f = tid; f < BM + BN; f += NT) {
+            const float *from = f < BM ? a.sa : a.sb;
+            const int row = f < BM ? bm + f : bn + f - BM, end = f < BM ? a.M : a.N;
+            scale[f] = from != nullptr && row < end ? from[row] : 1.0f;
         }
+        // Fragments are read AHEAD k-steps before their MFMAs, across the tiles' borders:
+        // the last AHEAD steps of a tile are multiplied behind the barrier that ends its
+        // reads, while the stage that it was read from is filled with tile t + STG.
+#pragma unroll
+        for (int s = 0; s < STG; ++s) fetch(smem + s * STAGE, s * BK);
+        wait_loads<(STG - 1) * DP>();
+        landed(smem, 0);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) read(smem, s);
+        int cur = 0;  // stage of tile t
+        for (int t = 0; t < KT; ++t) {
+            char *st = smem + cur * STAGE;
+            cur = cur + 1 == STG ? 0 : cur + 1;
+            char *next = smem + cur * STAGE;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (s + AHEAD == STEPS) {
+                    wait_loads<(STG - 2) * DP>();
+                    landed(next, (t + 1) * BK);
+                }
+                if (s + AHEAD < STEPS) read(st, s + AHEAD);
+                else read(next, s + AHEAD - STEPS);
+                if (s + AHEAD == STEPS) fetch(st, (t + STG) * BK);
+                multiply(s);
+            }
+        }
+        wait_loads<0>();
     }
 
-    // acc[i][j] register r on lane (li, lh): row 32 i + 8 (r / 4) + 4 lh + r % 4, column 32 j + li
+    // acc[i][j] register r on lane (li, lh): row 32 i + 8 (r / 4) + 4 lh + r % 4, column
+    // 32 j + li.  C through a descriptor from the tile's first element to the last one:
+    // rows beyond it are cut off there, columns get an offset outside.
+    const rsrc_t rc = whole_rsrc(a.C + (int64_t)bm * a.ldc + bn, ((int64_t)(a.M - bm - 1) * a.ldc + (a.N - bn)) * 4);
+    const uint32_t ldc4 = (uint32_t)a.ldc * 4u;
     double sb_of[NI];
+    uint32_t col[NI];
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
-        const int n = bn + wn + 32 * j + li;
-        sb_of[j] = a.K > 0 && n < a.N ? (double)a.alpha * scale_at(a.sb, n) : 0.0;
+        const int n = wn + 32 * j + li;
+        sb_of[j] = KT > 0 ? (double)a.alpha * (double)scale[BM + n] : 0.0;
+        col[j] = bn + n < a.N ? 4u * (uint32_t)n : rowk::kOut;
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int m = bm + wm + 32 * i + 8 * (r >> 2) + 4 * lh + (r & 3);
-            if (m >= a.M) continue;
-            const double s = a.K > 0 ? scale_at(a.sa, m) : 0.0;
-            float *c = a.C + (int64_t)m * a.ldc + bn + wn + li;
+        for (int q = 0; q < 4; ++q) {
+            const int row = wm + 32 * i + 8 * q + 4 * lh;
+            const float4 s = KT > 0 ? *reinterpret_cast<const float4 *>(&scale[row]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float old[4][NI];
+            uint32_t off[4][NI];
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
-                if (bn + wn + 32 * j + li < a.N)
-                    c[32 * j] = scaled(a, acc[i][j][r], s * sb_of[j], a.beta != 0.0f ? c[32 * j] : 0.0f);
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    off[r][j] = col[j] == rowk::kOut ? rowk::kOut : (uint32_t)(row + r) * ldc4 + col[j];
+                    old[r][j] = a.beta != 0.0f ? sgk::raw_load_f32(rc, off[r][j], 0, 0) : 0.0f;
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const double sr = r == 0 ? s.x : r == 1 ? s.y : r == 2 ? s.z : s.w;
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+                    sgk::raw_store_f32(scaled(a, acc[i][j][4 * q + r], sr * sb_of[j], old[r][j]), rc, off[r][j], 0,
+                                       sgk::kCPolStream);
+            }
         }
 }
 

@@ -46,10 +46,12 @@ struct MaxInt {
 // maximum tells whether it holds either.
 __device__ __forceinline__ int magnitude(float v) { return __float_as_int(v) & 0x7fffffff; }
 
-// 8-bit rows: scale a / 127 and q = nearest even of v (127 / a).  A row of zeros has
-// scale 0; one that holds a NaN or an infinity scale NaN and whole numbers 0.
+// 8-bit rows: scale a / 127 and q = nearest even of v (127 (1 / a)), each operation
+// rounded to 64 bits (half of a is 63.5 steps give or take a rounding, so the order is
+// part of the definition).  A row of zeros has scale 0; one that holds a NaN or an
+// infinity scale NaN and whole numbers 0.
 __device__ __forceinline__ double steps_per(int most) {
-    return most > 0 && most < 0x7f800000 ? 127.0 / (double)__int_as_float(most) : 0.0;
+    return most > 0 && most < 0x7f800000 ? 127.0 * (1.0 / (double)__int_as_float(most)) : 0.0;
 }
 __device__ __forceinline__ float scale_of(int most) {
     return most < 0x7f800000 ? (float)((double)__int_as_float(most) / 127.0) : __int_as_float(0x7fc00000);

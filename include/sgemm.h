@@ -562,9 +562,9 @@ size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank);
  * are the same run to run.
  *
  * 8-bit rows.  A row v has the scale s = max |v| / 127 and the whole numbers
- * q = v (127 / max |v|), to the nearest, halves to the even one: q s stands for
- * v.  Both are computed in 64 bits from v, which is rounded to 32 (s is rounded
- * once more).  A row of zeros has s = 0; one that holds a NaN or an infinity has
+ * q = v (127 (1 / max |v|)), to the nearest, halves to the even one: q s stands for
+ * v.  Both are computed in 64 bits, each operation rounded, from v, which is rounded
+ * to 32 (and s is rounded to 32 last).  A row of zeros has s = 0; one that holds a NaN or an infinity has
  * s = NaN and q = 0, so that products of it are NaN.  Pointers to 8-bit numbers
  * need no alignment.
  *

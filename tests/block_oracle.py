@@ -59,7 +59,7 @@ def quantize(v):
     most = bits.max(1, initial=0).astype(np.uint32)
     finite = most < 0x7f800000
     top = np.where(finite, most, 0).astype(np.uint32).view(F32).astype(F64)
-    per = np.divide(127.0, top, out=np.zeros_like(top), where=top > 0)
+    per = 127.0 * np.divide(1.0, top, out=np.zeros_like(top), where=top > 0)
     q = np.where(finite[:, None], np.rint(np.where(finite[:, None], v, 0).astype(F64) * per[:, None]), 0)
     return q.astype(np.int8), np.where(finite, top / 127.0, np.nan).astype(F32)
 
