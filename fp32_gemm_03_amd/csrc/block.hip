@@ -55,33 +55,44 @@ template <class A, int N> const RowKernel<A> *row_kernel(const RowKernel<A> (&ta
     return nullptr;
 }
 template <class A> int launch_rows(const RowKernel<A> &k, int T, const A &a, hipStream_t stream) {
-    const int rows = k.threads < 256 ? 256 / k.threads : 1;
+    const int rows = k.threads == 64 ? 4 : 1;
     return enqueue(k.fn, ceil_div(T, rows), k.threads * rows, a, stream);
 }
 
 #define ROW(fn, NT, V, ...) {NT, 4 * NT * V, fn<NT, V, ##__VA_ARGS__>}
+// Threads x vectors by columns.  Measured (us, rows x columns; threads x vectors):
+//   norm to 8 bits: 4000 x 512 7.4 on 64 x 2, 8.6 on 128 x 2, 9.6 on 256 x 1; 515 x 1024 3.5
+//   on 128 x 2, 3.6 on 64 x 4, 4.0 on 256 x 2; 2011 x 2048 11.2 on 256 x 2, 12.0 on 64 x 8,
+//   12.3 on 512 x 1; 4095 x 4096 39.1 on 512 x 2, 39.6 on 256 x 4, 46.5 on 64 x 16, 41.7 on
+//   1024 x 1; one row of 4096 3.3, 3.5, 6.0 and 3.7.
+//   The gradient goes the same way (2011 x 2048 12.6 on 256 x 2, 13.3 on 128 x 4, 15.7 on 64 x 8).
 const RowKernel<normk::NormArgs> kNorms[] = {
-    ROW(normk::norm, 64, 1), ROW(normk::norm, 64, 2), ROW(normk::norm, 64, 4), ROW(normk::norm, 256, 2),
-    ROW(normk::norm, 256, 4), ROW(normk::norm, 512, 4), ROW(normk::norm, 1024, 4)};
+    ROW(normk::norm, 64, 1), ROW(normk::norm, 64, 2), ROW(normk::norm, 128, 2), ROW(normk::norm, 256, 2),
+    ROW(normk::norm, 512, 2), ROW(normk::norm, 512, 4), ROW(normk::norm, 1024, 4)};
 #define QUANTIZE(ACT)                                                                                          \
-    {ROW(normk::quantize, 64, 1, ACT), ROW(normk::quantize, 64, 2, ACT), ROW(normk::quantize, 64, 4, ACT),    \
-     ROW(normk::quantize, 256, 2, ACT), ROW(normk::quantize, 256, 4, ACT), ROW(normk::quantize, 512, 4, ACT), \
+    {ROW(normk::quantize, 64, 1, ACT), ROW(normk::quantize, 64, 2, ACT), ROW(normk::quantize, 256, 1, ACT),   \
+     ROW(normk::quantize, 256, 2, ACT), ROW(normk::quantize, 512, 2, ACT), ROW(normk::quantize, 512, 4, ACT), \
      ROW(normk::quantize, 1024, 4, ACT)}
 const RowKernel<normk::QuantArgs> kQuants[4][7] = {QUANTIZE(0), QUANTIZE(1), QUANTIZE(2), QUANTIZE(-1)};
 void (*const kLongQuants[4])(normk::QuantArgs) = {normk::quantize_long<0>, normk::quantize_long<1>,
                                                   normk::quantize_long<2>, normk::quantize_long<-1>};
 const RowKernel<normk::NormGradArgs> kNormGrads[] = {
-    ROW(normk::norm_grad, 64, 1), ROW(normk::norm_grad, 64, 2), ROW(normk::norm_grad, 256, 1),
-    ROW(normk::norm_grad, 256, 2), ROW(normk::norm_grad, 256, 4), ROW(normk::norm_grad, 512, 4)};
+    ROW(normk::norm_grad, 64, 1), ROW(normk::norm_grad, 64, 2), ROW(normk::norm_grad, 128, 2),
+    ROW(normk::norm_grad, 256, 2), ROW(normk::norm_grad, 512, 2), ROW(normk::norm_grad, 512, 4)};
 
-// Shares that dweight is summed in: a workgroup each.
-int weight_shares(int T) { return T < 512 ? T : 512; }
+// Shares that dweight is summed in, a workgroup each.  Measured (us, gradient + sum of the
+// shares): 2011 x 2048 12.6 + 3.8 with 512, 14.5 + 3.3 with 256, 13.0 + 4.7 with 1024; on one
+// wave a row, 4000 x 512, 9.0 + 4.6 with 1024, 12.0 + 3.7 with 512, 8.8 + 6.6 with 2048.
+int weight_shares(int T, int N) {
+    const int most = N <= 512 ? 1024 : 512;
+    return T < most ? T : most;
+}
 
 bool workspace_ok(const void *p, size_t have, size_t need) {
     return need == 0 || (p != nullptr && have >= need && ((uintptr_t)p & 255u) == 0);
 }
 
-size_t norm_grad_bytes(int T, int N) { return round_up((size_t)weight_shares(T) * N * 4); }
+size_t norm_grad_bytes(int T, int N) { return round_up((size_t)weight_shares(T, N) * N * 4); }
 
 // ---- 8-bit products ------------------------------------------------------------
 struct I8Kernel {
@@ -260,12 +271,13 @@ int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, 
     a.part = dweight == nullptr ? nullptr : static_cast<float *>(workspace);
     a.dweight = dweight;
     a.beta = beta;
-    a.P = weight_shares(T);
+    a.P = weight_shares(T, N);
     const RowKernel<normk::NormGradArgs> *k = row_kernel(kNormGrads, N);
     const int rc = k == nullptr ? enqueue(normk::norm_grad_long, a.P, normk::kLongThreads, a, stream)
                                 : enqueue(k->fn, a.P, k->threads, a, stream);
     if (rc != SGEMM_OK || dweight == nullptr) return rc;
-    return enqueue(normk::norm_weight_grad, ceil_div(N, 64), 64 * normk::kShareWaves, a, stream);
+    return enqueue(normk::norm_weight_grad, ceil_div(N, normk::kShareColumns), normk::kShareColumns * normk::kShareGroups,
+                   a, stream);
 }
 
 int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const float *gate, int ldg, signed char *q,

@@ -94,7 +94,7 @@ __device__ __forceinline__ void put4(float *row, int i, int N, f32x4u v) {
 
 // ---------------------------------------------------------------------------
 // h = x + residual; y = h (mean h^2 + eps)^-1/2 weight; y to 8 bits.
-// NT threads hold a row of up to 4 NT V columns; 256 threads take 256 / NT rows.
+// NT threads hold a row of up to 4 NT V columns; of rows of one wave a workgroup takes four.
 // ---------------------------------------------------------------------------
 struct NormArgs {
     int T, N;
@@ -111,8 +111,8 @@ __device__ __forceinline__ float normed(float h, double r, float w, bool weighte
     return (float)(weighted ? v * (double)w : v);
 }
 
-template <int NT, int V> __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm(NormArgs a) {
-    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+template <int NT, int V> __global__ void __launch_bounds__(NT == 64 ? 256 : NT) norm(NormArgs a) {
+    constexpr int ROWS = NT == 64 ? 4 : 1;  // a wave each, or one of the workgroup
     __shared__ double sums[NT / 64 > 0 ? NT / 64 : 1];
     __shared__ int mosts[NT / 64 > 0 ? NT / 64 : 1];
     const int tid = threadIdx.x % NT;
@@ -288,8 +288,8 @@ template <int ACT> __device__ __forceinline__ f32x4u gated64(f32x4u g, f32x4u x)
 }
 
 // ACT < 0: no gate
-template <int NT, int V, int ACT> __global__ void __launch_bounds__(NT < 256 ? 256 : NT) quantize(QuantArgs a) {
-    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+template <int NT, int V, int ACT> __global__ void __launch_bounds__(NT == 64 ? 256 : NT) quantize(QuantArgs a) {
+    constexpr int ROWS = NT == 64 ? 4 : 1;  // a wave each, or one of the workgroup
     __shared__ int mosts[NT / 64 > 0 ? NT / 64 : 1];
     const int tid = threadIdx.x % NT;
     const int64_t t = __builtin_amdgcn_readfirstlane((int)blockIdx.x * ROWS + (int)threadIdx.x / NT);
@@ -461,21 +461,31 @@ __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
     }
 }
 
-// dweight = beta dweight + the sum of the P shares: 64 columns a workgroup, its
-// waves take every 16th share, added up in order.
-constexpr int kShareWaves = 16;
-__global__ void __launch_bounds__(64 * kShareWaves) norm_weight_grad(NormGradArgs a) {
-    __shared__ double sums[kShareWaves][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+// dweight = beta dweight + the sum of the P shares.  16 columns a workgroup (a line of
+// each share), its 64 groups of 16 lanes take every 64th share, eight loads in flight;
+// added up in order.
+constexpr int kShareColumns = 16, kShareGroups = 64;
+__global__ void __launch_bounds__(kShareColumns * kShareGroups) norm_weight_grad(NormGradArgs a) {
+    __shared__ double sums[kShareGroups][kShareColumns];
+    const int col = threadIdx.x % kShareColumns, group = threadIdx.x / kShareColumns;
+    const int64_t n = (int64_t)blockIdx.x * kShareColumns + col;
     double s = 0.0;
-    if (n < a.N)
-        for (int p = w; p < a.P; p += kShareWaves) s += (double)a.part[(int64_t)p * a.N + n];
-    sums[w][lane] = s;
-    __syncthreads();
-    if (w != 0 || n >= a.N) return;
+    if (n < a.N) {
+        const float *from = a.part + n;
+        for (int p = group; p < a.P; p += 8 * kShareGroups) {
+            float v[8];
 #pragma unroll
-    for (int i = 1; i < kShareWaves; ++i) s += sums[i][lane];
+            for (int i = 0; i < 8; ++i)
+                v[i] = p + i * kShareGroups < a.P ? from[(int64_t)(p + i * kShareGroups) * a.N] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += (double)v[i];
+        }
+    }
+    sums[group][col] = s;
+    __syncthreads();
+    if (group != 0 || n >= a.N) return;
+#pragma unroll 8
+    for (int i = 1; i < kShareGroups; ++i) s += sums[i][col];
     a.dweight[n] = (float)(a.beta != 0.0f ? fma((double)a.beta, (double)a.dweight[n], s) : s);
 }
 
