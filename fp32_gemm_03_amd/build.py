@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "rows.hip"), os.path.join(CSRC, "block.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, name) for name in (
-    "sgemm_kernels.hpp", "lanes.hpp", "rows_kernels.hpp", "grouped_kernels.hpp", "activations.hpp",
+    "sgemm_kernels.hpp", "lanes.hpp", "rows_api.hpp", "rows_kernels.hpp", "grouped_kernels.hpp", "activations.hpp",
     "norm_kernels.hpp", "i8_kernels.hpp", "gated_kernels.hpp")] + [os.path.join(INCLUDE, "sgemm.h")]
 LIBRARY = os.path.join(PKG, "libsgemm_mi355x.so")
 ARCH = "gfx950"

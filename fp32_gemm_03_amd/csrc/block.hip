@@ -10,6 +10,7 @@
 #include "gated_kernels.hpp"
 #include "i8_kernels.hpp"
 #include "norm_kernels.hpp"
+#include "rows_api.hpp"
 
 namespace {
 
@@ -151,19 +152,53 @@ struct GatedKernel {
 #define BACK_TILE(KIND, BM, BN, BK, WM, WN, WPE) \
     {BM, BN, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::KIND, BM, BN, BK, WM, WN, WPE>}
 #define GATED_THIN(MB, VW, WK, WPE) {16 * MB, 16 * VW, WK * 64, gatedk::gated_thin<MB, VW, WK, WPE>}
-const GatedKernel kForward[] = {FORWARD_TILE(256, 256, 32, 64, 64, 4), FORWARD_TILE(128, 128, 32, 32, 64, 4),
-                                FORWARD_TILE(64, 64, 32, 32, 64, 2)};
-const GatedKernel kBackX[] = {BACK_TILE(BACK_X, 256, 256, 32, 64, 64, 4), BACK_TILE(BACK_X, 128, 128, 32, 32, 64, 4),
-                              BACK_TILE(BACK_X, 64, 64, 32, 32, 32, 2)};
-const GatedKernel kBackW[] = {BACK_TILE(BACK_W, 256, 256, 32, 64, 64, 4), BACK_TILE(BACK_W, 128, 128, 32, 32, 64, 4),
-                              BACK_TILE(BACK_W, 64, 64, 32, 32, 32, 2)};
-const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(2, 1, 8, 4), GATED_THIN(4, 2, 4, 2)};
-const GatedKernel kSimple[] = {{32, 32, 256, gatedk::gated_simple<gatedk::FORWARD>},
-                               {32, 32, 256, gatedk::gated_simple<gatedk::BACK_X>},
-                               {32, 32, 256, gatedk::gated_simple<gatedk::BACK_W>}};
+const GatedKernel kForwardTile[] = {FORWARD_TILE(64, 128, 32, 32, 64, 4), FORWARD_TILE(128, 128, 32, 32, 64, 4),
+                                    FORWARD_TILE(256, 256, 32, 64, 64, 4)};
+// rows x columns: 16 x 16, 16 x 32, 16 x 64, 32 x 32, 32 x 64
+const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(1, 2, 8, 4), GATED_THIN(1, 4, 8, 4),
+                             GATED_THIN(2, 2, 8, 2), GATED_THIN(2, 4, 8, 2)};
+const GatedKernel kBackX = BACK_TILE(BACK_X, 256, 256, 32, 64, 64, 4);
+const GatedKernel kBackW[] = {BACK_TILE(BACK_W, 64, 128, 32, 32, 32, 4), BACK_TILE(BACK_W, 256, 256, 32, 64, 64, 4)};
+const GatedKernel kSimpleForward = {32, 32, 256, gatedk::gated_simple<gatedk::FORWARD>};
+const GatedKernel kSimpleBackW = {32, 32, 256, gatedk::gated_simple<gatedk::BACK_W>};
 
 long long tiles(const GatedKernel &k, const gatedk::TileArgs &a, int kind) {
     return ceil_div(a.M, k.bm) * ceil_div(a.N, k.bn) * (kind == gatedk::BACK_W ? 2 : 1);
+}
+
+// Up to 32 rows G and U are read once and that is the time, so the tiles are as narrow as
+// gives every CU one and as wide as leaves about one round of them.  Measured (us, rows x N x
+// K; by columns of a tile):
+//   1 x 4096 x 2048: 16.5 (16), 18.2 (32), 26.7 (64); 1 x 6000 x 2048: 27.6, 25.3, 34.5;
+//   1 x 8000 x 2048: 30.9, 26.6, 34.2; 1 x 11008 x 4096: 108, 96, 73;
+//   29 rows (16-row tiles / 32-row): 1024 x 1000: 8.9, 10.9, 15.6 / 12.4, 14.9; 4096 x 2048:
+//   26.2, 19.6, 27.8 / 20.7, 26.5, 42.0; 6000 x 2048: 43, 42, 35 / 42, 34, 48; 11008 x 4096:
+//   162, 119, 122 / 140, 125, 91.
+// More rows: the matrix cores, and how the tiles fill rounds of 256 CUs, set the time.  A
+// round costs what 256 workgroups took at K = 2048 (alone; among others):
+//   61 x 4096: 31.9 on 16 x 32, 28.6 on 16 x 64, 26.7 on 32 x 32, 42 on 32 x 64, 83 on 64 x 64;
+//   100 x 4096: 55.7, 44.3, 50.4, 42.6, 83; 256 x 4096: 106, 84, 101, 85, 85, 136 (128 x 64);
+//   400 x 4096: 165, 141, 167, 158, 142, 136; 700 x 4096: 279, 225, 265, 241, 201, 251;
+//   1000 x 4096: 394, 319, 391, 340, 276, 255; 4096 x 4096: 1049 on 64 x 64, 1000 on 128 x
+//   64, 965 on 256 x 128.
+const GatedKernel &choose_forward(const gatedk::TileArgs &a) {
+    if (a.M <= 16) return kThin[a.N <= 4608 ? 0 : a.N <= 9216 ? 1 : 2];
+    if (a.M <= 32) return kThin[a.N <= 2304 ? 0 : a.N <= 4608 ? 1 : a.N <= 9216 ? 3 : 4];
+    struct Round {
+        const GatedKernel *kernel;
+        double alone, among;
+    };
+    const Round rounds[] = {{&kThin[0], 16, 10},         {&kThin[1], 18, 13.2},        {&kThin[2], 27, 20.6},
+                            {&kThin[3], 26, 25},         {&kThin[4], 42, 42},          {&kForwardTile[0], 83, 70},
+                            {&kForwardTile[1], 133, 125}, {&kForwardTile[2], 482, 482}};
+    const GatedKernel *best = nullptr;
+    double least = 0.0;
+    for (const Round &r : rounds) {
+        const long long n = ceil_div(tiles(*r.kernel, a, gatedk::FORWARD), 256);
+        const double cost = n <= 1 ? r.alone : r.among * (double)n;
+        if (best == nullptr || cost < least) best = r.kernel, least = cost;
+    }
+    return *best;
 }
 
 // 32-bit offsets from a tile's first row reach all of a tile's operands
@@ -172,17 +207,31 @@ bool reachable(const gatedk::TileArgs &a) {
     return a.lda <= reach && a.ldb[0] <= reach && a.ldb[1] <= reach;
 }
 
-int gated_product(int kind, gatedk::TileArgs a, hipStream_t stream) {
+// x^T [dgate | dup].  Measured (us, T x N x K; 64 x 128 tiles, 256 x 256, and two sums of
+// outer products one after the other): 1 x 2048 x 1024 9.7, 21.5, 16.5; 500 x 2048 x 1024
+// 43, 128, 46; 2000 x 2048 x 1024 140, 471, 136; 4096 x 4096 x 2048 1042, 967.
+const GatedKernel &choose_back_w(const gatedk::TileArgs &a) {
+    const double small = 140.0 / 2 * ceil_div(tiles(kBackW[0], a, gatedk::BACK_W), 256);
+    const double large = 482.0 * ceil_div(tiles(kBackW[1], a, gatedk::BACK_W), 256);
+    return kBackW[large < small ? 1 : 0];
+}
+
+int launch_gated(const GatedKernel &k, int kind, gatedk::TileArgs a, hipStream_t stream) {
     a.xcd_shift = xcd_shift();
-    const GatedKernel *k = &kSimple[kind];
-    if (reachable(a)) {
-        const GatedKernel *sizes = kind == gatedk::FORWARD ? kForward : kind == gatedk::BACK_X ? kBackX : kBackW;
-        if (kind == gatedk::FORWARD && a.M <= 64)
-            k = &kThin[a.M <= 16 ? 0 : a.M <= 32 ? 1 : 2];
-        else
-            k = &sizes[tiles(sizes[0], a, kind) >= 256 ? 0 : tiles(sizes[1], a, kind) >= 256 ? 1 : 2];
-    }
-    return enqueue(k->fn, tiles(*k, a, kind), k->threads, a, stream);
+    return enqueue(k.fn, tiles(k, a, kind), k.threads, a, stream);
+}
+
+// dx = dgate G^T + dup U^T: in one sum on 256 x 256 tiles where they fill the chip, else one
+// product after the other on the kernels of sgemm_grouped().  Measured (us, T x N x K): 29 x
+// 2048 x 1024 21 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 56 (98), 2000 x 2048 x 1024
+// 150 (128 x 64 tiles: 151).
+int gated_back_x(const gatedk::TileArgs &a, hipStream_t stream) {
+    if (reachable(a) && tiles(kBackX, a, gatedk::BACK_X) >= 224) return launch_gated(kBackX, gatedk::BACK_X, a, stream);
+    const int rc = rowk::rows_product(a.M, a.N, a.K, a.A[0], (int)a.lda, a.B[0], (int)a.ldb[0], true, 0.0f, a.C[0],
+                                      (int)a.ldc[0], stream);
+    if (rc != SGEMM_OK) return rc;
+    return rowk::rows_product(a.M, a.N, a.K, a.A[1], (int)a.lda, a.B[1], (int)a.ldb[1], true, 1.0f, a.C[0],
+                              (int)a.ldc[0], stream);
 }
 
 // Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors
@@ -385,7 +434,7 @@ int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, co
     a.up = up;
     a.ldgate = ldgate;
     a.ldup = ldup;
-    return gated_product(gatedk::FORWARD, a, stream);
+    return launch_gated(reachable(a) ? choose_forward(a) : kSimpleForward, gatedk::FORWARD, a, stream);
 }
 
 size_t sgemm_gated_grad_workspace_size(int T, int N, int K) {
@@ -421,8 +470,8 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     NEED(22, (dG == nullptr) == (dU == nullptr) && aligned4(dU));
     NEED(23, lddu >= at_least_1(N));
     if (slopes && !workspace_ok(workspace, workspace_bytes, gated_grad_bytes(T, N))) return SGEMM_ERR_WORKSPACE;
-    if (T > kLongest || N > kLongest || K > kLongest) return SGEMM_ERR_TOO_LARGE;
-    const int64_t ldz = slope_ld(N);
+    if (T > kLongest || N > kLongest || K > kLongest || (to_x && T >= rowk::kMostRows)) return SGEMM_ERR_TOO_LARGE;
+    const int64_t ldz = slope_ld(at_least_1(N));  // (a leading dimension, also of no columns)
     float *dgate = static_cast<float *>(workspace);
     float *dup = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up((size_t)T * ldz * 4));
     if (slopes) {
@@ -460,7 +509,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
         a.ldb[1] = ldu;
         a.C[0] = a.C[1] = dx;
         a.ldc[0] = a.ldc[1] = lddx;
-        const int rc = gated_product(gatedk::BACK_X, a, stream);
+        const int rc = gated_back_x(a, stream);
         if (rc != SGEMM_OK) return rc;
     }
     if (to_w && !(T == 0 && beta == 1.0f)) {
@@ -478,7 +527,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
         a.ldc[0] = lddg;
         a.ldc[1] = lddu;
         a.beta = beta;
-        return gated_product(gatedk::BACK_W, a, stream);
+        return launch_gated(reachable(a) ? choose_back_w(a) : kSimpleBackW, gatedk::BACK_W, a, stream);
     }
     return SGEMM_OK;
 }

@@ -164,15 +164,16 @@ gated_tile(TileArgs a) {
         }
     };
     auto landed = [&](float *st, int t) {
-        __builtin_amdgcn_s_waitcnt(0);
+        rowk::wait_loads<0>();
         if constexpr (KIND != BACK_W) {
             const int left = a.K - (KIND == BACK_X && t >= KT1 ? t - KT1 : t) * BK;
             if ((a.K & 3) != 0 && t < KT && left > 0 && left < BK) {
                 sa.clear(st, wave, lane, left);
                 if constexpr (B_LONG) sb.clear(st + SA::SIZE, wave, lane, left);
+                __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0
             }
         }
-        __syncthreads();
+        rowk::meet();
     };
 
     floatx16 acc[MI][NI];
@@ -194,88 +195,90 @@ gated_tile(TileArgs a) {
     const int b_at = SA::SIZE + (B_LONG ? (wn + li) * BK
                                         : lh * (BK / 2) * CN + (DUAL ? wn / 2 + NI / 2 * li : wn + NI * li));
 
-    auto tile = [&](const float *__restrict__ st, float *__restrict__ nx, int tnext) {
-        float av[2][MI][4], bv[2][NI][4];
-        auto read_a = [&](int d, int q) {
-            if constexpr (A_WIDE) {
+    float av[2][MI][4], bv[2][NI][4];
+    auto read = [&](const float *__restrict__ st, int q) {
+        const int d = q & 1;
+        if constexpr (B_LONG) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    typedef typename sgk::vec_t<MI>::type V;
-                    const V v = *reinterpret_cast<const V *>(st + a_at + (4 * q + e) * BM);
-#pragma unroll
-                    for (int i = 0; i < MI; ++i) av[d][i][e] = sgk::vget(v, i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const float4 v = *reinterpret_cast<const float4 *>(st + a_at + i * 32 * BK + at[q]);
-                    av[d][i][0] = v.x;
-                    av[d][i][1] = v.y;
-                    av[d][i][2] = v.z;
-                    av[d][i][3] = v.w;
-                }
+            for (int j = 0; j < NI; ++j) {
+                const float4 v = *reinterpret_cast<const float4 *>(st + b_at + j * 32 * BK + at[q]);
+                bv[d][j][0] = v.x;
+                bv[d][j][1] = v.y;
+                bv[d][j][2] = v.z;
+                bv[d][j][3] = v.w;
             }
-        };
-        auto read_b = [&](int d, int q) {
-            if constexpr (B_LONG) {
-#pragma unroll
-                for (int j = 0; j < NI; ++j) {
-                    const float4 v = *reinterpret_cast<const float4 *>(st + b_at + j * 32 * BK + at[q]);
-                    bv[d][j][0] = v.x;
-                    bv[d][j][1] = v.y;
-                    bv[d][j][2] = v.z;
-                    bv[d][j][3] = v.w;
-                }
-            } else {
-                constexpr int W = DUAL ? NI / 2 : NI;
-                typedef typename sgk::vec_t<W>::type V;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int s = 0; s < (DUAL ? 2 : 1); ++s) {
-                        const V v = *reinterpret_cast<const V *>(st + b_at + s * SB::SIZE + (4 * q + e) * CN);
-#pragma unroll
-                        for (int j = 0; j < W; ++j) bv[d][DUAL ? 2 * j + s : j][e] = sgk::vget(v, j);
-                    }
-            }
-        };
-        read_b(0, 0);
-        read_a(0, 0);
-#pragma unroll
-        for (int q = 0; q < QN; ++q) {
-            if (q + 1 < QN) {
-                read_b((q + 1) & 1, q + 1);
-                read_a((q + 1) & 1, q + 1);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            constexpr int W = DUAL ? NI / 2 : NI;
+            typedef typename sgk::vec_t<W>::type V;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
-                for (int i = 0; i < MI; ++i)
+                for (int s = 0; s < (DUAL ? 2 : 1); ++s) {
+                    const V v = *reinterpret_cast<const V *>(st + b_at + s * SB::SIZE + (4 * q + e) * CN);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(av[q & 1][i][e], bv[q & 1][j][e], acc[i][j], 0, 0, 0);
-                        __builtin_amdgcn_sched_barrier(0);
-                        // the next tile's loads, in pieces behind the first chunk's MFMAs
-                        constexpr int U = 4 * MI * NI;
-                        const int u = (e * MI + i) * NI + j;
-                        if (q == 0) {
+                    for (int j = 0; j < W; ++j) bv[d][DUAL ? 2 * j + s : j][e] = sgk::vget(v, j);
+                }
+        }
+        if constexpr (A_WIDE) {
 #pragma unroll
-                            for (int p = 0; p < DP; ++p)
-                                if (p * U / DP == u) fetch(nx, tnext, p);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    }
+            for (int e = 0; e < 4; ++e) {
+                typedef typename sgk::vec_t<MI>::type V;
+                const V v = *reinterpret_cast<const V *>(st + a_at + (4 * q + e) * BM);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) av[d][i][e] = sgk::vget(v, i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const float4 v = *reinterpret_cast<const float4 *>(st + a_at + i * 32 * BK + at[q]);
+                av[d][i][0] = v.x;
+                av[d][i][1] = v.y;
+                av[d][i][2] = v.z;
+                av[d][i][3] = v.w;
+            }
         }
     };
-    if (KT > 0) {
+    auto multiply = [&](int q, auto between) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int p = 0; p < DP; ++p) fetch(smem, 0, p);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(av[q & 1][i][e], bv[q & 1][j][e], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    between((e * MI + i) * NI + j);
+                }
+    };
+    if (KT > 0) {
+        // Fragments are read a chunk ahead, across the tiles' borders: a tile's last chunk is
+        // multiplied behind the barrier that ends its reads, and the loads of tile t + 2 go
+        // between its MFMAs, into the stage that was read.
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int p = 0; p < DP; ++p) fetch(smem + s * STAGE, s, p);
         landed(smem, 0);
+        read(smem, 0);
         for (int t = 0; t < KT; ++t) {
-            tile(smem + (t & 1) * STAGE, smem + ((t + 1) & 1) * STAGE, t + 1);
-            landed(smem + ((t + 1) & 1) * STAGE, t + 1);
+            float *st = smem + (t & 1) * STAGE, *next = smem + ((t + 1) & 1) * STAGE;
+#pragma unroll
+            for (int q = 0; q + 1 < QN; ++q) {
+                read(st, q + 1);
+                multiply(q, [](int) {});
+            }
+            landed(next, t + 1);
+            read(next, 0);
+            multiply(QN - 1, [&](int u) {
+                constexpr int U = 4 * MI * NI;
+#pragma unroll
+                for (int p = 0; p < DP; ++p)
+                    if (p * U / DP == u) fetch(st, t + 2, p);
+                __builtin_amdgcn_sched_barrier(0);
+            });
         }
+        rowk::wait_loads<0>();
     }
 
     // Register r of block (i, j) on lane (li, lh): block row 8 (r / 4) + 4 lh + r % 4 = b
@@ -314,6 +317,24 @@ gated_tile(TileArgs a) {
 // v_mfma_f32_16x16x4_f32: lane (li, lk) loads VW consecutive columns of k = 4 lk + e
 // of 16 k's, and the four k's of a row of x.  Partial sums meet in LDS in order.
 // ---------------------------------------------------------------------------
+// Tile columns go to the XCDs in turn in runs of RUN neighbours, which share lines where a
+// tile is narrower than one or rows are not aligned (one row, 4096 x 2048 on 16 columns:
+// 23.8 us in runs of one, 16.3 of two or four; 29 rows, 4095 x 2047 on 32: 25.2, 23.2, 22.8);
+// a column's row tiles stay on its XCD.
+template <int RUN>
+__device__ __forceinline__ void thin_place(int id, int nbm, int nbn, int xcd_shift, int &tm, int &tn) {
+    const int span = RUN << xcd_shift, dealt = nbn / span * span;
+    if (id < dealt * nbm) {
+        const int x = id & ((1 << xcd_shift) - 1), i = id >> xcd_shift, c = i / nbm;
+        tm = i - c * nbm;
+        tn = ((c / RUN << xcd_shift) + x) * RUN + c % RUN;
+        return;
+    }
+    const int i = id - dealt * nbm, c = i / nbm;
+    tm = i - c * nbm;
+    tn = dealt + c;
+}
+
 template <int MB, int VW, int WK, int WPE>
 __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) gated_thin(TileArgs a) {
     constexpr int BM = 16 * MB, BN = 16 * VW;
@@ -322,7 +343,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
     const int li = lane & 15, lk = lane >> 4;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
     int tm, tn;
-    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
+    thin_place<4>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const float *A = a.A[0] + (int64_t)m0 * a.lda;
     const int64_t a_bytes = ((int64_t)(a.M - m0 - 1) * a.lda + a.K) * 4;
@@ -462,7 +483,7 @@ template <int ACT> __global__ void __launch_bounds__(256) gated_slopes(SlopeArgs
 }
 
 // ---------------------------------------------------------------------------
-// Any strides: 32 x 32 tiles, every element checked.
+// Any strides: 32 x 32 tiles, every element checked (FORWARD and BACK_W).
 // ---------------------------------------------------------------------------
 template <int KIND> __global__ void __launch_bounds__(256) gated_simple(TileArgs a) {
     constexpr int T = 32;
@@ -473,36 +494,30 @@ template <int KIND> __global__ void __launch_bounds__(256) gated_simple(TileArgs
     const int64_t m0 = (int64_t)(blockIdx.x / cols) * T, n0 = (int64_t)(tn - which * nbn) * T;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int seg = 0; seg < (KIND == BACK_X ? 2 : 1); ++seg)
-        for (int64_t k0 = 0; k0 < a.K; k0 += T) {
+    for (int64_t k0 = 0; k0 < a.K; k0 += T) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty + 8 * i;
+            // As[m][k], Bs[k][n]; lanes walk what is contiguous
+            if (KIND == BACK_W)
+                As[tx][r] = k0 + r < a.K && m0 + tx < a.M ? a.A[0][(k0 + r) * a.lda + m0 + tx] : 0.0f;
+            else
+                As[r][tx] = k0 + tx < a.K && m0 + r < a.M ? a.A[0][(m0 + r) * a.lda + k0 + tx] : 0.0f;
+#pragma unroll
+            for (int s = 0; s < (KIND == FORWARD ? 2 : 1); ++s) {
+                const int src = KIND == FORWARD ? s : which;
+                Bs[s][r][tx] = k0 + r < a.K && n0 + tx < a.N ? a.B[src][(k0 + r) * a.ldb[src] + n0 + tx] : 0.0f;
+            }
+        }
+        __syncthreads();
+        for (int k = 0; k < T; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = ty + 8 * i;
-                // As[m][k], Bs[k][n]; lanes walk what is contiguous
-                if (KIND == BACK_W)
-                    As[tx][r] = k0 + r < a.K && m0 + tx < a.M ? a.A[0][(k0 + r) * a.lda + m0 + tx] : 0.0f;
-                else
-                    As[r][tx] = k0 + tx < a.K && m0 + r < a.M ? a.A[seg][(m0 + r) * a.lda + k0 + tx] : 0.0f;
-#pragma unroll
-                for (int s = 0; s < (KIND == FORWARD ? 2 : 1); ++s) {
-                    const int src = KIND == FORWARD ? s : KIND == BACK_X ? seg : which;
-                    const float *B = a.B[src];
-                    const int64_t ldb = a.ldb[src];
-                    if (KIND == BACK_X)
-                        Bs[s][tx][r] = k0 + tx < a.K && n0 + r < a.N ? B[(n0 + r) * ldb + k0 + tx] : 0.0f;
-                    else
-                        Bs[s][r][tx] = k0 + r < a.K && n0 + tx < a.N ? B[(k0 + r) * ldb + n0 + tx] : 0.0f;
-                }
+                acc[0][i] = fmaf(As[ty + 8 * i][k], Bs[0][k][tx], acc[0][i]);
+                if (KIND == FORWARD) acc[1][i] = fmaf(As[ty + 8 * i][k], Bs[1][k][tx], acc[1][i]);
             }
-            __syncthreads();
-            for (int k = 0; k < T; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[0][i] = fmaf(As[ty + 8 * i][k], Bs[0][k][tx], acc[0][i]);
-                    if (KIND == FORWARD) acc[1][i] = fmaf(As[ty + 8 * i][k], Bs[1][k][tx], acc[1][i]);
-                }
-            __syncthreads();
-        }
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + ty + 8 * i, n = n0 + tx;

@@ -16,7 +16,9 @@
 
 namespace i8k {
 
+using rowk::meet;
 using rowk::rsrc_t;
+using rowk::wait_loads;
 using rowk::whole_rsrc;
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
@@ -94,21 +96,6 @@ template <int ROWS, int BK, int NT> struct Stage {
         }
     }
 };
-
-// Waits until this wave's loads but the newest N have landed and its LDS accesses have
-// completed (gfx9 encoding: vmcnt in bits 3:0 and 15:14, lgkmcnt 0, expcnt any).
-template <int N> __device__ __forceinline__ void wait_loads() {
-    static_assert(N >= 0 && N <= 63, "vmcnt is 6 bits");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-    asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void meet() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
 
 template <int BM, int BN, int BK, int WM, int WN, int STG, int AHEAD, int WPE>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))

@@ -1,5 +1,6 @@
-// lanes.hpp -- what the row kernels share: buffer descriptors that end at an
-// operand's last element, lane exchange, four floats at any 4-byte alignment.
+// lanes.hpp -- what the row and block kernels share: buffer descriptors that end at an
+// operand's last element, lane exchange, four floats at any 4-byte alignment, waits for
+// loads that write LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -102,6 +103,21 @@ template <class V> __device__ __forceinline__ V fma4(float s, V a, V c) {
     r.z = fmaf(s, a.z, c.z);
     r.w = fmaf(s, a.w, c.w);
     return r;
+}
+
+// Waits until this wave's loads but the newest N have landed and its LDS accesses have
+// completed (gfx9 encoding: vmcnt in bits 3:0 and 15:14, lgkmcnt 0, expcnt any).
+template <int N> __device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N <= 63, "vmcnt is 6 bits");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 }  // namespace rowk

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "grouped_kernels.hpp"
+#include "rows_api.hpp"
 #include "rows_kernels.hpp"
 
 namespace {
@@ -29,7 +30,7 @@ int enqueue(void (*kernel)(A), long long grid, int threads, const A &args, hipSt
 // What a kernel's loop steps through in 31 bits is at most this long: no step
 // beyond the end passes INT_MAX (it would go on from below 0).
 constexpr int kLongest = INT_MAX - 1024;
-constexpr int kMostSlots = 1 << 29;  // of sgemm_grouped, and rows of the adapters
+constexpr int kMostSlots = rowk::kMostRows;  // of sgemm_grouped, and rows of the adapters
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -389,6 +390,11 @@ GroupedArgs expand(int M, int N, int G, int rank, float alpha, const float *H, c
 }
 
 }  // namespace
+
+int rowk::rows_product(int M, int N, int K, const float *A, int lda, const float *B, int ldb, bool trans_b, float beta,
+                       float *C, int ldc, hipStream_t stream) {
+    return grouped(projection(M, N, K, 1.0f, A, lda, B, ldb, beta, C, ldc), trans_b, stream);
+}
 
 extern "C" {
 

@@ -569,8 +569,8 @@ size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank);
  * need no alignment.
  *
  * Return value.  0; SGEMM_ERR_WORKSPACE; SGEMM_ERR_TOO_LARGE (a grid beyond one
- * launch; a size within 16384 of 2^31; K of sgemm_i8 above SGEMM_I8_MAX_K); a
- * positive hipError_t; or -(100 + position) for an invalid argument, as above.
+ * launch; a size within 16384 of 2^31; K of sgemm_i8 above SGEMM_I8_MAX_K; 2^29 rows or
+ * more of dx); a positive hipError_t; or -(100 + position) for an invalid argument, as above.
  * Checks run before any HIP call, the first bad argument wins, and a leading
  * dimension is checked whether or not its matrix is given; pointers to floats
  * have to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed. */
