@@ -706,7 +706,8 @@ def _matrix8(what, x, rows, cols, ld, device):
 
 
 def _sizes(*values):
-    """Integers that ctypes would cut to their low 32 bits are refused."""
+    """Integers that ctypes would cut to their low 32 bits are refused.  (Called where one of them
+    is negative or beyond 31 bits: the C call numbers those that 32 bits hold.)"""
     if max(values) > 0x7fffffff or min(values) < -0x80000000:
         raise ValueError(f"a size, leading dimension or choice among {values} is beyond 32 bits")
 
@@ -714,7 +715,8 @@ def _sizes(*values):
 def sgemm_norm(T, N, x, ldx, residual, ldr, weight, eps, sum, lds, y, ldy, q, ldq, scales, stream=None, check=True):
     """``sum`` = ``x`` + ``residual``; ``y`` = its root-mean-square norm times ``weight``; ``q`` (int8)
     and ``scales`` = y in 8 bits.  residual, weight, sum, y and q (with scales) may be None."""
-    _sizes(T, N, ldx, ldr, lds, ldy, ldq)
+    if (T | N | ldx | ldr | lds | ldy | ldq) >> 31:
+        _sizes(T, N, ldx, ldr, lds, ldy, ldq)
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_norm(
         T, N, _matrix("x", x, T, N, ldx, d), ldx, _matrix("residual", residual, T, N, ldr, d), ldr,
@@ -730,7 +732,8 @@ def sgemm_norm_grad_workspace_size(T, N) -> int:
 def sgemm_norm_grad(T, N, h, ldh, weight, eps, dy, lddy, dsum, ldds, dh, lddh, beta, dweight, workspace=None,
                     workspace_bytes=None, stream=None, check=True):
     """``dh`` (of x and of residual) and ``dweight`` from ``dy`` and ``dsum``; either may be None."""
-    _sizes(T, N, ldh, lddy, ldds, lddh)
+    if (T | N | ldh | lddy | ldds | lddh) >> 31:
+        _sizes(T, N, ldh, lddy, ldds, lddh)
     d, s = _begin(stream)
     ws, nbytes = _space(workspace, workspace_bytes, d)
     return _ret((_lib or load_library()).sgemm_norm_grad(
@@ -742,7 +745,8 @@ def sgemm_norm_grad(T, N, h, ldh, weight, eps, dy, lddy, dsum, ldds, dh, lddh, b
 
 def sgemm_quantize(T, N, x, ldx, activation, gate, ldg, q, ldq, scales, stream=None, check=True):
     """``q`` (int8) and ``scales`` = ``x``, or act(``gate``) * x, in 8 bits with a scale per row."""
-    _sizes(T, N, ldx, activation, ldg, ldq)
+    if (T | N | ldx | activation | ldg | ldq) >> 31:
+        _sizes(T, N, ldx, activation, ldg, ldq)
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_quantize(
         T, N, _matrix("x", x, T, N, ldx, d), ldx, activation, _matrix("gate", gate, T, N, ldg, d), ldg,
@@ -751,7 +755,8 @@ def sgemm_quantize(T, N, x, ldx, activation, gate, ldg, q, ldq, scales, stream=N
 
 def sgemm_i8(M, N, K, alpha, A, lda, a_scales, B, ldb, b_scales, beta, C, ldc, stream=None, check=True):
     """``C = alpha * a_scales[m] * b_scales[n] * <A[m], B[n]> + beta * C``, A (M x K) and B (N x K) int8."""
-    _sizes(M, N, K, lda, ldb, ldc)
+    if (M | N | K | lda | ldb | ldc) >> 31:
+        _sizes(M, N, K, lda, ldb, ldc)
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_i8(
         M, N, K, alpha, _matrix8("A", A, M, K, lda, d), lda, _floats("a_scales", a_scales, M, d),
@@ -761,7 +766,8 @@ def sgemm_i8(M, N, K, alpha, A, lda, a_scales, B, ldb, b_scales, beta, C, ldc, s
 
 def sgemm_gated(T, N, K, activation, x, ldx, G, ldg, U, ldu, y, ldy, gate, ldgate, up, ldup, stream=None, check=True):
     """``y`` = act(x G) * (x U); ``gate`` = x G and ``up`` = x U too, unless both are None."""
-    _sizes(T, N, K, activation, ldx, ldg, ldu, ldy, ldgate, ldup)
+    if (T | N | K | activation | ldx | ldg | ldu | ldy | ldgate | ldup) >> 31:
+        _sizes(T, N, K, activation, ldx, ldg, ldu, ldy, ldgate, ldup)
     d, s = _begin(stream)
     return _ret((_lib or load_library()).sgemm_gated(
         T, N, K, activation, _matrix("x", x, T, K, ldx, d), ldx, _matrix("G", G, K, N, ldg, d), ldg,
@@ -778,7 +784,8 @@ def sgemm_gated_grad(T, N, K, activation, x, ldx, G, ldg, U, ldu, gate, ldgate, 
                      lddg, dU, lddu, workspace, workspace_bytes=None, stream=None, check=True):
     """``dx``, and ``dG`` and ``dU``, from ``dy`` and the gate and up that sgemm_gated() wrote; dx, or dG and
     dU together, may be None."""
-    _sizes(T, N, K, activation, ldx, ldg, ldu, ldgate, ldup, lddy, lddx, lddg, lddu)
+    if (T | N | K | activation | ldx | ldg | ldu | ldgate | ldup | lddy | lddx | lddg | lddu) >> 31:
+        _sizes(T, N, K, activation, ldx, ldg, ldu, ldgate, ldup, lddy, lddx, lddg, lddu)
     d, s = _begin(stream)
     ws, nbytes = _space(workspace, workspace_bytes, d)
     return _ret((_lib or load_library()).sgemm_gated_grad(

@@ -108,8 +108,9 @@ const I8Kernel kI8Mid = I8_TILE(128, 128, 128, 32, 64, 2, 1, 4);    // 8 waves, 
 const I8Kernel kI8Lone = I8_TILE(128, 128, 256, 32, 64, 2, 1, 2);   // 8 waves, one per CU
 const I8Kernel kI8Small = I8_TILE(64, 64, 256, 32, 32, 2, 3, 2);    // 4 waves, two per CU
 const I8Kernel kI8Thin1 = I8_THIN(1, 1, 8, 4);
-const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 4);
+const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 2);
 const I8Kernel kI8Thin4 = I8_THIN(4, 1, 8, 2);
+const I8Kernel kI8Thin42 = I8_THIN(4, 2, 8, 2);
 const I8Kernel kI8Simple = {32, 32, 256, i8k::i8_simple};
 
 long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ceil_div(N, k.bn); }
@@ -123,7 +124,10 @@ long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ce
 //   256 x 256    46.3 46.2 28.6 46.3 46.6 50.6  51.7  54.0    73
 // So up to 64 rows thin; then by rounds of tiles (256 CUs; 64 x 64: two on each), each
 // priced by what a full one took: 64 x 64 10, 128 x 128 16 alone on its CU and 12.4
-// among others, 256 x 256 41.
+// among others, 256 x 256 41.  A CU takes in about 40 GB/s however the loads are laid out,
+// so 64 x 32 thin tiles win where one round of them is enough (100 x 4096 x 4096 14.7 against
+// 17.4 on 64 x 64, 700 x 700 x 5000 16.1 against 23.7; 515 x 1024 x 2816, 288 tiles, 17.9
+// against 13.3).
 const I8Kernel &choose_i8(const i8k::Args &a) {
     // the fast kernels load 16 bytes at 4-byte alignment, at 32-bit offsets from a tile's
     // first row
@@ -137,6 +141,7 @@ const I8Kernel &choose_i8(const i8k::Args &a) {
     const double small = 10.0 * ceil_div(tiles(kI8Small, a.M, a.N), 512);
     const double middle = mid <= 256 ? 16.0 : 12.4 * ceil_div(mid, 256);
     const double large = 41.0 * ceil_div(tiles(kI8Large, a.M, a.N), 256);
+    if (tiles(kI8Thin42, a.M, a.N) <= 256) return kI8Thin42;
     if (small <= middle && small <= large) return kI8Small;
     if (middle <= large) return mid <= 256 ? kI8Lone : kI8Mid;
     return kI8Large;
@@ -223,15 +228,12 @@ int launch_gated(const GatedKernel &k, int kind, gatedk::TileArgs a, hipStream_t
 
 // dx = dgate G^T + dup U^T: in one sum on 256 x 256 tiles where they fill the chip, else one
 // product after the other on the kernels of sgemm_grouped().  Measured (us, T x N x K): 29 x
-// 2048 x 1024 21 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 56 (98), 2000 x 2048 x 1024
+// 2048 x 1024 16 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 56 (98), 2000 x 2048 x 1024
 // 150 (128 x 64 tiles: 151).
 int gated_back_x(const gatedk::TileArgs &a, hipStream_t stream) {
     if (reachable(a) && tiles(kBackX, a, gatedk::BACK_X) >= 224) return launch_gated(kBackX, gatedk::BACK_X, a, stream);
-    const int rc = rowk::rows_product(a.M, a.N, a.K, a.A[0], (int)a.lda, a.B[0], (int)a.ldb[0], true, 0.0f, a.C[0],
-                                      (int)a.ldc[0], stream);
-    if (rc != SGEMM_OK) return rc;
-    return rowk::rows_product(a.M, a.N, a.K, a.A[1], (int)a.lda, a.B[1], (int)a.ldb[1], true, 1.0f, a.C[0],
-                              (int)a.ldc[0], stream);
+    const int ldb[2] = {(int)a.ldb[0], (int)a.ldb[1]};
+    return rowk::rows_product_pair(a.M, a.N, a.K, a.A, (int)a.lda, a.B, ldb, a.C[0], (int)a.ldc[0], stream);
 }
 
 // Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors

@@ -586,6 +586,19 @@ __global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_
     thin_tile<MB, VW, WK, WN, WPE, TRANS_B>(a, (int)blockIdx.x);
 }
 
+// Two products of the same size into one C, a tile of both per workgroup: the second adds
+// to what the same threads have written (29 x 2048 x 1024, N x K: 21 us in two launches, 16
+// in one).
+struct TwoArgs {
+    GroupedArgs first, second;  // second.beta 1
+};
+template <int MB, int VW, int WK, int WN, int WPE, bool TRANS_B>
+__global__ void __launch_bounds__(WK * WN * 64) __attribute__((amdgpu_waves_per_eu(WPE))) thin_twice(TwoArgs a) {
+    thin_tile<MB, VW, WK, WN, WPE, TRANS_B>(a.first, (int)blockIdx.x);
+    __syncthreads();  // (the partial sums' LDS)
+    thin_tile<MB, VW, WK, WN, WPE, TRANS_B>(a.second, (int)blockIdx.x);
+}
+
 // A product and, in workgroups of its own ahead of it, few rows times their
 // adapters' U: neither needs the other, and together they are one launch (with
 // expand_rows behind it, one row, 4096 x 4096: 18.4 us, 21.4 one after the other;

@@ -176,16 +176,19 @@ i8_tile(Args a) {
         __builtin_amdgcn_sched_barrier(0);
     };
     if (KT > 0) {
-        for (int f = tid; f < BM + BN; f += NT) {
-            const float *from = f < BM ? a.sa : a.sb;
-            const int row = f < BM ? bm + f : bn + f - BM, end = f < BM ? a.M : a.N;
-            scale[f] = from != nullptr && row < end ? from[row] : 1.0f;
+        static_assert(BM + BN <= NT, "a scale per thread");
+        float mine = 1.0f;  // (asked for ahead of the tiles, so that its wait is not theirs)
+        if (tid < BM + BN) {
+            const float *from = tid < BM ? a.sa : a.sb;
+            const int row = tid < BM ? bm + tid : bn + tid - BM, end = tid < BM ? a.M : a.N;
+            if (from != nullptr && row < end) mine = from[row];
         }
         // Fragments are read AHEAD k-steps before their MFMAs, across the tiles' borders:
         // the last AHEAD steps of a tile are multiplied behind the barrier that ends its
         // reads, while the stage that it was read from is filled with tile t + STG.
 #pragma unroll
         for (int s = 0; s < STG; ++s) fetch(smem + s * STAGE, s * BK);
+        if (tid < BM + BN) scale[tid] = mine;
         wait_loads<(STG - 1) * DP>();
         landed(smem, 0);
 #pragma unroll
@@ -306,6 +309,15 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[d][h][i], bv[d][h][j], acc[i][j], 0, 0, 0);
     };
     const int whole = (int64_t)u1 * 128 > a.K ? u1 - 1 : u1;
+    constexpr int OUT = (BM * BN + WK * 64 - 1) / (WK * 64);  // results per thread
+    float sa[OUT], sb[OUT];  // (asked for ahead of the operands)
+#pragma unroll
+    for (int o = 0; o < OUT; ++o) {
+        const int f = tid + o * WK * 64, m = m0 + f / BN, n = n0 + f % BN;
+        const bool there = a.K > 0 && f < BM * BN && m < a.M && n < a.N;
+        sa[o] = there && a.sa != nullptr ? a.sa[m] : 1.0f;
+        sb[o] = there && a.sb != nullptr ? a.sb[n] : 1.0f;
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch(d, u0 + d);
     for (int u = u0; u < u1; u += D) {
@@ -330,15 +342,15 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 #pragma unroll
             for (int r = 0; r < 4; ++r) part[w][(16 * i + 4 * lk + r) * BN + 16 * j + li] = acc[i][j][r];
     __syncthreads();
-    for (int f = tid; f < BM * BN; f += WK * 64) {
-        const int m = m0 + f / BN, n = n0 + f % BN;
-        if (m >= a.M || n >= a.N) continue;
+#pragma unroll
+    for (int o = 0; o < OUT; ++o) {
+        const int f = tid + o * WK * 64, m = m0 + f / BN, n = n0 + f % BN;
+        if (f >= BM * BN || m >= a.M || n >= a.N) continue;
         int sum = part[0][f];
 #pragma unroll
         for (int i = 1; i < WK; ++i) sum += part[i][f];
         float *c = a.C + (int64_t)m * a.ldc + n;
-        const double s = a.K > 0 ? (double)a.alpha * scale_at(a.sa, m) * scale_at(a.sb, n) : 0.0;
-        *c = scaled(a, sum, s, a.beta != 0.0f ? *c : 0.0f);
+        *c = scaled(a, sum, (double)a.alpha * (double)sa[o] * (double)sb[o], a.beta != 0.0f ? *c : 0.0f);
     }
 }
 

@@ -66,6 +66,7 @@ long long row_tiles(const GroupedArgs &a, int bm) {
 
 typedef void (*GroupedFn)(GroupedArgs);
 typedef void (*PairFn)(rowk::PairArgs);
+typedef void (*TwoFn)(rowk::TwoArgs);
 
 // The fast kernels' byte offsets are 32-bit: a gathered operand is addressed
 // from its first row, one in order from the tile's (tn: the group's) first.
@@ -79,14 +80,16 @@ struct Block {
     int bm, bn, threads;
     GroupedFn fn;
     PairFn pair;  // with few rows' adapters ahead of it
+    TwoFn two;    // two products into one C
 };
 #define THIN_NN(MB, VW, WK, WN, WPE) \
-    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, nullptr}
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, nullptr, nullptr}
 #define THIN_FEW(MB, VW, WK, WN, WPE)                                              \
     {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, false>, \
-     rowk::thin_and_shrink<MB, VW, WK, WN, WPE>}
-#define THIN_NT(MB, VW, WK, WN, WPE) \
-    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, true>, nullptr}
+     rowk::thin_and_shrink<MB, VW, WK, WN, WPE>, nullptr}
+#define THIN_NT(MB, VW, WK, WN, WPE)                                                        \
+    {16 * MB, 16 * VW * WN, WK * WN * 64, rowk::thin<MB, VW, WK, WN, WPE, true>, nullptr, \
+     rowk::thin_twice<MB, VW, WK, WN, WPE, true>}
 // rows x columns of a tile; waves over K x waves over columns.  B as K x N:
 const Block kTall = THIN_NN(4, 4, 2, 2, 2);      // 64 x 128, 2 x 2
 const Block kLow = THIN_FEW(2, 4, 4, 1, 4);       // 32 x 64, 4 x 1
@@ -174,7 +177,7 @@ int grouped(GroupedArgs a, bool trans_b, hipStream_t stream) {
     if (a.alpha == 0.0f) a.K = 0;
     if (a.K == 0 && a.beta == 1.0f) return SGEMM_OK;
     if (reachable(a, trans_b)) return launch_block(choose_block(a, trans_b), true, a, stream);
-    const Block simple = {32, 32, 256, trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>, nullptr};
+    const Block simple = {32, 32, 256, trans_b ? rowk::grouped_simple<true> : rowk::grouped_simple<false>, nullptr, nullptr};
     return launch_block(simple, false, a, stream);
 }
 
@@ -391,9 +394,19 @@ GroupedArgs expand(int M, int N, int G, int rank, float alpha, const float *H, c
 
 }  // namespace
 
-int rowk::rows_product(int M, int N, int K, const float *A, int lda, const float *B, int ldb, bool trans_b, float beta,
-                       float *C, int ldc, hipStream_t stream) {
-    return grouped(projection(M, N, K, 1.0f, A, lda, B, ldb, beta, C, ldc), trans_b, stream);
+int rowk::rows_product_pair(int M, int N, int K, const float *const A[2], int lda, const float *const B[2],
+                            const int ldb[2], float *C, int ldc, hipStream_t stream) {
+    if (M >= kMostSlots || K > kLongest) return SGEMM_ERR_TOO_LARGE;
+    TwoArgs t = {projection(M, N, K, 1.0f, A[0], lda, B[0], ldb[0], 0.0f, C, ldc),
+                 projection(M, N, K, 1.0f, A[1], lda, B[1], ldb[1], 1.0f, C, ldc)};
+    if (M > 0 && N > 0 && K > 0 && reachable(t.first, true) && reachable(t.second, true)) {
+        const Block &b = choose_block(t.first, true);
+        const long long grid = grid_of(b, true, t.first);
+        t.second.xcd_shift = t.first.xcd_shift;
+        return enqueue(b.two, grid, b.threads, t, stream);
+    }
+    const int rc = grouped(t.first, true, stream);
+    return rc != SGEMM_OK ? rc : grouped(t.second, true, stream);
 }
 
 extern "C" {
