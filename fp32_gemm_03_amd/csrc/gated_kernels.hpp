@@ -104,9 +104,8 @@ template <int COLS, int BK, int NT> struct Wide {
 // FORWARD's wave holds gate and up of the same columns (block columns 2 j and 2 j +
 // 1), so the activation's product is taken in registers.
 // ---------------------------------------------------------------------------
-template <int KIND, int BM, int BN, int BK, int WM, int WN, int WPE>
-__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
-gated_tile(TileArgs a) {
+template <int KIND, int BM, int BN, int BK, int WM, int WN>
+__device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, float *smem) {
     constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
     constexpr bool DUAL = KIND == FORWARD, A_WIDE = KIND == BACK_W, B_LONG = KIND == BACK_X;
     constexpr int CN = DUAL ? BN / 2 : BN;  // columns of the result
@@ -114,13 +113,12 @@ gated_tile(TileArgs a) {
     typedef typename std::conditional<A_WIDE, Wide<BM, BK, NT>, Long<BM, BK, NT>>::type SA;
     typedef typename std::conditional<B_LONG, Long<BN, BK, NT>, Wide<CN, BK, NT>>::type SB;
     constexpr int STAGE = (BM + BN) * BK;
-    __shared__ __attribute__((aligned(16))) float smem[2 * STAGE];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 31, lh = lane >> 5;
     const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + CN - 1) / CN;
     int tm, tn;
-    sgk::tile_of<2, 8>((int)blockIdx.x, nbm, KIND == BACK_W ? 2 * nbn : nbn, a.xcd_shift, tm, tn);
+    sgk::tile_of<2, 8>(block, nbm, KIND == BACK_W ? 2 * nbn : nbn, a.xcd_shift, tm, tn);
     const int which = KIND == BACK_W && tn >= nbn ? 1 : 0;  // BACK_W: dG's columns, then dU's
     const int bm = tm * BM, bn = (tn - which * nbn) * CN;
 
@@ -311,6 +309,13 @@ gated_tile(TileArgs a) {
         }
 }
 
+template <int KIND, int BM, int BN, int BK, int WM, int WN, int WPE>
+__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+gated_tile(TileArgs a) {
+    __shared__ __attribute__((aligned(16))) float smem[2 * (BM + BN) * BK];
+    gated_tile_of<KIND, BM, BN, BK, WM, WN>(a, (int)blockIdx.x, smem);
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: reading G and U once is the work.  16 MB rows and 16 VW columns of both a
 // workgroup, its WK waves each a share of K, operands from memory straight to
@@ -448,6 +453,123 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
             a.up[(int64_t)m * a.ldup + n] = u;
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// Back from few rows, both gradients in one launch: the first workgroups compute dx, which
+// reads G and U once, the others dG and dU, which they write once.
+//   dx: 16 MB rows and 16 VW columns a workgroup; waves 0 to 3 a share of K each of dgate
+//   G^T, waves 4 to 7 of dup U^T, operands (both along K) from memory straight to
+//   v_mfma_f32_16x16x4_f32; a step is 32 of K, whole lines; partial sums meet in LDS.
+//   A CU takes in 25 to 40 GB/s, which bounds dx where it has few tiles (K split over
+//   workgroups as well: 29 rows, 2048 x 1024, 19.5 us with the launch that adds them up, 22.0
+//   without; 1 x 4096 x 2048 36.8 against 34.7; not kept).
+// ---------------------------------------------------------------------------
+struct FewArgs {
+    TileArgs x, w;  // of BACK_X and BACK_W
+    int ahead;      // workgroups of dx, a multiple of 8: the others keep their XCDs
+};
+
+template <int MB, int VW> __device__ __forceinline__ void few_rows_dx(const TileArgs &a, int block, float *part) {
+    constexpr int BM = 16 * MB, BN = 16 * VW, WK = 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int seg = wave / WK, w = wave % WK;
+    const int li = lane & 15, lk = lane >> 4;
+    const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
+    if (block >= nbm * nbn) return;  // (rounded up to the XCDs)
+    int tm, tn;
+    thin_place<1>(block, nbm, nbn, a.xcd_shift, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const float *A = a.A[seg] + (int64_t)m0 * a.lda, *B = a.B[seg] + (int64_t)n0 * a.ldb[seg];
+    const int64_t a_bytes = ((int64_t)(a.M - m0 - 1) * a.lda + a.K) * 4;
+    const int64_t b_bytes = ((int64_t)(a.N - n0 - 1) * a.ldb[seg] + a.K) * 4;
+    uint32_t ao[MB], bo[VW];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) ao[i] = (uint32_t)(((16 * i + li) * a.lda + 8 * lk) * 4);
+#pragma unroll
+    for (int j = 0; j < VW; ++j) bo[j] = (uint32_t)(((16 * j + li) * a.ldb[seg] + 8 * lk) * 4);
+
+    floatx4 acc[MB][VW];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < VW; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int steps = (a.K + 31) / 32;
+    const int u0 = (int)((int64_t)steps * w / WK), u1 = (int)((int64_t)steps * (w + 1) / WK);
+    constexpr int STEP = 8 * (MB + VW), D = 64 / STEP < 2 ? 2 : 64 / STEP;
+    f32x4 av[D][2][MB], bv[D][2][VW];
+    auto fetch = [&](int d, int u) {  // (past the wave's last step the descriptors are empty)
+        const int64_t k0 = 32 * (int64_t)u;
+        const rsrc_t ra = whole_rsrc(A + k0, u < u1 ? a_bytes - 4 * k0 : 0);
+        const rsrc_t rb = whole_rsrc(B + k0, u < u1 ? b_bytes - 4 * k0 : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < VW; ++j) bv[d][h][j] = sgk::raw_load_v4f32(rb, bo[j] + 16 * h, 0, 0);
+#pragma unroll
+            for (int i = 0; i < MB; ++i) av[d][h][i] = sgk::raw_load_v4f32(ra, ao[i] + 16 * h, 0, 0);
+        }
+    };
+    auto multiply = [&](int d) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int j = 0; j < VW; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[d][h][i][e], bv[d][h][j][e], acc[i][j], 0, 0, 0);
+    };
+    const int whole = (int64_t)u1 * 32 > a.K ? u1 - 1 : u1;
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(d, u0 + d);
+    for (int u = u0; u < u1; u += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (u + d == whole) {  // K's end: both rows go on into what follows them
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int left = a.K - 32 * whole - 8 * lk - 4 * h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int i = 0; i < MB; ++i) av[d][h][i][e] = e < left ? av[d][h][i][e] : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) bv[d][h][j][e] = e < left ? bv[d][h][j][e] : 0.0f;
+                    }
+                }
+            }
+            if (u + d < u1) multiply(d);
+            if (u + D < u1) fetch(d, u + d + D);
+        }
+    }
+    // acc[i][j] register r on lane (li, lk): row 16 i + 4 lk + r, column 16 j + li
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) part[wave * (BM * BN) + (16 * i + 4 * lk + r) * BN + 16 * j + li] = acc[i][j][r];
+    __syncthreads();
+    for (int f = tid; f < BM * BN; f += 2 * WK * 64) {
+        const int m = m0 + f / BN, n = n0 + f % BN;
+        if (m >= a.M || n >= a.N) continue;
+        float sum = part[f];
+#pragma unroll
+        for (int i = 1; i < 2 * WK; ++i) sum += part[i * (BM * BN) + f];
+        a.C[0][(int64_t)m * a.ldc[0] + n] = sum;
+    }
+}
+
+template <int MB, int VW>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_back_few(FewArgs a) {
+    constexpr int TILE = 2 * (64 + 128) * 32, PART = 8 * 16 * MB * 16 * VW;
+    __shared__ __attribute__((aligned(16))) float smem[TILE > PART ? TILE : PART];
+    const int block = (int)blockIdx.x;
+    if (block < a.ahead) few_rows_dx<MB, VW>(a.x, block, smem);
+    else gated_tile_of<BACK_W, 64, 128, 32, 32, 32>(a.w, block - a.ahead, smem);
 }
 
 // ---------------------------------------------------------------------------
