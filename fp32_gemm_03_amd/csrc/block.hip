@@ -164,7 +164,7 @@ const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(1, 2, 8, 4), GAT
                              GATED_THIN(2, 2, 8, 2), GATED_THIN(2, 4, 8, 2)};
 struct FewKernel {
     int bm, bn;  // of dx
-    void (*fn)(gatedk::FewArgs);
+    void (*fn)(gatedk::BackArgs);
 };
 #define GATED_BACK_FEW(MB, VW) {16 * MB, 16 * VW, gatedk::gated_back_few<MB, VW>}
 const FewKernel kFew[] = {GATED_BACK_FEW(1, 1), GATED_BACK_FEW(2, 2)};
@@ -254,10 +254,27 @@ const FewKernel *choose_few(const gatedk::TileArgs &x) {
     return nullptr;
 }
 
-int launch_few(const FewKernel &k, gatedk::FewArgs a, hipStream_t stream) {
+int launch_few(const FewKernel &k, gatedk::BackArgs a, hipStream_t stream) {
     a.x.xcd_shift = a.w.xcd_shift = xcd_shift();
     a.ahead = (int)(ceil_div(ceil_div(a.x.M, k.bm) * ceil_div(a.x.N, k.bn), 8) * 8);
     return enqueue(k.fn, a.ahead + tiles(kBackW[0], a.w, gatedk::BACK_W), kBackW[0].threads, a, stream);
+}
+
+// In one launch too where dx has a 128 x 64 tile for nearly every CU, unless the tiles of 256 x
+// 256 fill the chip.  Measured (us, T x N x K; one launch, one after the other): 2000 x 2048 x
+// 1024 262, 275; 2000 x 1000 x 1000 135, 149; 1000 x 2048 x 1024, 128 tiles, 207, 144.
+bool back_in_one(const gatedk::BackArgs &a) {
+    return reachable(a.x) && ceil_div(a.x.M, 128) * ceil_div(a.x.N, 64) >= 224 &&
+           tiles(kBackX, a.x, gatedk::BACK_X) < 224 && &choose_back_w(a.w) == &kBackW[0];
+}
+
+int launch_back_in_one(gatedk::BackArgs a, hipStream_t stream) {
+    a.x.xcd_shift = a.w.xcd_shift = xcd_shift();
+    const long long dx = ceil_div(a.x.M, 128) * ceil_div(a.x.N, 64);
+    const long long dw = ceil_div(a.w.M, 128) * ceil_div(a.w.N, 64) * 2;
+    if (dx > INT_MAX) return SGEMM_ERR_TOO_LARGE;
+    a.ahead = (int)dx;
+    return enqueue(gatedk::gated_back_tiles, dx + dw, 512, a, stream);
 }
 
 // Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors
@@ -521,7 +538,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
                                ceil_div(s.units, 4), 256, s, stream);
         if (rc != SGEMM_OK) return rc;
     }
-    gatedk::FewArgs a = {};
+    gatedk::BackArgs a = {};
     a.x.M = T;
     a.x.N = K;
     a.x.K = N;
@@ -550,6 +567,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     if (to_x && to_w && N > 0 && reachable(a.w)) {
         const FewKernel *few = choose_few(a.x);
         if (few != nullptr) return launch_few(*few, a, stream);
+        if (back_in_one(a)) return launch_back_in_one(a, stream);
     }
     if (to_x) {
         const int rc = gated_back_x(a.x, stream);

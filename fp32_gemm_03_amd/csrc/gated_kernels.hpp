@@ -465,9 +465,9 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 //   workgroups as well: 29 rows, 2048 x 1024, 19.5 us with the launch that adds them up, 22.0
 //   without; 1 x 4096 x 2048 36.8 against 34.7; not kept).
 // ---------------------------------------------------------------------------
-struct FewArgs {
+struct BackArgs {
     TileArgs x, w;  // of BACK_X and BACK_W
-    int ahead;      // workgroups of dx, a multiple of 8: the others keep their XCDs
+    int ahead;      // workgroups of dx (few rows: a multiple of 8, so that the others keep their XCDs)
 };
 
 template <int MB, int VW> __device__ __forceinline__ void few_rows_dx(const TileArgs &a, int block, float *part) {
@@ -564,12 +564,21 @@ template <int MB, int VW> __device__ __forceinline__ void few_rows_dx(const Tile
 }
 
 template <int MB, int VW>
-__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_back_few(FewArgs a) {
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_back_few(BackArgs a) {
     constexpr int TILE = 2 * (64 + 128) * 32, PART = 8 * 16 * MB * 16 * VW;
     __shared__ __attribute__((aligned(16))) float smem[TILE > PART ? TILE : PART];
     const int block = (int)blockIdx.x;
     if (block < a.ahead) few_rows_dx<MB, VW>(a.x, block, smem);
     else gated_tile_of<BACK_W, 64, 128, 32, 32, 32>(a.w, block - a.ahead, smem);
+}
+
+// Both gradients of many rows in one launch, dx's tiles ahead: a sum of 2 N products keeps a
+// CU for longer than one of T, and a CU holds three workgroups.
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_back_tiles(BackArgs a) {
+    __shared__ __attribute__((aligned(16))) float smem[2 * (128 + 64) * 32];
+    const int block = (int)blockIdx.x;
+    if (block < a.ahead) gated_tile_of<BACK_X, 128, 64, 32, 32, 32>(a.x, block, smem);
+    else gated_tile_of<BACK_W, 128, 64, 32, 32, 32>(a.w, block - a.ahead, smem);
 }
 
 // ---------------------------------------------------------------------------

@@ -305,7 +305,11 @@ template <int NT, int V, int ACT> __global__ void __launch_bounds__(NT == 64 ? 2
 #pragma unroll
         for (int c = 0; c < V; ++c) g[c] = row4(rg, 4 * (c * NT + tid));
 #pragma unroll
-        for (int c = 0; c < V; ++c) v[c] = gated64<ACT>(g[c], v[c]);
+        for (int c = 0; c < V; ++c) {
+            // (a wave wholly beyond the row has nothing to compute: 515 x 2816, 8 waves of two
+            // vectors, 6.9 us with that and 6.0 without)
+            if (c == 0 || __builtin_amdgcn_readfirstlane(4 * (c * NT + tid)) < a.N) v[c] = gated64<ACT>(g[c], v[c]);
+        }
     }
     int most = 0;  // (what lies beyond the row is read as 0, and act(0) 0 is 0)
 #pragma unroll

@@ -200,3 +200,16 @@ def test_gated_grad_against_differences(kind):
         for at in np.ndindex(*v.shape):
             near = _difference(lambda w: loss(*[w if j == i else o for j, o in enumerate((x, G, U))]), v, at, 1e-5)
             assert abs(near - grads[i][at]) < 1e-7
+
+
+def test_block_kernels_use_no_scratch():
+    """Their kernels too keep their state in registers and LDS (see the library's own such test)."""
+    from fp32_gemm_03_amd import build as b
+    try:
+        resources = b.kernel_resources(source=2)
+    except (RuntimeError, OSError) as e:
+        pytest.skip(f"cannot read the code object: {e}")
+    assert len(resources) > 40
+    for name, r in resources.items():
+        assert r["private_segment_fixed_size"] == 0 and r["vgpr_spill_count"] == 0, name
+        assert 0 <= r["group_segment_fixed_size"] <= 160 * 1024, name
