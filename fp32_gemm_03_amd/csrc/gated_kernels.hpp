@@ -174,13 +174,19 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
         rowk::meet();
     };
 
-    floatx16 acc[MI][NI];
+    // With one block a wave, odd k-steps have a sum of their own: MFMAs that add to one sum wait
+    // for each other, and two shorter sums are nearer to 64 bits.
+    constexpr int SUMS = MI * NI == 1 ? 2 : 1;
+    floatx16 sums[SUMS][MI][NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int c = 0; c < SUMS; ++c)
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sums[c][i][j][r] = 0.0f;
+    floatx16(&acc)[MI][NI] = sums[0];
 
     // A chunk is four k-steps: q of BK / 8, lane half lh its own
     constexpr int QN = BK / 8;
@@ -244,7 +250,8 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(av[q & 1][i][e], bv[q & 1][j][e], acc[i][j], 0, 0, 0);
+                    floatx16 &sum = sums[e % SUMS][i][j];
+                    sum = __builtin_amdgcn_mfma_f32_32x32x2f32(av[q & 1][i][e], bv[q & 1][j][e], sum, 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                     between((e * MI + i) * NI + j);
                 }
@@ -277,6 +284,10 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
             });
         }
         rowk::wait_loads<0>();
+        if constexpr (SUMS == 2) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[0][0][r] += sums[1][0][0][r];
+        }
     }
 
     // Register r of block (i, j) on lane (li, lh): block row 8 (r / 4) + 4 lh + r % 4 = b
