@@ -111,7 +111,7 @@ const I8Kernel kI8Thin1 = I8_THIN(1, 1, 8, 4);
 const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 2);
 const I8Kernel kI8Thin4 = I8_THIN(4, 1, 8, 2);
 const I8Kernel kI8Thin42 = I8_THIN(4, 2, 8, 2);
-const I8Kernel kI8Simple = {32, 32, 256, i8k::i8_simple};
+const I8Kernel kI8Any = {64, 64, 256, i8k::i8_any};
 
 long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ceil_div(N, k.bn); }
 
@@ -133,7 +133,7 @@ const I8Kernel &choose_i8(const i8k::Args &a) {
     // first row
     const bool words = ((uintptr_t)a.A & 3) == 0 && ((uintptr_t)a.B & 3) == 0 && a.lda % 4 == 0 && a.ldb % 4 == 0;
     constexpr int64_t reach = (1LL << 31) / 256 - 1024;
-    if (!words || a.lda > reach || a.ldb > reach || a.ldc > reach / 4) return kI8Simple;
+    if (!words || a.lda > reach || a.ldb > reach || a.ldc > reach / 4) return kI8Any;
     if (a.M <= 16) return kI8Thin1;
     if (a.M <= 32) return kI8Thin2;
     if (a.M <= 64) return kI8Thin4;

@@ -614,7 +614,8 @@ int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const 
  * the sum exact, the rest in 64 bits and rounded once.  Scales NULL: all 1.
  * beta == 0 does not read C; alpha == 0 or K == 0 read neither A, B nor the scales
  * (C = beta * C).  A and B 4-byte aligned with leading dimensions that are
- * multiples of 4 below 2^23 take the fast kernels; others are slow. */
+ * multiples of 4 below 2^23 take the fast kernels (which read whole words: a row's
+ * last one, where K ends inside it); others take 1.5 to 4 times as long. */
 int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, const float *a_scales,
              const signed char *B, int ldb, const float *b_scales, float beta, float *C, int ldc, hipStream_t stream);
 
