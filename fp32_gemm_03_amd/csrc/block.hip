@@ -100,13 +100,13 @@ struct I8Kernel {
     int bm, bn, threads;
     void (*fn)(i8k::Args);
 };
-#define I8_TILE(BM, BN, BK, WM, WN, STG, AHEAD, WPE) \
-    {BM, BN, (BM / WM) * (BN / WN) * 64, i8k::i8_tile<BM, BN, BK, WM, WN, STG, AHEAD, WPE>}
+#define I8_TILE(BM, BN, BK, WM, WN, KG, WPE) \
+    {BM, BN, KG * (BM / WM) * (BN / WN) * 64, i8k::i8_tile<BM, BN, BK, WM, WN, KG, 2, 1, WPE>}
 #define I8_THIN(MB, NB, WK, WPE) {16 * MB, 16 * NB, WK * 64, i8k::i8_thin<MB, NB, WK, WPE>}
-const I8Kernel kI8Large = I8_TILE(256, 256, 128, 64, 64, 2, 1, 4);  // 16 waves, one workgroup per CU
-const I8Kernel kI8Mid = I8_TILE(128, 128, 128, 32, 64, 2, 1, 4);    // 8 waves, two per CU
-const I8Kernel kI8Lone = I8_TILE(128, 128, 256, 32, 64, 2, 1, 2);   // 8 waves, one per CU
-const I8Kernel kI8Small = I8_TILE(64, 64, 256, 32, 32, 2, 3, 2);    // 4 waves, two per CU
+const I8Kernel kI8Large = I8_TILE(256, 256, 128, 64, 64, 1, 4);  // 16 waves, one workgroup per CU
+const I8Kernel kI8Mid = I8_TILE(128, 128, 128, 32, 64, 1, 4);    // 8 waves, two per CU
+const I8Kernel kI8Lone = I8_TILE(128, 128, 256, 32, 64, 1, 2);   // 8 waves, one per CU
+const I8Kernel kI8Small = I8_TILE(64, 64, 256, 32, 32, 2, 4);    // 8 waves in two groups, two per CU
 const I8Kernel kI8Thin1 = I8_THIN(1, 1, 8, 4);
 const I8Kernel kI8Thin2 = I8_THIN(2, 1, 8, 2);
 const I8Kernel kI8Thin4 = I8_THIN(4, 1, 8, 2);
@@ -118,7 +118,8 @@ long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ce
 // Measured (us, N = K = 4096, A from memory; thin: 16, 32 and 64 rows):
 //   rows           1    8   37*  64  100  200  1024  2048  4096      (* 4096 x 2048)
 //   thin          5.2  5.7  6.1 12.0 18.4 33.4   145
-//   64 x 64      12.5 12.5  8.0 12.6 12.7 16.3  33.3  64.5   127
+//   64 x 64      12.5 12.5  8.0 12.6 12.7 16.3  33.3  64.5   127  (one group of 4 waves;
+//     two groups, B from memory too: 100 rows 16.3 against 17.8, 515 x 1024 x 2816 12.6 against 13.4)
 //   128 x 128    21.5 21.4 13.2 21.6 21.6 28.9  31.8  40.9    80
 //     256 of K   18.4 18.2 11.6 18.3 18.2 22.4  25.9  53.1   104
 //   256 x 256    46.3 46.2 28.6 46.3 46.6 50.6  51.7  54.0    73

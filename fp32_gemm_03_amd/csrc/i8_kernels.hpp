@@ -62,7 +62,9 @@ __device__ __forceinline__ intx4 first_bytes(intx4 v, int left) {
 // ends a K tile waits for the next one only.  A row of a stage is BK / 16 chunks of 16 bytes, permuted
 // (AKLayout) so that a load instruction (whole rows) and a fragment read (one chunk
 // of each of 16 consecutive rows) both touch every bank.  A wave sums a WM x WN tile
-// with v_mfma_i32_32x32x32_i8; lane half lh takes chunks lh BK / 32 + s.
+// with v_mfma_i32_32x32x32_i8; lane half lh takes chunks lh BK / 32 + s.  KG 2: two
+// groups of waves take half of a K tile's steps each, for small tiles, whose loads then
+// come from twice as many waves; the second group's sums go through LDS.
 // ---------------------------------------------------------------------------
 template <int ROWS, int BK, int NT> struct Stage {
     static constexpr int WAVES = NT / 64, CPR = BK / 16;
@@ -97,16 +99,18 @@ template <int ROWS, int BK, int NT> struct Stage {
     }
 };
 
-template <int BM, int BN, int BK, int WM, int WN, int STG, int AHEAD, int WPE>
-__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+template <int BM, int BN, int BK, int WM, int WN, int KG, int STG, int AHEAD, int WPE>
+__global__ void __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
 i8_tile(Args a) {
-    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
-    constexpr int STAGE = (BM + BN) * BK, STEPS = BK / 32;
+    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, WPG = (BM / WM) * WAVES_N, NT = KG * WPG * 64;
+    constexpr int STAGE = (BM + BN) * BK, STEPS = BK / 32 / KG;
+    static_assert(KG == 1 || KG == 2, "wave groups");
+    static_assert(KG == 1 || STG * STAGE >= BM * BN * 4, "the second group's sums");
     __shared__ __attribute__((aligned(16))) char smem[STG * STAGE];
     __shared__ __attribute__((aligned(16))) float scale[BM + BN];  // alpha's product comes later
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 31, lh = lane >> 5;
-    const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
+    const int group = wave / WPG, wm = wave % WPG / WAVES_N * WM, wn = wave % WAVES_N * WN;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
     int tm, tn;
     sgk::tile_of<2, 8>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
@@ -135,7 +139,8 @@ i8_tile(Args a) {
     const int a_row = (wm + li) * BK, b_row = BM * BK + (wn + li) * BK;
     int at[STEPS];  // (wm, wn and 32 i are multiples of 16 rows: one permutation)
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) at[s] = 16 * sgk::AKLayout<BK / 4>::chunk_pos(li, lh * STEPS + s);
+    for (int s = 0; s < STEPS; ++s)
+        at[s] = 16 * sgk::AKLayout<BK / 4>::chunk_pos(li, lh * (BK / 32) + group * STEPS + s);
 
     constexpr int DP = SA::P + SB::P;
     auto fetch = [&](char *st, int k0) {  // (past K nothing is read)
@@ -211,7 +216,25 @@ i8_tile(Args a) {
             }
         }
         wait_loads<0>();
+        if constexpr (KG == 2) {
+            meet();  // (every wave is past its last reads, every load has landed)
+            intx4 *part = reinterpret_cast<intx4 *>(smem) + wave % WPG * (MI * NI * 4 * 64) + lane;
+#pragma unroll
+            for (int v = 0; v < MI * NI * 4; ++v) {
+                intx16 &of = acc[v / 4 / NI][v / 4 % NI];
+                if (group == 1) part[64 * v] = intx4{of[v % 4 * 4], of[v % 4 * 4 + 1], of[v % 4 * 4 + 2], of[v % 4 * 4 + 3]};
+            }
+            __syncthreads();
+            if (group == 1) return;
+#pragma unroll
+            for (int v = 0; v < MI * NI * 4; ++v) {
+                const intx4 u = part[64 * v];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[v / 4 / NI][v / 4 % NI][v % 4 * 4 + r] += u[r];
+            }
+        }
     }
+    if (KG == 2 && group == 1) return;
 
     // acc[i][j] register r on lane (li, lh): row 32 i + 8 (r / 4) + 4 lh + r % 4, column
     // 32 j + li.  C through a descriptor from the tile's first element to the last one:
