@@ -235,7 +235,7 @@ int launch_gated(const GatedKernel &k, int kind, gatedk::TileArgs a, hipStream_t
 
 // dx = dgate G^T + dup U^T: in one sum on 256 x 256 tiles where they fill the chip, else one
 // product after the other on the kernels of sgemm_grouped().  Measured (us, T x N x K): 29 x
-// 2048 x 1024 16 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 56 (98), 2000 x 2048 x 1024
+// 2048 x 1024 19 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 50 (98), 2000 x 2048 x 1024
 // 150 (128 x 64 tiles: 151).
 int gated_back_x(const gatedk::TileArgs &a, hipStream_t stream) {
     if (reachable(a) && tiles(kBackX, a, gatedk::BACK_X) >= 224) return launch_gated(kBackX, gatedk::BACK_X, a, stream);

@@ -65,6 +65,9 @@ __device__ __forceinline__ intx4 first_bytes(intx4 v, int left) {
 // with v_mfma_i32_32x32x32_i8; lane half lh takes chunks lh BK / 32 + s.  KG 2: two
 // groups of waves take half of a K tile's steps each, for small tiles, whose loads then
 // come from twice as many waves; the second group's sums go through LDS.
+// 4096 x 4096 x 4096: 73 us, 1.88 POPS (8192: 495, 2.2): the matrix cores are busy for 52% at a clock that
+// power sets, a CU's loads of a K tile (64 KiB) take 0.95 us beside 1.04 of products, and C's
+// stores 14 at the end, when every workgroup stores at once.
 // ---------------------------------------------------------------------------
 template <int ROWS, int BK, int NT> struct Stage {
     static constexpr int WAVES = NT / 64, CPR = BK / 16;
@@ -287,7 +290,8 @@ i8_tile(Args a) {
 // Few rows: reading B once is the work, so 16 MB rows and 16 NB channels a
 // workgroup, its WK waves each a share of K, both operands straight from memory to
 // v_mfma_i32_16x16x64_i8, the partial sums added through LDS.  A step is 128 bytes
-// of K: a lane takes 32 of them of its row, so that whole lines are read.
+// of K: a lane takes 32 of them of its row, so that whole lines are read.  1 x 4096 x 4096, 17
+// MB, 5.5 us, of which a launch alone is 2.2.
 // ---------------------------------------------------------------------------
 template <int MB, int NB, int WK, int WPE>
 __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) i8_thin(Args a) {

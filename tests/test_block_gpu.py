@@ -102,8 +102,6 @@ def test_norm(T, N, residual):
     S, Y = floats(T, N, ld=N + 2), floats(T, N, ld=N + 5)
     Q, scales = Bytes(np.full((T, N), 3), N + 1), floats(T)
     for outputs in ((True, True, True), (True, False, True), (False, True, False), (False, False, True)):
-        for b in (S, Y, Q, scales):
-            b.owner.copy_(torch.where(torch.isnan(b.owner), b.owner, b.owner) if b is not Q else b.owner)
         s, y, q = outputs
         g.sgemm_norm(T, N, X.ptr, X.ld, R.ptr if residual else None, R.ld if residual else N, W.ptr if W else None, eps,
                      S.ptr if s else None, S.ld, Y.ptr if y else None, Y.ld, Q.ptr if q else None, Q.ld,
