@@ -17,11 +17,13 @@ namespace {
 #define NEED(position, condition) \
     if (!(condition)) return SGEMM_ERR_ARGUMENT - (position)
 
+// a launch holds fewer than 2^32 threads
+bool fits(long long grid, int threads) { return grid <= INT_MAX && grid * threads < (1LL << 32); }
+
 template <class A>
 int enqueue(void (*kernel)(A), long long grid, int threads, const A &args, hipStream_t stream) {
     if (grid <= 0) return SGEMM_OK;
-    // a launch holds fewer than 2^32 threads
-    if (grid > INT_MAX || grid * threads >= (1LL << 32)) return SGEMM_ERR_TOO_LARGE;
+    if (!fits(grid, threads)) return SGEMM_ERR_TOO_LARGE;
     (void)hipGetLastError();  // drop any stale error so the code below is this launch's
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, stream, args);
     return (int)hipGetLastError();
@@ -347,7 +349,9 @@ int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, 
     NEED(14, aligned4(dweight));
     if (N == 0 || (dh == nullptr && dweight == nullptr)) return SGEMM_OK;
     if (dweight != nullptr && !workspace_ok(workspace, workspace_bytes, norm_grad_bytes(T, N))) return SGEMM_ERR_WORKSPACE;
-    if (T > kLongest || N > kLongest) return SGEMM_ERR_TOO_LARGE;
+    const long long sums = ceil_div(N, normk::kShareColumns);
+    constexpr int sum_threads = normk::kShareColumns * normk::kShareGroups;
+    if (T > kLongest || N > kLongest || (dweight != nullptr && !fits(sums, sum_threads))) return SGEMM_ERR_TOO_LARGE;
     normk::NormGradArgs a;
     a.T = T;
     a.N = N;
@@ -369,8 +373,7 @@ int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, 
     const int rc = k == nullptr ? enqueue(normk::norm_grad_long, a.P, normk::kLongThreads, a, stream)
                                 : enqueue(k->fn, a.P, k->threads, a, stream);
     if (rc != SGEMM_OK || dweight == nullptr) return rc;
-    return enqueue(normk::norm_weight_grad, ceil_div(N, normk::kShareColumns), normk::kShareColumns * normk::kShareGroups,
-                   a, stream);
+    return enqueue(normk::norm_weight_grad, sums, sum_threads, a, stream);
 }
 
 int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const float *gate, int ldg, signed char *q,
@@ -518,27 +521,6 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     const int64_t ldz = slope_ld(at_least_1(N));  // (a leading dimension, also of no columns)
     float *dgate = static_cast<float *>(workspace);
     float *dup = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up((size_t)T * ldz * 4));
-    if (slopes) {
-        gatedk::SlopeArgs s;
-        s.T = T;
-        s.N = N;
-        s.gate = gate;
-        s.up = up;
-        s.dy = dy;
-        s.ldgate = ldgate;
-        s.ldup = ldup;
-        s.lddy = lddy;
-        s.ldz = ldz;
-        s.dgate = dgate;
-        s.dup = dup;
-        s.chunks = (int)ceil_div(ldz, 256);
-        s.units = (int64_t)T * s.chunks;
-        const int rc = enqueue(activation == SGEMM_ACT_SILU   ? gatedk::gated_slopes<normk::kSilu>
-                               : activation == SGEMM_ACT_GELU ? gatedk::gated_slopes<normk::kGelu>
-                                                              : gatedk::gated_slopes<normk::kGeluTanh>,
-                               ceil_div(s.units, 4), 256, s, stream);
-        if (rc != SGEMM_OK) return rc;
-    }
     gatedk::BackArgs a = {};
     a.x.M = T;
     a.x.N = K;
@@ -565,6 +547,30 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     a.w.C[1] = dU;
     a.w.ldc[0] = lddg;
     a.w.ldc[1] = lddu;
+    // (before the first launch)
+    const GatedKernel &weights = reachable(a.w) ? choose_back_w(a.w) : kSimpleBackW;
+    if (to_w && !fits(tiles(weights, a.w, gatedk::BACK_W), weights.threads)) return SGEMM_ERR_TOO_LARGE;
+    if (slopes) {
+        gatedk::SlopeArgs s;
+        s.T = T;
+        s.N = N;
+        s.gate = gate;
+        s.up = up;
+        s.dy = dy;
+        s.ldgate = ldgate;
+        s.ldup = ldup;
+        s.lddy = lddy;
+        s.ldz = ldz;
+        s.dgate = dgate;
+        s.dup = dup;
+        s.chunks = (int)ceil_div(ldz, 256);
+        s.units = (int64_t)T * s.chunks;
+        const int rc = enqueue(activation == SGEMM_ACT_SILU   ? gatedk::gated_slopes<normk::kSilu>
+                               : activation == SGEMM_ACT_GELU ? gatedk::gated_slopes<normk::kGelu>
+                                                              : gatedk::gated_slopes<normk::kGeluTanh>,
+                               ceil_div(s.units, 4), 256, s, stream);
+        if (rc != SGEMM_OK) return rc;
+    }
     if (to_x && to_w && N > 0 && reachable(a.w)) {
         const FewKernel *few = choose_few(a.x);
         if (few != nullptr) return launch_few(*few, a, stream);
@@ -575,7 +581,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
         if (rc != SGEMM_OK) return rc;
     }
     if (to_w && !(T == 0 && beta == 1.0f))
-        return launch_gated(reachable(a.w) ? choose_back_w(a.w) : kSimpleBackW, gatedk::BACK_W, a.w, stream);
+        return launch_gated(weights, gatedk::BACK_W, a.w, stream);
     return SGEMM_OK;
 }
 

@@ -573,7 +573,9 @@ size_t sgemm_adapters_grad_workspace_size(int M, int N, int K, int G, int rank);
  * more of dx); a positive hipError_t; or -(100 + position) for an invalid argument, as above.
  * Checks run before any HIP call, the first bad argument wins, and a leading
  * dimension is checked whether or not its matrix is given; pointers to floats
- * have to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed. */
+ * have to be 4-byte aligned, whatever the sizes.  Sizes of zero are allowed.
+ * Outputs and workspaces overlap neither inputs nor one another, but where a call
+ * says so. */
 #define SGEMM_ACT_SILU 0      /* g / (1 + exp(-g)) */
 #define SGEMM_ACT_GELU 1      /* g (1 + erf(g / sqrt(2))) / 2 */
 #define SGEMM_ACT_GELU_TANH 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
@@ -622,8 +624,7 @@ int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, co
 /* Both projections of a gated block, the activation and the product:
  *   gate = x G,  up = x U,  y = act(gate) * up,
  * x (T x K), G and U (K x N), y (T x N).  gate and up (T x N) are written where
- * they are wanted, for the gradient (both NULL: neither).  No output overlaps an
- * input or another output. */
+ * they are wanted, for the gradient (both NULL: neither). */
 int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg, const float *U,
                 int ldu, float *y, int ldy, float *gate, int ldgate, float *up, int ldup, hipStream_t stream);
 

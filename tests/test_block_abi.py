@@ -106,6 +106,11 @@ def test_sizes_beyond_a_launch_are_refused():
     wide = dict(T=2 ** 30, N=2 ** 30, ldg=2 ** 30, ldu=2 ** 30, ldy=2 ** 30, ldgate=2 ** 30, ldup=2 ** 30)
     assert g.sgemm_gated(*{**GATED, **wide}.values(), stream=0, check=False) == -22
     assert g.sgemm_gated(*{**GATED, "T": BIG}.values(), stream=0, check=False) == -22
+    # the last launch of several is too large: refused before the first
+    wide = dict.fromkeys(("N", "ldh", "lddy", "ldds", "lddh"), 2 ** 26)
+    assert g.sgemm_norm_grad(*{**GRAD, **wide, "workspace_bytes": 1 << 40}.values(), stream=0, check=False) == -22
+    wide = dict.fromkeys([name for name in BACK if name in ("N", "K") or name.startswith("ld")], 2 ** 20)
+    assert g.sgemm_gated_grad(*{**BACK, **wide, "workspace_bytes": 1 << 40}.values(), stream=0, check=False) == -22
 
 
 @pytest.mark.parametrize("fn,base,names", [
