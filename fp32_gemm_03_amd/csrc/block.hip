@@ -5,6 +5,7 @@
 #include "sgemm.h"
 
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "gated_kernels.hpp"
@@ -232,26 +233,16 @@ const GatedKernel &choose_back_w(const gatedk::TileArgs &a) {
 
 int launch_gated(const GatedKernel &k, int kind, gatedk::TileArgs a, hipStream_t stream) {
     a.xcd_shift = xcd_shift();
+    a.shares = 1;
     return enqueue(k.fn, tiles(k, a, kind), k.threads, a, stream);
 }
 
-// dx = dgate G^T + dup U^T: in one sum on 256 x 256 tiles where they fill the chip, else one
-// product after the other on the kernels of sgemm_grouped().  Measured (us, T x N x K): 29 x
-// 2048 x 1024 19 (64 x 64 tiles in one sum: 98), 500 x 2048 x 1024 50 (98), 2000 x 2048 x 1024
-// 150 (128 x 64 tiles: 151).
-int gated_back_x(const gatedk::TileArgs &a, hipStream_t stream) {
-    if (reachable(a) && tiles(kBackX, a, gatedk::BACK_X) >= 224) return launch_gated(kBackX, gatedk::BACK_X, a, stream);
-    const int ldb[2] = {(int)a.ldb[0], (int)a.ldb[1]};
-    return rowk::rows_product_pair(a.M, a.N, a.K, a.A, (int)a.lda, a.B, ldb, a.C[0], (int)a.ldc[0], stream);
-}
-
-// Both gradients in one launch, where dx has no more than a tile of 16 x 16, or of 32 x 32,
-// for each CU.  Measured (us, T x N x K; 16 x 16, 32 x 32, and dx and the weights one after
-// the other): 1 x 2048 x 1024 17.5, 30.8, 24.0; 29 rows 22.0, 35.3, 29.0; 64 rows 25.1, 35.7,
-// 32.3; 130 rows 52.4, 38.9, 67.8; 200 rows 71.4, 51.3, 72.8; 500 rows 157, 96.8, 95.0; 29 x
-// 4096 x 2048 50.7, 68.9, 58.
+// Few rows: both gradients in one launch, where dx has no more than a tile of 16 x 16, or of 32 x
+// 32, for each CU.  Measured (us, T x N x K; 16 x 16, 32 x 32, and shares as below): 1 x 2048 x
+// 1024 17.5, 30.8, 23.6; 29 rows 21.2, 34, 24.5; 64 rows 25, 35, 26.8; 100 rows -, 37, 31.7; 250 rows -,
+// 54, 45.7; 29 x 4096 x 2048 50, 69, 61; 64 rows -, 65, 72; 128 rows -, 107, 87.
 const FewKernel *choose_few(const gatedk::TileArgs &x) {
-    if (!reachable(x)) return nullptr;
+    if (!reachable(x) || x.M > 64) return nullptr;
     for (const FewKernel &k : kFew)
         if (ceil_div(x.M, k.bm) * ceil_div(x.N, k.bn) <= 256) return &k;
     return nullptr;
@@ -259,30 +250,122 @@ const FewKernel *choose_few(const gatedk::TileArgs &x) {
 
 int launch_few(const FewKernel &k, gatedk::BackArgs a, hipStream_t stream) {
     a.x.xcd_shift = a.w.xcd_shift = xcd_shift();
+    a.w.shares = 1;
     a.ahead = (int)(ceil_div(ceil_div(a.x.M, k.bm) * ceil_div(a.x.N, k.bn), 8) * 8);
     return enqueue(k.fn, a.ahead + tiles(kBackW[0], a.w, gatedk::BACK_W), kBackW[0].threads, a, stream);
 }
 
-// In one launch too where dx has a 128 x 64 tile for nearly every CU, unless the tiles of 256 x
-// 256 fill the chip.  Measured (us, T x N x K; one launch, one after the other): 2000 x 2048 x
-// 1024 262, 275; 2000 x 1000 x 1000 135, 149; 1000 x 2048 x 1024, 128 tiles, 207, 144.
-bool back_in_one(const gatedk::BackArgs &a) {
-    return reachable(a.x) && ceil_div(a.x.M, 128) * ceil_div(a.x.N, 64) >= 224 &&
-           tiles(kBackX, a.x, gatedk::BACK_X) < 224 && &choose_back_w(a.w) == &kBackW[0];
+// Shares that the sums of dx and of dG and dU are cut into, of their 128 x 64 tiles in one launch
+// (either may have none).  Priced in K tiles of 32, about a us: a workgroup costs two beside its
+// own, a CU holds three, dx's first, and goes on with what is left; a CU alone with one waits for memory
+// (4 more); adding the shares up is a launch and their bytes.  Measured (us, T x N x K; dx's
+// shares, the chosen one marked): 455 x 2276 x 2069 224 (1), 187 (2), 172* (3), 178 (4), 172 (8); 500 x
+// 2048 x 1024 179 (1), 112 (2), 88 (3), 77* (4), 80 (8); 1000 x 2048 x 1024 207 (1), 145* (2),
+// 144 (4); 2000 x 2048 x 1024 263* (1), 271 (2); 128 x 4096 x 1500 307 (1), 97 (4), 77* (6), 73 (8).
+struct Cut {
+    int x, w;
+};
+constexpr size_t kCutBytes = 32 << 20;  // of shares, at most
+long long whole_vectors(int n) { return ((long long)n + 3) / 4 * 4; }
+size_t cut_bytes(int T, int N, int K, const Cut &c) {
+    return round_up(c.x > 1 ? (size_t)c.x * T * whole_vectors(K) * 4 : 0) +
+           2 * round_up(c.w > 1 ? (size_t)c.w * K * whole_vectors(N) * 4 : 0);
+}
+long long tiles128x64(long long m, long long n) { return ceil_div(m, 128) * ceil_div(n, 64); }
+Cut choose_cut(int T, int N, int K, bool to_x, bool to_w) {
+    const double nx = to_x ? (double)tiles128x64(T, K) : 0.0, nw = to_w ? 2.0 * tiles128x64(K, N) : 0.0;
+    const double lx = 2.0 * ceil_div(N, 32), lw = (double)ceil_div(T, 32);
+    Cut best = {1, 1};
+    double least = 0.0;
+    for (int w = 1; w <= 8 && (w == 1 || (to_w && lw >= 4 * w && nw * w <= 768)); ++w)
+        for (int x = 1; x <= 16 && (x == 1 || (to_x && lx >= 4 * x && nx * x <= 1024)); ++x) {
+            const Cut c = {x, w};
+            const double bytes = (double)cut_bytes(T, N, K, c);
+            if (bytes > (double)kCutBytes) continue;
+            const double bx = to_x ? lx / x + 2 : 0.0, bw = to_w ? lw / w + 2 : 0.0;
+            const double held = fmin(3.0, ceil((nx * x + nw * w) / 256)), dx = fmin(held, ceil(nx * x / 256));
+            const double first = fmax(dx * bx + (held - dx) * bw, fmax(bx, bw)) + (held == 1.0 ? 4 : 0);
+            const double cost = fmax((nx * x * bx + nw * w * bw) / 256, first) + (bytes > 0 ? 2.5 + bytes / 12e6 : 0.0);
+            if ((x == 1 && w == 1) || cost < least) best = c, least = cost;
+        }
+    return best;
 }
 
-int launch_back_in_one(gatedk::BackArgs a, hipStream_t stream) {
+// Tiles of 256 x 256 where they fill the chip: dx in one sum over both halves.
+bool back_x_large(const gatedk::TileArgs &a) { return reachable(a) && tiles(kBackX, a, gatedk::BACK_X) >= 224; }
+
+// dx alone on the kernels of sgemm_grouped(), one product after the other, up to 64 rows, for one
+// round of short sums and where their tiles of 64 x 64 come in nearly whole rounds, else in shares.  Measured (us, T x N x K; products,
+// shares): 1 x 2048 x 1024 13, 18; 64 rows 19, 21; 130 rows 48, 28; 500 rows 50, 46; 1000 rows (256
+// tiles) 73, 80; 128 x 4096 x 2048 89, 47; 455 x 2276 x 2069 (264 tiles) 155, 108; 300 x 600 x 3000
+// (235) 30, 42; 2000 x 200 x 300 16, 19.  Large ones in one sum on 256 x 256 tiles: 4096 x
+// 2048 x 4096 967, 1115 as two products.
+bool back_x_pair(const gatedk::TileArgs &a) {
+    const long long n = ceil_div(a.M, 64) * ceil_div(a.N, 64);
+    return !reachable(a) || a.M <= 64 || (a.K <= 512 && n <= 256) || ceil_div(n, 256) * 256 <= n + n / 4;
+}
+int gated_back_x(const gatedk::TileArgs &a, hipStream_t stream) {
+    if (back_x_large(a)) return launch_gated(kBackX, gatedk::BACK_X, a, stream);
+    const int ldb[2] = {(int)a.ldb[0], (int)a.ldb[1]};
+    return rowk::rows_product_pair(a.M, a.N, a.K, a.A, (int)a.lda, a.B, ldb, a.C[0], (int)a.ldc[0], stream);
+}
+
+gatedk::Shares shares_of(int rows, int cols, int n, float beta, const float *part, float *out, int64_t ldo, int blocks) {
+    gatedk::Shares s = {};
+    s.blocks = blocks;
+    if (n <= 1) return s;
+    s.rows = rows;
+    s.cols = cols;
+    s.shares = n;
+    s.beta = beta;
+    s.part = part;
+    s.ldp = whole_vectors(cols);
+    s.out = out;
+    s.ldo = ldo;
+    s.units = rows * (s.ldp / 4);
+    s.blocks += (int)ceil_div(s.units, 256);  // (kCutBytes / 16 / 256 at most)
+    return s;
+}
+
+int launch_cut(const Cut &c, bool to_x, bool to_w, gatedk::BackArgs a, char *space, hipStream_t stream) {
+    const int T = a.x.M, K = a.x.N, N = a.x.K;
+    float *px = reinterpret_cast<float *>(space);
+    space += c.x > 1 ? round_up((size_t)c.x * T * whole_vectors(K) * 4) : 0;
+    float *pG = reinterpret_cast<float *>(space);
+    space += c.w > 1 ? round_up((size_t)c.w * K * whole_vectors(N) * 4) : 0;
+    float *pU = reinterpret_cast<float *>(space);
+    gatedk::SharesArgs sum;
+    sum.of[0] = shares_of(T, K, to_x ? c.x : 1, 0.0f, px, a.x.C[0], a.x.ldc[0], 0);
+    sum.of[1] = shares_of(K, N, to_w ? c.w : 1, a.w.beta, pG, a.w.C[0], a.w.ldc[0], sum.of[0].blocks);
+    sum.of[2] = shares_of(K, N, to_w ? c.w : 1, a.w.beta, pU, a.w.C[1], a.w.ldc[1], sum.of[1].blocks);
+    a.x.shares = c.x;
+    a.w.shares = c.w;
     a.x.xcd_shift = a.w.xcd_shift = xcd_shift();
-    const long long dx = ceil_div(a.x.M, 128) * ceil_div(a.x.N, 64);
-    const long long dw = ceil_div(a.w.M, 128) * ceil_div(a.w.N, 64) * 2;
+    if (c.x > 1) {
+        a.x.C[0] = a.x.C[1] = px;
+        a.x.ldc[0] = a.x.ldc[1] = whole_vectors(K);
+    }
+    if (c.w > 1) {
+        a.w.C[0] = pG;
+        a.w.C[1] = pU;
+        a.w.ldc[0] = a.w.ldc[1] = whole_vectors(N);
+        a.w.beta = 0.0f;
+    }
+    const long long dx = to_x ? tiles128x64(T, K) * c.x : 0, dw = to_w ? 2 * tiles128x64(K, N) * c.w : 0;
     if (dx > INT_MAX) return SGEMM_ERR_TOO_LARGE;
     a.ahead = (int)dx;
-    return enqueue(gatedk::gated_back_tiles, dx + dw, 512, a, stream);
+    const int rc = enqueue(gatedk::gated_back_tiles, dx + dw, 512, a, stream);
+    return rc != SGEMM_OK ? rc : enqueue(gatedk::gated_sum, sum.of[2].blocks, 256, sum, stream);
 }
 
-// Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors
+// Workspace of the gradient: dgate and dup, rows of N rounded up to whole vectors, and but for few
+// rows the room for shares (the same for all sizes: what is enough for T rows is for fewer)
 int64_t slope_ld(int N) { return ((int64_t)N + 3) / 4 * 4; }
-size_t gated_grad_bytes(int T, int N) { return 2 * round_up((size_t)T * slope_ld(N) * 4); }
+size_t slope_bytes(int T, int N) { return 2 * round_up((size_t)T * slope_ld(N) * 4); }
+size_t gated_grad_bytes(int T, int N, int K) {
+    const bool few = T <= 64 && ceil_div(T, 32) * ceil_div(K, 32) <= 256;
+    return slope_bytes(T, N) + (few ? 0 : kCutBytes);
+}
 
 }  // namespace
 
@@ -485,7 +568,7 @@ int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, co
 }
 
 size_t sgemm_gated_grad_workspace_size(int T, int N, int K) {
-    return T < 0 || N < 0 || K < 0 ? 0 : gated_grad_bytes(T, N);
+    return T < 0 || N < 0 || K < 0 ? 0 : gated_grad_bytes(T, N, K);
 }
 
 int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg,
@@ -516,7 +599,7 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     NEED(21, lddg >= at_least_1(N));
     NEED(22, (dG == nullptr) == (dU == nullptr) && aligned4(dU));
     NEED(23, lddu >= at_least_1(N));
-    if (slopes && !workspace_ok(workspace, workspace_bytes, gated_grad_bytes(T, N))) return SGEMM_ERR_WORKSPACE;
+    if (slopes && !workspace_ok(workspace, workspace_bytes, gated_grad_bytes(T, N, K))) return SGEMM_ERR_WORKSPACE;
     if (T > kLongest || N > kLongest || K > kLongest || (to_x && T >= rowk::kMostRows)) return SGEMM_ERR_TOO_LARGE;
     const int64_t ldz = slope_ld(at_least_1(N));  // (a leading dimension, also of no columns)
     float *dgate = static_cast<float *>(workspace);
@@ -547,9 +630,8 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
     a.w.C[1] = dU;
     a.w.ldc[0] = lddg;
     a.w.ldc[1] = lddu;
-    // (before the first launch)
     const GatedKernel &weights = reachable(a.w) ? choose_back_w(a.w) : kSimpleBackW;
-    if (to_w && !fits(tiles(weights, a.w, gatedk::BACK_W), weights.threads)) return SGEMM_ERR_TOO_LARGE;
+    if (to_w && !fits(tiles(weights, a.w, gatedk::BACK_W), weights.threads)) return SGEMM_ERR_TOO_LARGE;  // (before any launch)
     if (slopes) {
         gatedk::SlopeArgs s;
         s.T = T;
@@ -571,17 +653,24 @@ int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ld
                                ceil_div(s.units, 4), 256, s, stream);
         if (rc != SGEMM_OK) return rc;
     }
-    if (to_x && to_w && N > 0 && reachable(a.w)) {
+    char *room = static_cast<char *>(workspace) + slope_bytes(T, N);
+    const bool tiled = slopes && reachable(a.x) && reachable(a.w);
+    if (tiled && to_x && to_w) {
         const FewKernel *few = choose_few(a.x);
         if (few != nullptr) return launch_few(*few, a, stream);
-        if (back_in_one(a)) return launch_back_in_one(a, stream);
+        if (!back_x_large(a.x) && &weights == &kBackW[0])
+            return launch_cut(choose_cut(T, N, K, true, true), true, true, a, room, stream);
     }
     if (to_x) {
-        const int rc = gated_back_x(a.x, stream);
+        const int rc = tiled && !back_x_large(a.x) && !back_x_pair(a.x)
+                           ? launch_cut(choose_cut(T, N, K, true, false), true, false, a, room, stream)
+                           : gated_back_x(a.x, stream);
         if (rc != SGEMM_OK) return rc;
     }
-    if (to_w && !(T == 0 && beta == 1.0f))
-        return launch_gated(weights, gatedk::BACK_W, a.w, stream);
+    if (to_w && !(T == 0 && beta == 1.0f)) {
+        const Cut c = tiled && &weights == &kBackW[0] ? choose_cut(T, N, K, false, true) : Cut{1, 1};
+        return c.w > 1 ? launch_cut(c, false, true, a, room, stream) : launch_gated(weights, gatedk::BACK_W, a.w, stream);
+    }
     return SGEMM_OK;
 }
 

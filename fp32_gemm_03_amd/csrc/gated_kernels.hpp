@@ -43,6 +43,7 @@ struct TileArgs {
     float *C[2], *gate, *up;  // FORWARD: C[0] is y, gate and up may be NULL
     int64_t ldc[2], ldgate, ldup;
     int xcd_shift;
+    int shares;  // BACK_X, BACK_W: of the sum, share s at C[..] + s M ldc[..]
 };
 
 // ---------------------------------------------------------------------------
@@ -121,8 +122,13 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
     const int li = lane & 31, lh = lane >> 5;
     const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + CN - 1) / CN;
-    int tm, tn;
-    sgk::tile_of<2, 8>(block, nbm, KIND == BACK_W ? 2 * nbn : nbn, a.xcd_shift, tm, tn);
+    int tm, tn, share = 0;
+    const int columns = KIND == BACK_W ? 2 * nbn : nbn;
+    if (KIND != FORWARD && a.shares > 1) {
+        share = block / (nbm * columns);
+        block -= share * (nbm * columns);
+    }
+    sgk::tile_of<2, 8>(block, nbm, columns, a.xcd_shift, tm, tn);
     const int which = KIND == BACK_W && tn >= nbn ? 1 : 0;  // BACK_W: dG's columns, then dU's
     const int bm = tm * BM, bn = (tn - which * nbn) * CN;
 
@@ -134,12 +140,18 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
     if constexpr (KIND != BACK_W) sb2.init(a.ldb[1], wave, lane);
 
     const int KT1 = (a.K + BK - 1) / BK, KT = KIND == BACK_X ? 2 * KT1 : KT1;
+    // the K tiles of this workgroup (BACK_X: of dgate's and then dup's)
+    int T0 = 0, T1 = KT;
+    if (KIND != FORWARD && a.shares > 1) {  // (up to 16 shares of 2^27)
+        T0 = (int)((uint32_t)KT * (uint32_t)share / (uint32_t)a.shares);
+        T1 = (int)((uint32_t)KT * (uint32_t)(share + 1) / (uint32_t)a.shares);
+    }
     // loads of K tile t, piece p: A's, then B's (DUAL: G's, then U's)
     constexpr int DP = SA::P + (DUAL ? 2 : 1) * SB::P;
     auto fetch = [&](float *st, int t, int p) {
         const int seg = KIND == BACK_X && t >= KT1 ? 1 : 0;
         const int64_t k0 = (int64_t)(t - seg * KT1) * BK;
-        const int64_t left = t < KT ? a.K - k0 : 0;  // (past the last tile nothing is read)
+        const int64_t left = t < T1 ? a.K - k0 : 0;  // (past the last tile nothing is read)
         if (p < SA::P) {
             const float *A = a.A[seg];
             const rsrc_t r = A_WIDE ? whole_rsrc(A + k0 * a.lda + bm, left > 0 ? ((left - 1) * a.lda + (a.M - bm)) * 4 : 0)
@@ -169,7 +181,7 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
         rowk::wait_loads<0>();
         if constexpr (KIND != BACK_W) {
             const int left = a.K - (KIND == BACK_X && t >= KT1 ? t - KT1 : t) * BK;
-            if ((a.K & 3) != 0 && t < KT && left > 0 && left < BK) {
+            if ((a.K & 3) != 0 && t < T1 && left > 0 && left < BK) {
                 sa.clear(st, wave, lane, left);
                 if constexpr (B_LONG) sb.clear(st + SA::SIZE, wave, lane, left);
                 __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt 0
@@ -260,18 +272,18 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
                     between((e * MI + i) * NI + j);
                 }
     };
-    if (KT > 0) {
+    if (T0 < T1) {
         // Fragments are read a chunk ahead, across the tiles' borders: a tile's last chunk is
         // multiplied behind the barrier that ends its reads, and the loads of tile t + 2 go
         // between its MFMAs, into the stage that was read.
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int p = 0; p < DP; ++p) fetch(smem + s * STAGE, s, p);
-        landed(smem, 0);
+            for (int p = 0; p < DP; ++p) fetch(smem + s * STAGE, T0 + s, p);
+        landed(smem, T0);
         read(smem, 0);
-        for (int t = 0; t < KT; ++t) {
-            float *st = smem + (t & 1) * STAGE, *next = smem + ((t + 1) & 1) * STAGE;
+        for (int t = T0; t < T1; ++t) {
+            float *st = smem + (t - T0 & 1) * STAGE, *next = smem + (t - T0 + 1 & 1) * STAGE;
 #pragma unroll
             for (int q = 0; q + 1 < QN; ++q) {
                 read(st, q + 1);
@@ -298,6 +310,7 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
     // of the wave's row 32 i + b (A along K) or MI b + i (across); column 32 j + li (B
     // along K), NI li + j (across), NI / 2 li + j / 2 of gate (even j) and up (odd).
     const int W = DUAL ? NI / 2 : NI;
+    float *const C = a.C[which] + (int64_t)share * a.M * a.ldc[which];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -309,7 +322,7 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
             for (int j = 0; j < W; ++j) {
                 const int n = bn + (B_LONG ? wn + 32 * j + li : DUAL ? wn / 2 + W * li + j : wn + W * li + j);
                 if (n >= a.N) continue;
-                float *c = a.C[which] + (int64_t)m * a.ldc[which] + n;
+                float *c = C + (int64_t)m * a.ldc[which] + n;
                 if constexpr (DUAL) {
                     const float g = acc[i][2 * j][r], u = acc[i][2 * j + 1][r];
                     *c = gated(a.act, g, u);
@@ -590,13 +603,49 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) g
 }
 
 // Both gradients of many rows in one launch, dx's tiles ahead: a sum of 2 N products keeps a
-// CU for longer than one of T, and a CU holds three workgroups.  2000 x 2048 x 1024: 262 us, 128
+// CU for longer than one of T, and a CU holds three workgroups.  Where that leaves CUs without work, the
+// sums are cut into shares of K tiles that `gated_sum` adds up.  2000 x 2048 x 1024: 262 us, 128
 // TFLOP/s, the matrix cores busy for 85% of it.
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_back_tiles(BackArgs a) {
     __shared__ __attribute__((aligned(16))) float smem[2 * (128 + 64) * 32];
     const int block = (int)blockIdx.x;
     if (block < a.ahead) gated_tile_of<BACK_X, 128, 64, 32, 32, 32>(a.x, block, smem);
     else gated_tile_of<BACK_W, 128, 64, 32, 32, 32>(a.w, block - a.ahead, smem);
+}
+
+// What was summed in shares: out = beta out + the shares, in order.  A thread four columns.
+struct Shares {
+    int rows, cols, shares;
+    float beta;
+    const float *part;  // rows ldp apart, shares `rows` of them
+    int64_t ldp, ldo, units;
+    float *out;
+    int blocks;  // up to this sum's last one
+};
+struct SharesArgs {
+    Shares of[3];
+};
+__global__ void __launch_bounds__(256) gated_sum(SharesArgs all) {
+    const int block = (int)blockIdx.x, which = block < all.of[0].blocks ? 0 : block < all.of[1].blocks ? 1 : 2;
+    const Shares &a = all.of[which];
+    const int64_t unit = (int64_t)(which > 0 ? block - all.of[which - 1].blocks : block) * 256 + threadIdx.x;
+    if (unit >= a.units) return;
+    const int64_t per = a.ldp / 4, t = unit / per;
+    const int n = 4 * (int)(unit - t * per), left = a.cols - n;  // (ldp: the columns in whole vectors)
+    const float *from = a.part + t * a.ldp + n;
+    f32x4u s = *reinterpret_cast<const f32x4u *>(from);
+    for (int i = 1; i < a.shares; ++i) {
+        const f32x4u v = *reinterpret_cast<const f32x4u *>(from + i * (a.rows * a.ldp));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    float *out = a.out + t * a.ldo + n;
+    if (a.beta != 0.0f) {
+        const f32x4u old = rowk::load4(out, left);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = fmaf(a.beta, old[e], s[e]);
+    }
+    rowk::store4(out, left, s);
 }
 
 // ---------------------------------------------------------------------------

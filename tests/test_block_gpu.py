@@ -335,7 +335,7 @@ def test_i8_scales_and_special_cases():
 GATED = [(1, 1, 1), (1, 100, 333), (5, 17, 3), (16, 64, 128), (17, 33, 65), (29, 300, 515), (33, 20, 31), (64, 130, 100),
          (65, 64, 32), (70, 129, 66), (200, 100, 45), (130, 1000, 129), (600, 700, 64), (1030, 1030, 40), (2050, 2050, 67), (100, 2100, 50), (20, 4700, 40),
          (30, 9300, 30), (4100, 33, 4100),
-         (1900, 70, 1000)]
+         (1900, 70, 1000), (300, 515, 200), (600, 130, 203), (130, 700, 1030), (1100, 40, 515), (261, 2049, 130)]
 
 
 def operands(T, N, K, seed):
@@ -405,11 +405,12 @@ def backward(kind, x, G, U, gate, up, dy, beta, dG0, dU0, pad, parts="both"):
     DX = floats(T, K, ld=K + pad)
     DG, DU = (Buffer(v, N + pad) for v in (dG0, dU0))
     need = g.sgemm_gated_grad_workspace_size(T, N, K)
-    space = torch.full((max(need, 256),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
+    space = torch.full((need + 1024,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
     g.sgemm_gated_grad(T, N, K, kind, X.ptr, X.ld, GB.ptr, GB.ld, UB.ptr, UB.ld, GA.ptr, GA.ld, UP.ptr, UP.ld, DY.ptr,
                        DY.ld, DX.ptr if parts != "weights" else None, DX.ld, beta,
                        DG.ptr if parts != "rows" else None, DG.ld, DU.ptr if parts != "rows" else None, DU.ld, space)
     torch.cuda.synchronize()
+    assert bool((space[need:] == 0xFF).all()), "beyond the workspace"
     return DX.read(), DG.read(), DU.read()
 
 
