@@ -156,13 +156,13 @@ struct GatedKernel {
     int bm, bn, threads;  // columns of the result
     void (*fn)(gatedk::TileArgs);
 };
-#define FORWARD_TILE(BM, BN, BK, WM, WN, WPE) \
-    {BM, BN / 2, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::FORWARD, BM, BN, BK, WM, WN, WPE>}
+#define FORWARD_TILE(BM, BN, BK, WM, WN, KG, WPE) \
+    {BM, BN / 2, KG * (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::FORWARD, BM, BN, BK, WM, WN, KG, WPE>}
 #define BACK_TILE(KIND, BM, BN, BK, WM, WN, WPE) \
-    {BM, BN, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::KIND, BM, BN, BK, WM, WN, WPE>}
+    {BM, BN, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::KIND, BM, BN, BK, WM, WN, 1, WPE>}
 #define GATED_THIN(MB, VW, WK, WPE) {16 * MB, 16 * VW, WK * 64, gatedk::gated_thin<MB, VW, WK, WPE>}
-const GatedKernel kForwardTile[] = {FORWARD_TILE(64, 128, 32, 32, 64, 4), FORWARD_TILE(128, 128, 32, 32, 64, 4),
-                                    FORWARD_TILE(256, 256, 32, 64, 64, 4)};
+const GatedKernel kForwardTile[] = {FORWARD_TILE(64, 128, 32, 32, 64, 1, 4), FORWARD_TILE(128, 128, 32, 32, 64, 1, 4),
+                                    FORWARD_TILE(256, 256, 32, 64, 64, 1, 4), FORWARD_TILE(64, 128, 32, 32, 64, 2, 4)};
 // rows x columns: 16 x 16, 16 x 32, 16 x 64, 32 x 32, 32 x 64
 const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(1, 2, 8, 4), GATED_THIN(1, 4, 8, 4),
                              GATED_THIN(2, 2, 8, 2), GATED_THIN(2, 4, 8, 2)};
@@ -196,7 +196,9 @@ long long tiles(const GatedKernel &k, const gatedk::TileArgs &a, int kind) {
 //   400 x 4096: 165, 141, 167, 158, 142, 136; 700 x 4096: 279, 225, 265, 241, 201, 251;
 //   1000 x 4096: 394, 319, 391, 340, 276, 255; 4096 x 4096: 1049 on 64 x 64, 1000 on 128 x
 //   64, 965 on 256 x 128.
-const GatedKernel &choose_forward(const gatedk::TileArgs &a) {
+// A round of 64 x 64 alone on its CUs has two groups of waves (74, with one 83: 300 x 3000 x 2000 75,
+// 86; 512 x 2048 x 1024 42, 48), beyond one group (1000 x 3001 x 1000 111, with two 118).
+const GatedKernel &choose_forward(const gatedk::TileArgs &a, double &least) {
     if (a.M <= 16) return kThin[a.N <= 4608 ? 0 : a.N <= 9216 ? 1 : 2];
     if (a.M <= 32) return kThin[a.N <= 2304 ? 0 : a.N <= 4608 ? 1 : a.N <= 9216 ? 3 : 4];
     struct Round {
@@ -205,15 +207,40 @@ const GatedKernel &choose_forward(const gatedk::TileArgs &a) {
     };
     const Round rounds[] = {{&kThin[0], 16, 10},         {&kThin[1], 18, 13.2},        {&kThin[2], 27, 20.6},
                             {&kThin[3], 26, 25},         {&kThin[4], 42, 42},          {&kForwardTile[0], 83, 70},
-                            {&kForwardTile[1], 133, 125}, {&kForwardTile[2], 482, 482}};
+                            {&kForwardTile[1], 133, 125}, {&kForwardTile[2], 482, 482}, {&kForwardTile[3], 74, 74}};
     const GatedKernel *best = nullptr;
-    double least = 0.0;
     for (const Round &r : rounds) {
         const long long n = ceil_div(tiles(*r.kernel, a, gatedk::FORWARD), 256);
         const double cost = n <= 1 ? r.alone : r.among * (double)n;
         if (best == nullptr || cost < least) best = r.kernel, least = cost;
     }
     return *best;
+}
+
+// Rows that 64 do not divide: up to a round of tiles of 64 x 64 and the last rows in tiles of 16 x
+// 32 behind them, on CUs that hold one of the others.  Priced as above, and 14 for the end.  Measured (us,
+// T x N x K; so, and one kind of tile): 455 x 2276 x 2069 96, 116; 456 x 2304 x 2048 87, 103.
+bool rest_apart(const gatedk::TileArgs &a, double least) {
+    if (a.M <= 64 || a.M % 64 == 0) return false;
+    const double first = (double)(a.M / 64 * ceil_div(a.N, 64)), rest = (double)(ceil_div(a.M % 64, 16) * ceil_div(a.N, 32));
+    return first <= 256 && fmax((first * 72 + rest * 13.2) / 256, 74.0) + 14 < least;
+}
+int launch_and_rest(gatedk::TileArgs a, hipStream_t stream) {
+    a.xcd_shift = xcd_shift();
+    gatedk::RestArgs r = {a, a, 0};
+    const int rows = a.M / 64 * 64;
+    r.first.M = rows;
+    r.rest.M = a.M - rows;
+    r.rest.A[0] = r.rest.A[1] = a.A[0] + rows * a.lda;
+    r.rest.C[0] = r.rest.C[1] = a.C[0] + rows * a.ldc[0];
+    if (a.gate != nullptr) {
+        r.rest.gate = a.gate + rows * a.ldgate;
+        r.rest.up = a.up + rows * a.ldup;
+    }
+    const long long ahead = ceil_div(rows / 64 * ceil_div(a.N, 64), 8) * 8;
+    if (ahead > INT_MAX) return SGEMM_ERR_TOO_LARGE;
+    r.ahead = (int)ahead;
+    return enqueue(gatedk::gated_and_rest, ahead + ceil_div(r.rest.M, 16) * ceil_div(a.N, 32), 512, r, stream);
 }
 
 // 32-bit offsets from a tile's first row reach all of a tile's operands
@@ -564,7 +591,10 @@ int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, co
     a.up = up;
     a.ldgate = ldgate;
     a.ldup = ldup;
-    return launch_gated(reachable(a) ? choose_forward(a) : kSimpleForward, gatedk::FORWARD, a, stream);
+    if (!reachable(a)) return launch_gated(kSimpleForward, gatedk::FORWARD, a, stream);
+    double cost = 0.0;
+    const GatedKernel &k = choose_forward(a, cost);
+    return rest_apart(a, cost) ? launch_and_rest(a, stream) : launch_gated(k, gatedk::FORWARD, a, stream);
 }
 
 size_t sgemm_gated_grad_workspace_size(int T, int N, int K) {

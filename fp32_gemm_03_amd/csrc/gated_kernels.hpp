@@ -4,6 +4,7 @@
 //   * gated_tile: LDS tiles; one product of x with [G | U] (the activation in the
 //     epilogue), dgate G^T + dup U^T as one sum, or x^T [dgate | dup].
 //   * gated_thin: few rows; operands from memory straight to the matrix cores.
+//   * gated_and_rest: 64-row tiles, the last rows as few.
 //   * gated_slopes: dgate and dup from dy and what the forward kept.
 //   * gated_back_few, gated_back_tiles: dx's tiles and the weights' in one launch.
 //   * gated_simple: any strides.
@@ -103,15 +104,17 @@ template <int COLS, int BK, int NT> struct Wide {
 // Tiles of BM x BN (FORWARD: BN / 2 columns of gate and the same of up), K in tiles
 // of BK, two LDS stages, WM x WN per wave with v_mfma_f32_32x32x2_f32.  Within a K
 // tile lane half lh takes k = lh BK / 2 + j in k-step j, of both operands.
+// KG 2: two groups of waves take half of a K tile's steps each, then add up half of the sums each.
 // FORWARD's wave holds gate and up of the same columns (block columns 2 j and 2 j +
 // 1), so the activation's product is taken in registers.  Bound by the matrix cores, busy
 // for 93% of 4096 x 4096 x 2048 on 256 x 256 tiles (964 us, 142.5 TFLOP/s; sgemm takes 948 for the
 // same work), for 84% of 2000 x 2048 x 1024 on 128 x 128 (134 us): the ring's start and the stores
 // at the end are a larger part of fewer K tiles.
 // ---------------------------------------------------------------------------
-template <int KIND, int BM, int BN, int BK, int WM, int WN>
+template <int KIND, int BM, int BN, int BK, int WM, int WN, int KG = 1>
 __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, float *smem) {
-    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, NT = (BM / WM) * WAVES_N * 64;
+    constexpr int MI = WM / 32, NI = WN / 32, WAVES_N = BN / WN, WPG = (BM / WM) * WAVES_N, NT = KG * WPG * 64;
+    static_assert(KG == 1 || KG == 2, "wave groups");
     constexpr bool DUAL = KIND == FORWARD, A_WIDE = KIND == BACK_W, B_LONG = KIND == BACK_X;
     constexpr int CN = DUAL ? BN / 2 : BN;  // columns of the result
     static_assert(!DUAL || NI % 2 == 0, "gate and up in pairs of block columns");
@@ -120,7 +123,7 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
     constexpr int STAGE = (BM + BN) * BK;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 31, lh = lane >> 5;
-    const int wm = wave / WAVES_N * WM, wn = wave % WAVES_N * WN;
+    const int group = KG == 1 ? 0 : wave / WPG, wm = wave % WPG / WAVES_N * WM, wn = wave % WAVES_N * WN;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + CN - 1) / CN;
     int tm, tn, share = 0;
     const int columns = KIND == BACK_W ? 2 * nbn : nbn;
@@ -204,16 +207,17 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
                 for (int r = 0; r < 16; ++r) sums[c][i][j][r] = 0.0f;
     floatx16(&acc)[MI][NI] = sums[0];
 
-    // A chunk is four k-steps: q of BK / 8, lane half lh its own
-    constexpr int QN = BK / 8;
+    // A chunk is four k-steps: q of BK / 8 / KG, lane half lh and wave group their own
+    constexpr int QN = BK / 8 / KG;
+    static_assert(KG == 1 || QN % 2 == 0, "two sets of fragments");
     int at[QN];  // of a row's chunk (rows wm + 32 i and wn + 32 j + li: one permutation)
     if constexpr (!A_WIDE) {
 #pragma unroll
-        for (int q = 0; q < QN; ++q) at[q] = 4 * sgk::AKLayout<BK>::chunk_pos(li, lh * QN + q);
+        for (int q = 0; q < QN; ++q) at[q] = 4 * sgk::AKLayout<BK>::chunk_pos(li, lh * (BK / 8) + group * QN + q);
     }
-    const int a_at = A_WIDE ? lh * (BK / 2) * BM + wm + MI * li : (wm + li) * BK;
-    const int b_at = SA::SIZE + (B_LONG ? (wn + li) * BK
-                                        : lh * (BK / 2) * CN + (DUAL ? wn / 2 + NI / 2 * li : wn + NI * li));
+    const int k_at = lh * (BK / 2) + group * 4 * QN;  // row of a stage that is across
+    const int a_at = A_WIDE ? k_at * BM + wm + MI * li : (wm + li) * BK;
+    const int b_at = SA::SIZE + (B_LONG ? (wn + li) * BK : k_at * CN + (DUAL ? wn / 2 + NI / 2 * li : wn + NI * li));
 
     float av[2][MI][4], bv[2][NI][4];
     auto read = [&](const float *__restrict__ st, int q) {
@@ -305,6 +309,38 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
             for (int r = 0; r < 16; ++r) acc[0][0][r] += sums[1][0][0][r];
         }
     }
+    if constexpr (KG == 2) {  // each group adds up and stores one half of the registers
+        static_assert(2 * (BM + BN) * BK >= KG * WPG * MI * NI * 8 * 64, "the other group's half");
+        rowk::meet();  // (every wave is past its last reads)
+        floatx4 *part = reinterpret_cast<floatx4 *>(smem) + lane;
+        auto place = [&](int of, int i, int j, int h) { return 64 * (((of * WPG + wave % WPG) * MI * NI + i * NI + j) * 2 + h); };
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        if (g != group) {
+                            const int r = 8 * g + 4 * h;
+                            part[place(g, i, j, h)] = floatx4{acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
+                        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const floatx4 v = part[place(group, i, j, h)];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        if (g == group)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][j][8 * g + 4 * h + e] += v[e];
+                }
+    }
 
     // Register r of block (i, j) on lane (li, lh): block row 8 (r / 4) + 4 lh + r % 4 = b
     // of the wave's row 32 i + b (A along K) or MI b + i (across); column 32 j + li (B
@@ -315,6 +351,7 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+            if (KG == 2 && r / 8 != group) continue;
             const int b = 8 * (r >> 2) + 4 * lh + (r & 3);
             const int m = bm + wm + (A_WIDE ? MI * b + i : 32 * i + b);
             if (m >= a.M) continue;
@@ -337,11 +374,11 @@ __device__ __forceinline__ void gated_tile_of(const TileArgs &a, int block, floa
         }
 }
 
-template <int KIND, int BM, int BN, int BK, int WM, int WN, int WPE>
-__global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
+template <int KIND, int BM, int BN, int BK, int WM, int WN, int KG, int WPE>
+__global__ void __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(WPE)))
 gated_tile(TileArgs a) {
     __shared__ __attribute__((aligned(16))) float smem[2 * (BM + BN) * BK];
-    gated_tile_of<KIND, BM, BN, BK, WM, WN>(a, (int)blockIdx.x, smem);
+    gated_tile_of<KIND, BM, BN, BK, WM, WN, KG>(a, (int)blockIdx.x, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -370,15 +407,15 @@ __device__ __forceinline__ void thin_place(int id, int nbm, int nbn, int xcd_shi
     tn = dealt + c;
 }
 
-template <int MB, int VW, int WK, int WPE>
-__global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) gated_thin(TileArgs a) {
+template <int MB, int VW, int WK>
+__device__ __forceinline__ void gated_thin_of(const TileArgs &a, int block, float *smem) {
     constexpr int BM = 16 * MB, BN = 16 * VW;
-    __shared__ __attribute__((aligned(16))) float part[WK][2][BM * BN];
+    float(*part)[2][BM * BN] = reinterpret_cast<float(*)[2][BM * BN]>(smem);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lk = lane >> 4;
     const int nbm = (a.M + BM - 1) / BM, nbn = (a.N + BN - 1) / BN;
     int tm, tn;
-    thin_place<4>((int)blockIdx.x, nbm, nbn, a.xcd_shift, tm, tn);
+    thin_place<4>(block, nbm, nbn, a.xcd_shift, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const float *A = a.A[0] + (int64_t)m0 * a.lda;
     const int64_t a_bytes = ((int64_t)(a.M - m0 - 1) * a.lda + a.K) * 4;
@@ -483,6 +520,25 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
             a.up[(int64_t)m * a.ldup + n] = u;
         }
     }
+}
+
+template <int MB, int VW, int WK, int WPE>
+__global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WPE))) gated_thin(TileArgs a) {
+    __shared__ __attribute__((aligned(16))) float smem[WK * 2 * 16 * MB * 16 * VW];
+    gated_thin_of<MB, VW, WK>(a, (int)blockIdx.x, smem);
+}
+
+// Rows in whole tiles of 64 x 64 and the last ones in tiles of 16 x 32 behind them.
+struct RestArgs {
+    TileArgs first, rest;
+    int ahead;  // workgroups of the first rows: a multiple of 8, so that the others keep their XCDs
+};
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) gated_and_rest(RestArgs a) {
+    __shared__ __attribute__((aligned(16))) float smem[2 * (64 + 128) * 32];
+    static_assert(8 * 2 * 16 * 32 <= 2 * (64 + 128) * 32, "the partial sums");
+    const int block = (int)blockIdx.x;
+    if (block >= a.ahead) gated_thin_of<1, 2, 8>(a.rest, block - a.ahead, smem);
+    else if (block < a.first.M / 64 * ((a.first.N + 63) / 64)) gated_tile_of<FORWARD, 64, 128, 32, 32, 64, 2>(a.first, block, smem);
 }
 
 // ---------------------------------------------------------------------------

@@ -335,7 +335,8 @@ def test_i8_scales_and_special_cases():
 GATED = [(1, 1, 1), (1, 100, 333), (5, 17, 3), (16, 64, 128), (17, 33, 65), (29, 300, 515), (33, 20, 31), (64, 130, 100),
          (65, 64, 32), (70, 129, 66), (200, 100, 45), (130, 1000, 129), (600, 700, 64), (1030, 1030, 40), (2050, 2050, 67), (100, 2100, 50), (20, 4700, 40),
          (30, 9300, 30), (4100, 33, 4100),
-         (1900, 70, 1000), (300, 515, 200), (600, 130, 203), (130, 700, 1030), (1100, 40, 515), (261, 2049, 130)]
+         (1900, 70, 1000), (300, 515, 200), (600, 130, 203), (130, 700, 1030), (1100, 40, 515), (261, 2049, 130),
+         (320, 2999, 67), (455, 2276, 131), (456, 2304, 32), (257, 4000, 5)]
 
 
 def operands(T, N, K, seed):
