@@ -633,8 +633,9 @@ int sgemm_gated(int T, int N, int K, int activation, const float *x, int ldx, co
  *   dx = dgate G^T + dup U^T,
  *   dG = x^T dgate + beta * dG,  dU = x^T dup + beta * dU.
  * dx, or dG and dU together, may be NULL (not wanted).  beta == 0 reads neither dG
- * nor dU.  Workspace: at least sgemm_gated_grad_workspace_size() bytes, 256-byte
- * aligned, any contents; calls that share one must not overlap in time. */
+ * nor dU.  Workspace: at least sgemm_gated_grad_workspace_size() bytes (what is
+ * enough for T rows is for fewer), 256-byte aligned, any contents; calls that share
+ * one must not overlap in time. */
 int sgemm_gated_grad(int T, int N, int K, int activation, const float *x, int ldx, const float *G, int ldg,
                      const float *U, int ldu, const float *gate, int ldgate, const float *up, int ldup,
                      const float *dy, int lddy, float *dx, int lddx, float beta, float *dG, int lddg, float *dU,

@@ -90,6 +90,9 @@ def test_workspaces_are_refused():
             assert fn(*{**base, **bad}.values(), stream=0, check=False) == -24
     assert g.sgemm_norm_grad_workspace_size(-1, 8) == 0 and g.sgemm_norm_grad_workspace_size(0, 8) == 0
     assert g.sgemm_gated_grad_workspace_size(4, -6, 8) == 0
+    for N, K in ((100, 50), (2048, 1024), (1000, 9000), (6, 8)):  # enough for T rows is enough for fewer
+        sizes = [g.sgemm_gated_grad_workspace_size(T, N, K) for T in range(300)]
+        assert sizes == sorted(sizes)
 
 
 def test_sizes_beyond_a_launch_are_refused():
