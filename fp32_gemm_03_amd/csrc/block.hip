@@ -127,11 +127,20 @@ long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ce
 //     256 of K   18.4 18.2 11.6 18.3 18.2 22.4  25.9  53.1   104
 //   256 x 256    46.3 46.2 28.6 46.3 46.6 50.6  51.7  54.0    73
 // So up to 64 rows thin; then by rounds of tiles (256 CUs; 64 x 64: two on each), each
-// priced by what a full one took: 64 x 64 10, 128 x 128 16 alone on its CU and 12.4
-// among others, 256 x 256 41.  A CU takes in about 40 GB/s however the loads are laid out,
+// priced by what a full one took: 64 x 64 10, 128 x 128 16 alone on its CU and 13.5
+// among others, 256 x 256 48, of which 22 by how full it is (2700 x 3200 x 3328, 143 tiles of 256 x 256: 48
+// us, 550 of 128 x 128: 59).  A CU takes in about 40 GB/s however the loads are laid out,
 // so 64 x 32 thin tiles win where one round of them is enough (100 x 4096 x 4096 14.7 against
 // 17.4 on 64 x 64, 700 x 700 x 5000 16.1 against 23.7; 515 x 1024 x 2816, 288 tiles, 17.9
 // against 13.3).
+// C's stores go past the caches, but for a large C whose rows do not begin on half a line: two
+// stores fill a half there, and come to memory apart.  Measured (us; past the caches, not): 4096 x 4095
+// x 4096 91, 77; 2700 x 3109 x 3298 64, 62; 4096 x 4096 x 4096 74.9, 75.0; 3000 x 6000 x 1000 43.8, 46.2;
+// 1000 x 2001 x 500 (8 MB) 7.9, 8.6.
+bool i8_streams(const i8k::Args &a) {
+    return (a.ldc % 16 == 0 && ((uintptr_t)a.C & 63) == 0) || a.M * (int64_t)a.N < (4 << 20);
+}
+
 const I8Kernel &choose_i8(const i8k::Args &a) {
     // the fast kernels load 16 bytes at 4-byte alignment, at 32-bit offsets from a tile's
     // first row
@@ -143,8 +152,9 @@ const I8Kernel &choose_i8(const i8k::Args &a) {
     if (a.M <= 64) return kI8Thin4;
     const long long mid = tiles(kI8Mid, a.M, a.N);
     const double small = 10.0 * ceil_div(tiles(kI8Small, a.M, a.N), 512);
-    const double middle = mid <= 256 ? 16.0 : 12.4 * ceil_div(mid, 256);
-    const double large = 41.0 * ceil_div(tiles(kI8Large, a.M, a.N), 256);
+    const double middle = mid <= 256 ? 16.0 : 13.5 * ceil_div(mid, 256);
+    const long long big = tiles(kI8Large, a.M, a.N), rounds = ceil_div(big, 256);
+    const double large = 26.0 * rounds + 22.0 * big / 256;
     if (tiles(kI8Thin42, a.M, a.N) <= 256) return kI8Thin42;
     if (small <= middle && small <= large) return kI8Small;
     if (middle <= large) return mid <= 256 ? kI8Lone : kI8Mid;
@@ -549,6 +559,7 @@ int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, co
     a.ldb = ldb;
     a.ldc = ldc;
     a.xcd_shift = xcd_shift();
+    a.stream = i8_streams(a);
     const I8Kernel &k = choose_i8(a);
     return enqueue(k.fn, tiles(k, M, N), k.threads, a, stream);
 }

@@ -32,6 +32,7 @@ struct Args {
     float *C;
     int64_t lda, ldb, ldc;
     int xcd_shift;
+    bool stream;  // C's stores go past the caches (K in tiles of 256, for smaller C: always)
 };
 
 __device__ __forceinline__ double scale_at(const float *s, int64_t i) { return s == nullptr ? 1.0 : (double)s[i]; }
@@ -279,9 +280,11 @@ i8_tile(Args a) {
             for (int r = 0; r < 4; ++r) {
                 const double sr = r == 0 ? s.x : r == 1 ? s.y : r == 2 ? s.z : s.w;
 #pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    sgk::raw_store_f32(scaled(a, acc[i][j][4 * q + r], sr * sb_of[j], old[r][j]), rc, c_at(row + r, j), 0,
-                                       sgk::kCPolStream);
+                for (int j = 0; j < NI; ++j) {
+                    const float v = scaled(a, acc[i][j][4 * q + r], sr * sb_of[j], old[r][j]);
+                    if (BK == 256 || a.stream) sgk::raw_store_f32(v, rc, c_at(row + r, j), 0, sgk::kCPolStream);
+                    else sgk::raw_store_f32(v, rc, c_at(row + r, j), 0, 0);
+                }
             }
         }
 }

@@ -276,7 +276,8 @@ def test_quantize_halves():
 # ---------------------------------------------------------------------------
 I8S = [(1, 1, 1), (1, 64, 128), (1, 500, 1000), (3, 17, 5), (16, 33, 127), (17, 31, 129), (29, 100, 640), (33, 20, 255),
        (64, 130, 300), (65, 64, 64), (100, 90, 130), (130, 260, 257), (200, 1500, 96), (1000, 70, 1025), (600, 3000, 384),
-       (2049, 1793, 145), (4100, 4100, 70), (2, 300, 20011), (70, 40, 131071)]
+       (2049, 1793, 145), (4100, 4100, 70), (2, 300, 20011), (70, 40, 131071),
+       (2050, 2051, 33), (1030, 4093, 40)]
 
 
 @pytest.mark.parametrize("M,N,K", I8S)
