@@ -172,6 +172,27 @@ def test_streams(T, N, K):
         assert all(torch.equal(out[n], want[n]) for n in out), given
 
 
+def test_two_streams_at_once():
+    """Every operator on two streams, a workspace each: the bits that each has alone."""
+    sets = [everything(300, 260, 516, 3), everything(130, 516, 260, 4)]
+    want = []
+    for calls, out, _ in sets:
+        calls()
+        torch.cuda.synchronize()
+        want.append({n: v.clone() for n, v in out.items()})
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _, out, _ in sets:
+        for v in out.values():
+            v.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (calls, _, _), stream in zip(sets, streams):
+            calls(stream)
+    torch.cuda.synchronize()
+    for (_, out, _), w in zip(sets, want):
+        assert all(torch.equal(out[n], w[n]) for n in out)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 64, 256), (40, 520, 132), (300, 260, 516)])
 def test_graphs(T, N, K):
     """Captured once, replayed on new inputs between eager calls of another set that shares nothing."""
