@@ -87,8 +87,10 @@ const RowKernel<normk::NormGradArgs> kNormGrads[] = {
 // Shares that dweight is summed in, a workgroup each.  Measured (us, gradient + sum of the
 // shares): 2011 x 2048 12.6 + 3.8 with 512, 14.5 + 3.3 with 256, 13.0 + 4.7 with 1024; on one
 // wave a row, 4000 x 512, 9.0 + 4.6 with 1024, 12.0 + 3.7 with 512, 8.8 + 6.6 with 2048.
+// Rows too long for registers have half as many, of 64 bits, where they are of more than one row.
+bool long_shares(int T, int N) { return row_kernel(kNormGrads, N) == nullptr && T > 512; }
 int weight_shares(int T, int N) {
-    const int most = N <= 512 ? 1024 : 512;
+    const int most = N <= 512 ? 1024 : long_shares(T, N) ? 256 : 512;
     return T < most ? T : most;
 }
 
@@ -96,7 +98,7 @@ bool workspace_ok(const void *p, size_t have, size_t need) {
     return need == 0 || (p != nullptr && have >= need && ((uintptr_t)p & 255u) == 0);
 }
 
-size_t norm_grad_bytes(int T, int N) { return round_up((size_t)weight_shares(T, N) * N * 4); }
+size_t norm_grad_bytes(int T, int N) { return round_up((size_t)weight_shares(T, N) * N * (long_shares(T, N) ? 8 : 4)); }
 
 // ---- 8-bit products ------------------------------------------------------------
 struct I8Kernel {
@@ -485,15 +487,17 @@ int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, 
     a.ldds = ldds;
     a.lddh = lddh;
     a.dh = dh;
-    a.part = dweight == nullptr ? nullptr : static_cast<float *>(workspace);
+    a.part = dweight == nullptr ? nullptr : workspace;
     a.dweight = dweight;
     a.beta = beta;
-    a.P = weight_shares(T, N);
+    const bool wide = dweight != nullptr && long_shares(T, N);
+    a.P = weight_shares(T, N) * (dweight == nullptr && long_shares(T, N) ? 2 : 1);  // (dh alone: 512 workgroups too)
     const RowKernel<normk::NormGradArgs> *k = row_kernel(kNormGrads, N);
-    const int rc = k == nullptr ? enqueue(normk::norm_grad_long, a.P, normk::kLongThreads, a, stream)
-                                : enqueue(k->fn, a.P, k->threads, a, stream);
+    const int rc = k != nullptr ? enqueue(k->fn, a.P, k->threads, a, stream)
+                                : enqueue(wide ? normk::norm_grad_long_shares : normk::norm_grad_long, a.P,
+                                          normk::kLongThreads, a, stream);
     if (rc != SGEMM_OK || dweight == nullptr) return rc;
-    return enqueue(normk::norm_weight_grad, sums, sum_threads, a, stream);
+    return enqueue(wide ? normk::norm_weight_grad<double> : normk::norm_weight_grad<float>, sums, sum_threads, a, stream);
 }
 
 int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const float *gate, int ldg, signed char *q,

@@ -356,8 +356,8 @@ template <int ACT> __global__ void __launch_bounds__(kLongThreads) quantize_long
 // ---------------------------------------------------------------------------
 // The norm's gradient.  With g = weight dy and r = (mean h^2 + eps)^-1/2:
 //   dh = r (g - h r^2 mean(g h)) + dsum,   dweight_n = sum_t dy h r.
-// A workgroup takes every P-th row and keeps its share of dweight in registers
-// (64 bits); the P shares are added up in order by `norm_weight_grad`.  Bound by HBM:
+// A workgroup takes every P-th row and sums its share of dweight in 64 bits, in registers or,
+// of rows too long for them, in the workspace; the P shares are added up in order by `norm_weight_grad`.  Bound by HBM:
 // 2011 x 2048 with dsum, 66 MB and 4 of shares, 12.6 us, then 3.8 for the shares.
 // ---------------------------------------------------------------------------
 struct NormGradArgs {
@@ -365,7 +365,8 @@ struct NormGradArgs {
     double eps;
     const float *h, *weight, *dy, *dsum;
     int64_t ldh, lddy, ldds, lddh;
-    float *dh, *part, *dweight;
+    float *dh, *dweight;
+    void *part;  // P shares of dweight: float, in norm_grad_long_shares double
     float beta;
 };
 
@@ -426,14 +427,15 @@ template <int NT, int V> __global__ void __launch_bounds__(NT) norm_grad(NormGra
     if (a.part == nullptr) return;
 #pragma unroll
     for (int c = 0; c < V; ++c)
-        put4(a.part + (int64_t)blockIdx.x * a.N, 4 * (c * NT + tid), a.N, f32x4u{(float)dw[c][0], (float)dw[c][1], (float)dw[c][2], (float)dw[c][3]});
+        put4(static_cast<float *>(a.part) + (int64_t)blockIdx.x * a.N, 4 * (c * NT + tid), a.N,
+             f32x4u{(float)dw[c][0], (float)dw[c][1], (float)dw[c][2], (float)dw[c][3]});
 }
 
-// Rows too long for registers: the row is read twice, dweight's share is summed
-// in its place in the workspace (32 bits).
+// Rows too long for registers: a row is read twice.  For dh, and for shares of dweight that
+// are one row each (P >= T).
 __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
     __shared__ double sums[2][kLongThreads / 64];
-    float *part = a.part == nullptr ? nullptr : a.part + (int64_t)blockIdx.x * a.N;
+    float *part = a.part == nullptr ? nullptr : static_cast<float *>(a.part) + (int64_t)blockIdx.x * a.N;
     for (int64_t t = blockIdx.x; t < a.T; t += a.P) {
         const float *h = a.h + t * a.ldh, *d = a.dy + t * a.lddy;
         auto weight = [&](int i) {
@@ -455,12 +457,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
         each(a.N, [&](int i) {
             const int left = a.N - i;
             const f32x4u x = rowk::load4(h + i, left), y = rowk::load4(d + i, left), w = weight(i);
-            f32x4u ds = {0.0f, 0.0f, 0.0f, 0.0f}, p = ds, o;
+            f32x4u ds = {0.0f, 0.0f, 0.0f, 0.0f}, p, o;
             if (a.dsum != nullptr) ds = rowk::load4(a.dsum + t * a.ldds + i, left);
-            if (part != nullptr && t != (int64_t)blockIdx.x) p = rowk::load4(part + i, left);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                p[e] = (float)fma((double)y[e] * r, (double)x[e], (double)p[e]);
+                p[e] = (float)((double)y[e] * r * (double)x[e]);
                 o[e] = norm_back(x[e], y[e], w[e], ds[e], r, k);
             }
             if (part != nullptr) rowk::store4(part + i, left, p);
@@ -469,22 +470,104 @@ __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
     }
 }
 
+// The same with several rows in a share of dweight, which is summed in its place in the
+// workspace, in 64 bits: eight rows at a time, so that a share is read and written once for
+// them, their factors in LDS.  Measured (us, with dh and dsum; so, one row at a time, two, four):
+// 4096 x 16384 327, 413, 347, 316; 2000 x 40003 436, 639, 519, 454; 1100 x 8195 50, 61, 57, 55; 8192 x
+// 12288 459, 597, 500, 437.
+typedef double f64x2u __attribute__((ext_vector_type(2), aligned(8)));
+__device__ __forceinline__ void get_share(const double *p, int left, double (&v)[4]) {
+    if (left >= 4) {
+        const f64x2u a = *reinterpret_cast<const f64x2u *>(p), b = *reinterpret_cast<const f64x2u *>(p + 2);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    } else {
+        if (left > 0) v[0] = p[0];
+        if (left > 1) v[1] = p[1];
+        if (left > 2) v[2] = p[2];
+    }
+}
+__device__ __forceinline__ void put_share(double *p, int left, const double (&v)[4]) {
+    if (left >= 4) {
+        *reinterpret_cast<f64x2u *>(p) = f64x2u{v[0], v[1]};
+        *reinterpret_cast<f64x2u *>(p + 2) = f64x2u{v[2], v[3]};
+    } else {
+        if (left > 0) p[0] = v[0];
+        if (left > 1) p[1] = v[1];
+        if (left > 2) p[2] = v[2];
+    }
+}
+__global__ void __launch_bounds__(kLongThreads) norm_grad_long_shares(NormGradArgs a) {
+    constexpr int ROWS = 8;
+    __shared__ double sums[2][kLongThreads / 64], factors[ROWS][2];
+    double *part = static_cast<double *>(a.part) + (int64_t)blockIdx.x * a.N;
+    auto weight = [&](int i) {
+        return a.weight == nullptr ? f32x4u{1.0f, 1.0f, 1.0f, 1.0f} : rowk::load4(a.weight + i, a.N - i);
+    };
+    for (int64_t t0 = blockIdx.x; t0 < a.T; t0 += (int64_t)ROWS * a.P) {
+        const int64_t there = (a.T - t0 + a.P - 1) / a.P;
+        const int rows = there < ROWS ? (int)there : ROWS;
+        for (int q = 0; q < rows; ++q) {
+            const int64_t t = t0 + (int64_t)q * a.P;
+            const float *h = a.h + t * a.ldh, *d = a.dy + t * a.lddy;
+            double s = 0.0, m = 0.0;
+            each(a.N, [&](int i) {
+                const f32x4u x = rowk::load4(h + i, a.N - i), y = rowk::load4(d + i, a.N - i), w = weight(i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s = fma((double)x[e], (double)x[e], s);
+                    m = fma((double)y[e] * (double)w[e], (double)x[e], m);
+                }
+            });
+            s = over_row<kLongThreads>(s, rowk::Add(), sums[0]);  // (its barriers: the last rows' factors are read)
+            m = over_row<kLongThreads>(m, rowk::Add(), sums[1]);
+            if (threadIdx.x == 0) {
+                const double r = 1.0 / sqrt(s / (double)a.N + a.eps);
+                factors[q][0] = r;
+                factors[q][1] = r * r * (m / (double)a.N);
+            }
+        }
+        __syncthreads();
+        each(a.N, [&](int i) {
+            const int left = a.N - i;
+            const f32x4u w = weight(i);
+            double p[4] = {0.0, 0.0, 0.0, 0.0};
+            if (t0 != (int64_t)blockIdx.x) get_share(part + i, left, p);
+#pragma unroll 2
+            for (int q = 0; q < rows; ++q) {
+                const int64_t t = t0 + (int64_t)q * a.P;
+                const double r = factors[q][0], k = factors[q][1];
+                const f32x4u x = rowk::load4(a.h + t * a.ldh + i, left), y = rowk::load4(a.dy + t * a.lddy + i, left);
+                f32x4u ds = {0.0f, 0.0f, 0.0f, 0.0f}, o;
+                if (a.dsum != nullptr) ds = rowk::load4(a.dsum + t * a.ldds + i, left);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = fma((double)y[e] * r, (double)x[e], p[e]);
+                    o[e] = norm_back(x[e], y[e], w[e], ds[e], r, k);
+                }
+                if (a.dh != nullptr) rowk::store4(a.dh + t * a.lddh + i, left, o);
+            }
+            put_share(part + i, left, p);
+        });
+    }
+}
+
 // dweight = beta dweight + the sum of the P shares.  16 columns a workgroup (a line of
 // each share), its 64 groups of 16 lanes take every 64th share, eight loads in flight;
 // added up in order.
 constexpr int kShareColumns = 16, kShareGroups = 64;
+template <class Share>
 __global__ void __launch_bounds__(kShareColumns * kShareGroups) norm_weight_grad(NormGradArgs a) {
     __shared__ double sums[kShareGroups][kShareColumns];
     const int col = threadIdx.x % kShareColumns, group = threadIdx.x / kShareColumns;
     const int64_t n = (int64_t)blockIdx.x * kShareColumns + col;
     double s = 0.0;
     if (n < a.N) {
-        const float *from = a.part + n;
+        const Share *from = static_cast<const Share *>(a.part) + n;
         for (int p = group; p < a.P; p += 8 * kShareGroups) {
-            float v[8];
+            Share v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = p + i * kShareGroups < a.P ? from[(int64_t)(p + i * kShareGroups) * a.N] : 0.0f;
+                v[i] = p + i * kShareGroups < a.P ? from[(int64_t)(p + i * kShareGroups) * a.N] : Share(0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += (double)v[i];
         }

@@ -597,7 +597,8 @@ int sgemm_norm(int T, int N, const float *x, int ldx, const float *residual, int
  *   dweight = sum over the rows of dy h r, + beta * dweight,
  * h as sgemm_norm() summed it.  dh (the gradient of x and of residual alike) or
  * dweight may be NULL (not wanted); dh may be dy or dsum itself.  beta == 0 does
- * not read dweight.  Workspace, where dweight is wanted: at least
+ * not read dweight.  dweight is summed in 64 bits, in shares that are rounded to 32 at
+ * most once each and added in 64.  Workspace, where dweight is wanted: at least
  * sgemm_norm_grad_workspace_size() bytes, 256-byte aligned, any contents; calls
  * that share one must not overlap in time. */
 int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, float eps, const float *dy, int lddy,
