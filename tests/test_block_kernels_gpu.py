@@ -27,6 +27,47 @@ def _gpu_available():
 
 
 # ---------------------------------------------------------------------------
+# the norm's outputs, each combination by itself
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("T,N", tb.NORMS)
+def test_norm_writes_what_is_asked_for(T, N, residual):
+    """Buffers of their own for every combination of outputs: what is asked for is written, the bits
+    the same in all of them, and what is not is left as it was."""
+    gu.say("norm's outputs", T, N, residual)
+    eps = 1e-5
+    x = stream(T, N, 1)
+    r = stream(T, N, 2, special=False) if residual else None
+    w = (1 + 0.3 * rng_of(12, N).standard_normal(N)).astype(np.float32) if N % 2 else None
+    want_h, want = bo.norm(x, r, w, eps)
+    X, R = Buffer(x, N + 1), Buffer(r, N + 3) if residual else None
+    W = Buffer(w) if w is not None else None
+    first = None
+    for s, y, q in ((True, True, True), (True, True, False), (True, False, True), (False, True, True),
+                    (True, False, False), (False, True, False), (False, False, True)):
+        S, Y, scales = floats(T, N, ld=N + 2), floats(T, N, ld=N + 5), floats(T)
+        Q = Bytes(np.full((T, N), -128), N + 1)  # (no row to 8 bits has a -128)
+        g.sgemm_norm(T, N, X.ptr, X.ld, R.ptr if residual else None, R.ld if residual else N, W.ptr if W else None, eps,
+                     S.ptr if s else None, S.ld, Y.ptr if y else None, Y.ld, Q.ptr if q else None, Q.ld,
+                     scales.ptr if q else None)
+        torch.cuda.synchronize()
+        got = S.read(), Y.read(), Q.read(), scales.read()
+        if first is None:
+            first = got
+            # equal numbers and zeros of the same sign
+            assert np.array_equal(got[0], want_h, equal_nan=True)
+            assert np.array_equal(np.signbit(got[0]) & ~np.isnan(got[0]), np.signbit(want_h) & ~np.isnan(want_h))
+            within(got[1], want, np.abs(want), ONCE, "y")
+            want_q, want_s = bo.quantize(got[1])
+            assert np.array_equal(got[2], want_q) and np.array_equal(got[3], want_s, equal_nan=True)
+        for name, v, all_, asked, left in zip(("sum", "y", "q", "scales"), got, first, (s, y, q, q), (7.0, 7.0, -128, 7.0)):
+            if asked:
+                assert np.array_equal(v.view(np.uint8), all_.view(np.uint8)), (name, s, y, q)
+            else:
+                assert (v == left).all(), (name, "written", s, y, q)
+
+
+# ---------------------------------------------------------------------------
 # dweight of more rows than it has shares
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("N", [300, 8192, 8195, 20003])
