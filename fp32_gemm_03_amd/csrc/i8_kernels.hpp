@@ -46,7 +46,9 @@ __device__ __forceinline__ intx4 load16(rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(intx4, sgk::raw_load_v4f32(r, off, 0, 0));
 }
 // Descriptors are checked by whole 4-byte words: a last word that K fills in part
-// counts as inside (it is aligned, so no page begins in it).
+// counts as inside (it is aligned, so no page begins in it).  They end with a matrix's
+// last row: of the others a load also brings what follows K, padding or the next row.
+// Only A's is cleared; what B brings is multiplied by those zeros.
 __device__ __forceinline__ int words(int bytes) { return (bytes + 3) & ~3; }
 // the first `left` of 16 bytes
 __device__ __forceinline__ intx4 first_bytes(intx4 v, int left) {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(WK * 64) __attribute__((amdgpu_waves_per_eu(WP
 // Rows of any alignment and any leading dimensions: tiles of 64 x 64, 128 bytes of K at a
 // time through registers (loads of 16 bytes at any address; the bytes of a row's end one by
 // one), otherwise as i8_tile.  Measured, rows K bytes apart against 16-byte aligned ones: 1000 x
-// 1000 x 999 12.7 us and 8.5, 4096 x 4096 x 4095 244 and 74, 1 x 4096 x 4095 21 and 4.9.
+// 1000 x 999 13.7 us and 7.6, 4096 x 4096 x 4095 247 and 73, 1 x 4096 x 4095 21 and 4.8.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) i8_any(Args a) {
     constexpr int BM = 64, BK = 128, STAGE = 2 * BM * BK;

@@ -616,9 +616,11 @@ int sgemm_quantize(int T, int N, const float *x, int ldx, int activation, const 
  *   C[m][n] = alpha * a_scales[m] * b_scales[n] * sum_k A[m][k] B[n][k] + beta * C[m][n],
  * the sum exact, the rest in 64 bits and rounded once.  Scales NULL: all 1.
  * beta == 0 does not read C; alpha == 0 or K == 0 read neither A, B nor the scales
- * (C = beta * C).  A and B 4-byte aligned with leading dimensions that are
- * multiples of 4 below 2^23 take the fast kernels (which read whole words: a row's
- * last one, where K ends inside it); others take 1.5 to 4 times as long. */
+ * (C = beta * C).  The fast kernels take A and B that are 4-byte aligned, with leading
+ * dimensions that are multiples of 4 up to 2^23 - 1024, and ldc up to 2^21 - 256; others
+ * take 1.5 to 4.5 times as long.  The fast kernels also read what follows a row's K
+ * numbers: of all rows but a matrix's last up to the bytes of the next rows, of the last
+ * to the end of the 4-byte word that K ends in.  Its values do not matter. */
 int sgemm_i8(int M, int N, int K, float alpha, const signed char *A, int lda, const float *a_scales,
              const signed char *B, int ldb, const float *b_scales, float beta, float *C, int ldc, hipStream_t stream);
 
