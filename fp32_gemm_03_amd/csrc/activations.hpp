@@ -26,14 +26,15 @@ __device__ __forceinline__ double erfc_of(double x) { return erfc(x); }
 __device__ __forceinline__ float size_of(float x) { return fabsf(x); }
 __device__ __forceinline__ double size_of(double x) { return fabs(x); }
 
-
 // exp(x), x <= 0, in 64 bits to 2^-45: 2^k times the series of r = x - k ln 2, |r| <=
-// 0.3466, up to r^11 (the next term is below 2^-47).  Half the instructions of exp(),
-// which with the quotient below set the time of 8-bit rows behind a gate.
+// 0.3466, up to r^11 (the next term is below 2^-47).  ln 2 is taken off in two parts (Cody and
+// Waite): its first 32 bits, whose product with k is exact, and the rest, rounded to 64.  Half
+// the instructions of exp(), which with the quotient below set the time of 8-bit rows behind
+// SiLU and the tanh form.
 __device__ __forceinline__ double exp_below_0(double x) {
     x = x < -800.0 ? -800.0 : x;  // (0 from -745 on; NaN stays)
     const double k = rint(x * 1.4426950408889634);
-    const double r = fma(k, -1.9082149292705877e-10, fma(k, -0.693147180369123816490, x));
+    const double r = fma(k, -0x1.a39ef35793c76p-33, fma(k, -0x1.62e42feep-1, x));
     double p = 1.0 / 39916800.0;
     p = fma(p, r, 1.0 / 3628800.0);
     p = fma(p, r, 1.0 / 362880.0);
