@@ -173,7 +173,7 @@ struct GatedKernel {
 #define BACK_TILE(KIND, BM, BN, BK, WM, WN, WPE) \
     {BM, BN, (BM / WM) * (BN / WN) * 64, gatedk::gated_tile<gatedk::KIND, BM, BN, BK, WM, WN, 1, WPE>}
 #define GATED_THIN(MB, VW, WK, WPE) {16 * MB, 16 * VW, WK * 64, gatedk::gated_thin<MB, VW, WK, WPE>}
-const GatedKernel kForwardTile[] = {FORWARD_TILE(64, 128, 32, 32, 64, 1, 4), FORWARD_TILE(128, 128, 32, 32, 64, 1, 4),
+const GatedKernel kForwardTile[] = {FORWARD_TILE(64, 128, 32, 32, 64, 1, 3), FORWARD_TILE(128, 128, 32, 32, 64, 1, 4),
                                     FORWARD_TILE(256, 256, 32, 64, 64, 1, 4), FORWARD_TILE(64, 128, 32, 32, 64, 2, 4)};
 // rows x columns: 16 x 16, 16 x 32, 16 x 64, 32 x 32, 32 x 64
 const GatedKernel kThin[] = {GATED_THIN(1, 1, 8, 4), GATED_THIN(1, 2, 8, 4), GATED_THIN(1, 4, 8, 4),
