@@ -131,10 +131,12 @@ long long tiles(const I8Kernel &k, int M, int N) { return ceil_div(M, k.bm) * ce
 // So up to 64 rows thin; then by rounds of tiles (256 CUs; 64 x 64: two on each), each
 // priced by what a full one took: 64 x 64 10, 128 x 128 16 alone on its CU and 13.5
 // among others, 256 x 256 48, of which 22 by how full it is (2700 x 3200 x 3328, 143 tiles of 256 x 256: 48
-// us, 550 of 128 x 128: 59).  A CU takes in about 40 GB/s however the loads are laid out,
-// so 64 x 32 thin tiles win where one round of them is enough (100 x 4096 x 4096 14.7 against
-// 17.4 on 64 x 64, 700 x 700 x 5000 16.1 against 23.7; 515 x 1024 x 2816, 288 tiles, 17.9
-// against 13.3).
+// us, 550 of 128 x 128: 59).  The prices are of K = 4096 and hold the start and the stores, which
+// weigh more where K is short; up to 64 rows wide N was not measured.  The thin and the 64 x 64
+// kernels take in about 40 GB/s per CU at these sizes, with the loads that they have in flight (256 x 256
+// takes in 69), so 64 x 32 thin tiles, which take in less, win where one round of them is
+// enough (100 x 4096 x 4096 14.7 against 17.4 on 64 x 64, 700 x 700 x 5000 16.1 against 23.7; 515 x
+// 1024 x 2816, 288 tiles, 17.9 against 13.3).
 // C's stores go past the caches, but for a large C whose rows do not begin on half a line: two
 // stores fill a half there, and come to memory apart.  Measured (us; past the caches, not): 4096 x 4095
 // x 4096 91, 77; 2700 x 3109 x 3298 64, 62; 4096 x 4096 x 4096 74.9, 75.0; 3000 x 6000 x 1000 43.8, 46.2;
@@ -230,8 +232,9 @@ const GatedKernel &choose_forward(const gatedk::TileArgs &a, double &least) {
 }
 
 // Rows that 64 do not divide: up to a round of tiles of 64 x 64 and the last rows in tiles of 16 x
-// 32 behind them, on CUs that hold one of the others.  Priced as above, and 14 for the end.  Measured (us,
-// T x N x K; so, and one kind of tile): 455 x 2276 x 2069 96, 116; 456 x 2304 x 2048 87, 103.
+// 32 behind them, on CUs that hold one of the others.  Priced as above (K = 2048; short K was not
+// measured), and 14 for the end.  Measured (us, T x N x K; so, and one kind of tile): 455 x 2276 x
+// 2069 96, 116; 456 x 2304 x 2048 87, 103.
 bool rest_apart(const gatedk::TileArgs &a, double least) {
     if (a.M <= 64 || a.M % 64 == 0) return false;
     const double first = (double)(a.M / 64 * ceil_div(a.N, 64)), rest = (double)(ceil_div(a.M % 64, 16) * ceil_div(a.N, 32));

@@ -547,9 +547,9 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) g
 //   dx: 16 MB rows and 16 VW columns a workgroup; waves 0 to 3 a share of K each of dgate
 //   G^T, waves 4 to 7 of dup U^T, operands (both along K) from memory straight to
 //   v_mfma_f32_16x16x4_f32; a step is 32 of K, whole lines; partial sums meet in LDS.
-//   A CU takes in 25 to 40 GB/s, which bounds dx where it has few tiles (K split over
-//   workgroups as well: 29 rows, 2048 x 1024, 19.5 us with the launch that adds them up, 22.0
-//   without; 1 x 4096 x 2048 36.8 against 34.7; not kept).
+//   A workgroup takes in 25 to 40 GB/s with the loads that it has in flight, which bounds dx where
+//   it has few tiles (K split over workgroups as well: 29 rows, 2048 x 1024, 19.5 us with the launch
+//   that adds them up, 22.0 without; 1 x 4096 x 2048 36.8 against 34.7; not kept).
 // ---------------------------------------------------------------------------
 struct BackArgs {
     TileArgs x, w;  // of BACK_X and BACK_W

@@ -289,8 +289,9 @@ template <int ACT> __device__ __forceinline__ f32x4u gated64(f32x4u g, f32x4u x)
     return v;
 }
 
-// ACT < 0: no gate.  2047 x 4096: 8.3 us without one (42 MB, 5 TB/s), behind SiLU 17 to 21
-// (75 MB, 4 TB/s), the tanh form 21, GELU 35: the 64-bit exponentials.  A row of 4095 3.3 us.
+// ACT < 0: no gate.  2047 x 4096: 7.7 to 8.3 us without one (42 MB, 5 TB/s), behind SiLU and the
+// tanh form 17 to 21 (75 MB, 4 TB/s; the 64-bit exponential), GELU 30 to 35 (the library's 64-bit
+// erfc).  A row of 4095 3.3 us.
 template <int NT, int V, int ACT> __global__ void __launch_bounds__(NT == 64 ? 256 : NT) quantize(QuantArgs a) {
     constexpr int ROWS = NT == 64 ? 4 : 1;  // a wave each, or one of the workgroup
     __shared__ int mosts[NT / 64 > 0 ? NT / 64 : 1];
