@@ -116,6 +116,37 @@ def test_norm_grad_of_many_long_rows(T, N):
                 first = got
 
 
+def test_norm_grad_of_long_rows_in_a_graph():
+    """Captured on a stream of its own and replayed on other inputs, between eager calls."""
+    T, N = 770, 8195
+    gu.say("norm_grad of long rows in a graph")
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    h, dy = (torch.randn(T, N, generator=gen, device="cuda") for _ in range(2))
+    dh, dw = torch.empty(T, N, device="cuda"), torch.empty(N, device="cuda")
+    space, other = (torch.empty(g.sgemm_norm_grad_workspace_size(T, N), dtype=torch.uint8, device="cuda") for _ in range(2))
+
+    def call(dh, dw, space):
+        g.sgemm_norm_grad(T, N, h, N, None, 1e-5, dy, N, None, N, dh, N, 0.0, dw, space)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(dh, dw, space)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            call(dh, dw, space)
+    torch.cuda.synchronize()
+    want_dh, want_dw = torch.empty_like(dh), torch.empty_like(dw)
+    for turn in range(3):
+        h.mul_(-0.75).add_(0.01 * turn)
+        graph.replay()
+        torch.cuda.synchronize()
+        call(want_dh, want_dw, other)
+        torch.cuda.synchronize()
+        assert torch.equal(dh, want_dh) and torch.equal(dw, want_dw), turn
+        space.fill_(0xFF)
+        dw.zero_()
+
+
 # ---------------------------------------------------------------------------
 # large tiles: remainders in every direction, strides, beta
 # ---------------------------------------------------------------------------
