@@ -493,6 +493,7 @@ int sgemm_norm_grad(int T, int N, const float *h, int ldh, const float *weight, 
     a.part = dweight == nullptr ? nullptr : workspace;
     a.dweight = dweight;
     a.beta = beta;
+    a.stream = T * (int64_t)N >= (32 << 20);  // 128 MiB, half of the last-level cache
     const bool wide = dweight != nullptr && long_shares(T, N);
     a.P = weight_shares(T, N) * (dweight == nullptr && long_shares(T, N) ? 2 : 1);  // (dh alone: 512 workgroups too)
     const RowKernel<normk::NormGradArgs> *k = row_kernel(kNormGrads, N);

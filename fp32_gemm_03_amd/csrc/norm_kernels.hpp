@@ -369,6 +369,7 @@ struct NormGradArgs {
     float *dh, *dweight;
     void *part;  // P shares of dweight: float, in norm_grad_long_shares double
     float beta;
+    bool stream;  // dh is larger than the caches (norm_grad_long)
 };
 
 __device__ __forceinline__ float norm_back(float h, float dy, float w, float ds, double r, double c) {
@@ -433,7 +434,9 @@ template <int NT, int V> __global__ void __launch_bounds__(NT) norm_grad(NormGra
 }
 
 // Rows too long for registers: a row is read twice.  For dh, and for shares of dweight that
-// are one row each (P >= T).
+// are one row each (P >= T).  The stores of a large dh go past the caches, which leaves them to
+// the rows' second reading (dh alone, us; so, and not: 2000 x 40003 321, 341; 2048 x 65536 522, 573; 4096 x
+// 16384 228, 239; of a smaller dh no difference, and what reads it next finds it there).
 __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
     __shared__ double sums[2][kLongThreads / 64];
     float *part = a.part == nullptr ? nullptr : static_cast<float *>(a.part) + (int64_t)blockIdx.x * a.N;
@@ -466,7 +469,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_grad_long(NormGradArgs a) {
                 o[e] = norm_back(x[e], y[e], w[e], ds[e], r, k);
             }
             if (part != nullptr) rowk::store4(part + i, left, p);
-            if (a.dh != nullptr) rowk::store4(a.dh + t * a.lddh + i, left, o);
+            if (a.dh != nullptr) {
+                float *to = a.dh + t * a.lddh + i;
+                if (a.stream && left >= 4) __builtin_nontemporal_store(o, reinterpret_cast<f32x4u *>(to));
+                else rowk::store4(to, left, o);
+            }
         });
     }
 }

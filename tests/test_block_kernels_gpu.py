@@ -116,6 +116,30 @@ def test_norm_grad_of_many_long_rows(T, N):
                 first = got
 
 
+@pytest.mark.parametrize("T,N,weight", [(3700, 9101, False), (400, 90001, True)])
+def test_norm_grad_of_rows_larger_than_the_caches(T, N, weight):
+    """dh's stores go past the caches: the same numbers, and nothing behind a row is written."""
+    gu.say("norm_grad of large rows", T, N)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    h, dy, ds = (torch.randn(T, N, generator=gen, device="cuda") for _ in range(3))
+    w = torch.randn(N, generator=gen, device="cuda")
+    own, dw = torch.full((T, N + 1), 7.0, device="cuda"), torch.empty(N, device="cuda")
+    dh = own[:, :N]
+    space = torch.empty(g.sgemm_norm_grad_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    g.sgemm_norm_grad(T, N, h, N, w, 2.0 ** -12, dy, N, ds, N, dh, N + 1, 0.0, dw if weight else None, space)
+    assert bool((own[:, N] == 7.0).all())
+    g64, h64 = dy.double() * w.double(), h.double()
+    r = torch.rsqrt(h64.square().mean(1, keepdim=True) + 2.0 ** -12)
+    part = h64 * r * r
+    want = r * (g64 - part * (g64 * h64).mean(1, keepdim=True)) + ds.double()
+    size = r * (g64.abs() + part.abs() * (g64 * h64).abs().mean(1, keepdim=True)) + ds.abs()
+    # one rounding, and 2^-45 of the terms for what cancels in 64 bits
+    assert bool(((dh.double() - want).abs() <= ONCE * (want.abs() + 2.0 ** -21 * size)).all())
+    if weight:
+        terms = dy.double() * h64 * r
+        assert bool(((dw.double() - terms.sum(0)).abs() <= 2.02 * U24 * terms.abs().sum(0)).all())
+
+
 def test_norm_grad_of_long_rows_in_a_graph():
     """Captured on a stream of its own and replayed on other inputs, between eager calls."""
     T, N = 770, 8195
